@@ -12,7 +12,11 @@ Language Models" (WISE):
   support only (§5.2 Eqs 7-8);
 * :func:`discover_select` / :func:`select_finalize` -- the same discovery and
   selection with each window step's Eq 6 support taken in the discovery
-  launch itself (no mass tensors kept across the window, no selection pass).
+  launch itself (no mass tensors kept across the window, no selection pass);
+* :func:`cache_append`, :func:`tree_attention`, :func:`cache_accept` -- what
+  follows the prompt: a paged cache of keys and values, attention of a next
+  token or of a tree of drafted tokens over it, and the drafted tokens that
+  are kept.
 
 Torch tensors supply device memory and the stream; every computation runs in
 the library's CUDA kernels. There is no CPU path: without the compiled
@@ -20,6 +24,7 @@ library on a CUDA device these functions raise.
 """
 from __future__ import annotations
 
+import contextlib
 import dataclasses
 import math
 from typing import Optional, Sequence, Tuple
@@ -32,7 +37,8 @@ from ._lib import (WISE_BF16, WISE_F32, WISE_SUPPORT_DIAG, WISE_SUPPORT_SINK, Wi
 __all__ = ["discover", "select_support", "sparse", "Support", "device_status", "WiseError", "discover_select",
            "select_finalize", "new_select_state",
            "WISE_SUPPORT_SINK", "WISE_SUPPORT_DIAG", "useful_flops", "dense_flops", "retained_mass",
-           "support_jaccard", "select_control", "gather_plan"]
+           "support_jaccard", "select_control", "gather_plan", "PagedCache", "Rope", "rope_frequencies",
+           "pack_tree_mask", "cache_append", "tree_attention", "cache_accept"]
 
 _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
 
@@ -488,6 +494,222 @@ def support_jaccard(a: Support, b: Support, *, stream: Optional[torch.cuda.Strea
                                   row_counts.data_ptr(), counts.data_ptr(), jac.data_ptr(), _stream_handle(stream))
     _lib.check(st, "wise_support_jaccard")
     return row_counts, counts, jac
+
+
+# ---------------------------------------------------------------- paged cache
+
+@dataclasses.dataclass
+class PagedCache:
+    """Keys and values of a batch of sequences in pages of 16, 32, 64 or 128
+    tokens. Token t of sequence b lies in row t % page of page
+    page_table[b, t // page]; lengths[b] tokens are committed, and new
+    (drafted) tokens lie behind them. The pool and the table belong to the
+    caller, who hands pages to sequences."""
+    k_pages: torch.Tensor     # bf16 [n_pages, kv_heads, page, head_dim]
+    v_pages: torch.Tensor     # bf16 [n_pages, kv_heads, page, head_dim]
+    page_table: torch.Tensor  # int32 [batch, max_pages]
+    lengths: torch.Tensor     # int32 [batch]
+
+
+@dataclasses.dataclass
+class Rope:
+    """Position rotation of a head's first 2 * len(steps) values. steps[i] is
+    the rotation of pair i per position in units of 2^-64 turn (int64, modulo
+    2^64), so that the angle of any position is reduced exactly; build it with
+    :func:`rope_frequencies`. pairs: rotate neighbouring values instead of the
+    two halves."""
+    steps: torch.Tensor
+    pairs: bool = False
+
+
+def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, inv_freq: Optional[Sequence[float]] = None,
+                     pairs: bool = False, device="cuda") -> Rope:
+    """The Rope of `rotary_dim` values with frequencies base^(-2i / rotary_dim),
+    or with the rotary_dim / 2 frequencies `inv_freq` (radians per position)."""
+    if rotary_dim < 0 or rotary_dim % 16 != 0:
+        raise ValueError("rotary_dim must be a non-negative multiple of 16")
+    if inv_freq is None:
+        inv_freq = [base ** (-2.0 * i / rotary_dim) for i in range(rotary_dim // 2)]
+    freq = [float(f) for f in inv_freq]
+    if len(freq) != rotary_dim // 2 or not all(math.isfinite(f) for f in freq):
+        raise ValueError("inv_freq must hold rotary_dim / 2 finite frequencies")
+    steps = [int(round(f / (2.0 * math.pi) * 2.0 ** 64)) % (1 << 64) for f in freq]
+    steps = [x - (1 << 64) if x >> 63 else x for x in steps]
+    return Rope(torch.tensor(steps, dtype=torch.int64, device=device), pairs)
+
+
+def pack_tree_mask(mask: torch.Tensor) -> torch.Tensor:
+    """The packed mask of :func:`tree_attention` from a boolean one
+    [batch, n, n] (row i, column j: token i sees token j)."""
+    if mask.dtype != torch.bool or mask.dim() != 3 or mask.shape[1] != mask.shape[2]:
+        raise ValueError("mask must be a boolean [batch, n, n] tensor")
+    b, n, _ = mask.shape
+    words = (n + 31) // 32
+    bits = torch.nn.functional.pad(mask, (0, 32 * words - n)).reshape(b, n, words, 32).long()
+    packed = (bits << torch.arange(32, device=mask.device)).sum(-1)
+    return torch.where(packed >= 1 << 31, packed - (1 << 32), packed).to(torch.int32)
+
+
+def _check_array(name: str, t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], dev: int) -> int:
+    """Address of a dense array of exactly this type and shape on device `dev`."""
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
+    return t.data_ptr()
+
+
+def _check_cache(cache: PagedCache) -> Tuple[_lib.PagedCacheDesc, int]:
+    """The C descriptor of a cache and its device (the current one)."""
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    kp, table = cache.k_pages, cache.page_table
+    if not isinstance(kp, torch.Tensor) or kp.dim() != 4 or not isinstance(table, torch.Tensor) or table.dim() != 2:
+        raise ValueError("cache.k_pages must be [n_pages, kv_heads, page, head_dim] and cache.page_table [batch, max_pages]")
+    _check_device("cache.k_pages", kp)
+    dev = kp.get_device()
+    shape = tuple(kp.shape)
+    n_pages, hk, page, d = shape
+    b, max_pages = table.shape
+    return _lib.PagedCacheDesc(b, hk, d, page, max_pages, 0, n_pages,
+                               _check_array("cache.k_pages", kp, torch.bfloat16, shape, dev),
+                               _check_array("cache.v_pages", cache.v_pages, torch.bfloat16, shape, dev),
+                               _check_array("cache.page_table", table, torch.int32, (b, max_pages), dev),
+                               _check_array("cache.lengths", cache.lengths, torch.int32, (b,), dev)), dev
+
+
+def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d: int, dev: int) -> _lib.Rows:
+    """The C view of rows [batch, heads, n, d] (any strides of the first three axes)."""
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
+        raise ValueError(f"{name} must be a bfloat16 [batch, heads, tokens, head_dim] tensor")
+    if not t.is_cuda or t.get_device() != dev:
+        raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
+    shape, stride = t.shape, t.stride()
+    if shape[0] != batch or shape[3] != d or shape[2] < 1 or (heads is not None and shape[1] != heads):
+        raise ValueError(f"{name} of shape {tuple(shape)} does not fit the cache (batch {batch}, "
+                         + (f"{heads} heads, " if heads is not None else "") + f"head_dim {d})")
+    if stride[3] != 1:
+        raise ValueError(f"{name} must be contiguous in its last axis")
+    r = _lib.Rows(t.data_ptr())
+    for a in range(3):
+        r.stride[a] = stride[a] if shape[a] > 1 else 0
+    return r
+
+
+def _on_stream(stream: Optional[torch.cuda.Stream]):
+    """Buffers allocated for a call on another stream belong to that stream."""
+    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+
+
+def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
+                 q_out: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                 positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
+    """Write new tokens' keys and values [batch, kv_heads, n, head_dim] behind
+    the committed tokens, the keys rotated by `rope`; with q [batch, heads, n,
+    head_dim], return the rotated queries too (dense, or in q_out). Tokens
+    i < new_len[b] (default: all n) go to slots lengths[b] + i; their
+    positions are positions[b, i] (int32; default lengths[b] + i -- a drafted
+    token's is lengths[b] + its depth). k, v and q may have any strides that
+    are multiples of 8 with a contiguous last axis. `lengths` does not
+    change: see :func:`cache_accept`."""
+    desc, dev = _check_cache(cache)
+    lib = _lib.load()
+    b, hk, d = desc.batch, desc.kv_heads, desc.head_dim
+    kr, vr = _check_rows("k", k, b, hk, d, dev), _check_rows("v", v, b, hk, d, dev)
+    n = k.shape[2]
+    if v.shape[2] != n:
+        raise ValueError("k and v must hold the same number of tokens")
+    qr, heads, qo = None, 0, None
+    if q is not None:
+        qr = _check_rows("q", q, b, None, d, dev)
+        heads = q.shape[1]
+        if q.shape[2] != n:
+            raise ValueError("q and k must hold the same number of tokens")
+        if q_out is None:
+            with _on_stream(stream):
+                q_out = torch.empty((b, heads, n, d), dtype=torch.bfloat16, device=q.device)
+        qo = _check_array("q_out", q_out, torch.bfloat16, (b, heads, n, d), dev)
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
+    pos = None if positions is None else _check_array("positions", positions, torch.int32, (b, n), dev)
+    steps, rotary, flags = None, 0, 0
+    if rope is not None:
+        rotary = 2 * rope.steps.numel()
+        steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
+        flags = _lib.WISE_ROPE_PAIRS if rope.pairs else 0
+    st = lib.wise_cache_append(desc, n, kr, vr, heads, qr, qo, nl, pos, steps, rotary, flags, _stream_handle(stream))
+    _lib.check(st, "wise_cache_append")
+    return q_out
+
+
+def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torch.Tensor] = None,
+                   tree_mask: Optional[torch.Tensor] = None, want_lse: bool = True,
+                   out_dtype: torch.dtype = torch.bfloat16, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                   lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                   stream: Optional[torch.cuda.Stream] = None):
+    """Attention of new tokens q [batch, heads, n, head_dim] (1 <= n <= 128,
+    already appended with :func:`cache_append`) over a paged cache. Token
+    i < new_len[b] sees the lengths[b] committed tokens and the new tokens that
+    row i of tree_mask lists (int32 [batch, n, ceil(n / 32)], see
+    :func:`pack_tree_mask`; default: tokens 0 .. i, so n = 1 is a next token).
+    The cache may have fewer heads than q (grouped-query attention). Returns
+    (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None); rows that
+    see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf."""
+    desc, dev = _check_cache(cache)
+    lib = _lib.load()
+    b, d = desc.batch, desc.head_dim
+    qr = _check_rows("q", q, b, None, d, dev)
+    heads, n = q.shape[1], q.shape[2]
+    if heads % desc.kv_heads != 0:
+        raise ValueError("the cache's heads must divide q's heads")
+    if out_dtype not in _OUT:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
+    mask = None if tree_mask is None else _check_array("tree_mask", tree_mask, torch.int32, (b, n, (n + 31) // 32), dev)
+    nbytes = int(lib.wise_attn_tree_workspace(desc, heads, n))
+    with _on_stream(stream):
+        if out is None:
+            out = torch.empty((b, heads, n, d), dtype=out_dtype, device=q.device)
+        if want_lse and lse is None:
+            lse = torch.empty((b, heads, n), dtype=torch.float32, device=q.device)
+        if workspace is None:
+            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
+    o_ptr = _check_array("out", out, out_dtype, (b, heads, n, d), dev)
+    lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev) if want_lse else None
+    _check_bytes("workspace", workspace, nbytes, q.device)
+    st = lib.wise_attn_tree(desc, heads, n, qr, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr, workspace.data_ptr(),
+                            workspace.numel(), _stream_handle(stream))
+    _lib.check(st, "wise_attn_tree")
+    return out, (lse if want_lse else None)
+
+
+def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[torch.Tensor] = None, *,
+                 new_lengths: Optional[torch.Tensor] = None,
+                 stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Keep drafted tokens: the keys and values of new tokens path[b, i],
+    i < n_accepted[b] (int32; strictly ascending; the rest of a row is not
+    read), move to slots lengths[b] + i. Without a path the first n_accepted[b] new tokens are
+    kept where they are. Returns the new lengths (int32 [batch], not
+    cache.lengths itself: assign them, or copy them in place)."""
+    desc, dev = _check_cache(cache)
+    lib = _lib.load()
+    b = desc.batch
+    na = _check_array("n_accepted", n_accepted, torch.int32, (b,), dev)
+    tokens, path_ptr = desc.max_pages * desc.page, None
+    if path is not None:
+        if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[1] < 1:
+            raise ValueError("path must be an int32 [batch, path_tokens] tensor")
+        tokens = path.shape[1]
+        path_ptr = _check_array("path", path, torch.int32, (b, tokens), dev)
+    if new_lengths is None:
+        with _on_stream(stream):
+            new_lengths = torch.empty(b, dtype=torch.int32, device=cache.lengths.device)
+    out = _check_array("new_lengths", new_lengths, torch.int32, (b,), dev)
+    st = lib.wise_cache_accept(desc, tokens, path_ptr, na, out, _stream_handle(stream))
+    _lib.check(st, "wise_cache_accept")
+    return new_lengths
 
 
 def device_status(stream: Optional[torch.cuda.Stream] = None) -> int:

@@ -20,6 +20,7 @@ WISE_ERR_WORKSPACE = 4
 WISE_ERR_BAD_SUPPORT = 5
 WISE_ERR_CUDA = 6
 WISE_ERR_DEVICE_TIMEOUT = 7
+WISE_ERR_BAD_CACHE = 8
 
 WISE_BF16 = 0
 WISE_F32 = 1
@@ -27,6 +28,7 @@ WISE_SUPPORT_SINK = 1
 WISE_SUPPORT_DIAG = 2
 WISE_CONTROL_MASS_MATCHED = 1
 WISE_CONTROL_SIZE_MATCHED = 2
+WISE_ROPE_PAIRS = 1
 
 # Every symbol include/wise.h declares.
 EXPORTS = (
@@ -35,7 +37,8 @@ EXPORTS = (
     "wise_attn_sparse", "wise_validate_support", "wise_device_status", "wise_select_support_noalloc",
     "wise_support_retained_mass", "wise_support_jaccard", "wise_select_control", "wise_attn_discover_select",
     "wise_select_finalize", "wise_validate_schedule", "wise_wait_expiry_check", "wise_gather_plan_bytes",
-    "wise_gather_plan", "wise_attn_sparse_planned",
+    "wise_gather_plan", "wise_attn_sparse_planned", "wise_cache_append", "wise_attn_tree_workspace",
+    "wise_attn_tree", "wise_cache_accept",
 )
 
 
@@ -58,6 +61,28 @@ class AttnDesc(ctypes.Structure):
     ]
 
 
+class PagedCacheDesc(ctypes.Structure):
+    """wise_paged_cache"""
+    _fields_ = [
+        ("batch", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("page", ctypes.c_int32),
+        ("max_pages", ctypes.c_int32),
+        ("reserved", ctypes.c_int32),
+        ("n_pages", ctypes.c_int64),
+        ("k_pages", ctypes.c_void_p),
+        ("v_pages", ctypes.c_void_p),
+        ("page_table", ctypes.c_void_p),
+        ("lengths", ctypes.c_void_p),
+    ]
+
+
+class Rows(ctypes.Structure):
+    """wise_rows"""
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
+
+
 _lock = threading.Lock()
 _handle = None
 
@@ -67,6 +92,8 @@ _i32 = ctypes.c_int32
 _i64 = ctypes.c_int64
 _u32 = ctypes.c_uint32
 _dp = ctypes.POINTER(AttnDesc)
+_cp = ctypes.POINTER(PagedCacheDesc)
+_rp = ctypes.POINTER(Rows)
 
 _SIGNATURES = {
     "wise_abi_version": (ctypes.c_int, []),
@@ -93,6 +120,10 @@ _SIGNATURES = {
     "wise_gather_plan_bytes": (ctypes.c_size_t, [_dp]),
     "wise_gather_plan": (ctypes.c_int, [_dp, _vp, _vp, _i64, _vp, ctypes.c_size_t, _vp]),
     "wise_attn_sparse_planned": (ctypes.c_int, [_dp, _vp, _vp, _vp, _vp, _vp, _i64, _vp, _vp, _vp, _vp, _vp]),
+    "wise_cache_append": (ctypes.c_int, [_cp, _i32, _rp, _rp, _i32, _rp, _vp, _vp, _vp, _vp, _i32, _u32, _vp]),
+    "wise_attn_tree_workspace": (_sz, [_cp, _i32, _i32]),
+    "wise_attn_tree": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _sz, _vp]),
+    "wise_cache_accept": (ctypes.c_int, [_cp, _i32, _vp, _vp, _vp, _vp]),
     "wise_wait_expiry_check": (ctypes.c_int, [_vp]),
     "wise_device_status": (ctypes.c_int, [_vp]),
 }

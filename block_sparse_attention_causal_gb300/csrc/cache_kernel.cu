@@ -1,0 +1,207 @@
+// Maintenance of a paged key/value cache: new tokens' keys and values appended
+// with the position rotation applied on the way, and the drafted tokens that
+// are kept moved up behind the committed ones. (No counterpart in the WISE
+// paper: a served model's cache behind its prompt.)
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace wise {
+namespace {
+
+// Element offset in a pool of the row that holds token `slot` of sequence b
+// (head 0), or -1 (flagged) when the token does not fit the page table or its
+// page is not in the pool.
+__device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_t slot, int d, uint32_t* err) {
+  const int64_t col = slot >> c.page_shift;
+  if (slot < 0 || col >= c.max_pages) {
+    atomicOr(err, kErrBadCache);
+    return -1;
+  }
+  const int32_t pg = __ldg(c.page_table + (int64_t)b * c.max_pages + col);
+  if (pg < 0 || (int64_t)pg >= c.n_pages) {
+    atomicOr(err, kErrBadCache);
+    return -1;
+  }
+  const int64_t row = slot & ((1 << c.page_shift) - 1);
+  return ((((int64_t)pg * c.kv_heads) << c.page_shift) + row) * d;
+}
+
+// The two 16-byte chunks of a head that one thread rotates together.
+struct ChunkPair {
+  uint4 a, b;
+};
+
+// (x, y) -> (x c - y s, y c + x s) in fp32, rounded once to bf16. HALVES: x and
+// y are the same places of the two chunks (halves rotation); else neighbouring
+// values of one chunk, four pairs per chunk.
+template <bool PAIRS>
+__device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const float (&s)[8]) {
+  uint32_t* a = &p.a.x;
+  uint32_t* b = &p.b.x;
+  auto lo = [](uint32_t w) { return __uint_as_float(w << 16); };
+  auto hi = [](uint32_t w) { return __uint_as_float(w & 0xffff0000u); };
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if (PAIRS) {
+      const float x0 = lo(a[i]), y0 = hi(a[i]), x1 = lo(b[i]), y1 = hi(b[i]);
+      a[i] = pack_bf16x2(x0 * c[i] - y0 * s[i], y0 * c[i] + x0 * s[i]);
+      b[i] = pack_bf16x2(x1 * c[4 + i] - y1 * s[4 + i], y1 * c[4 + i] + x1 * s[4 + i]);
+    } else {
+      const int f = 2 * i;
+      const float x0 = lo(a[i]), y0 = lo(b[i]), x1 = hi(a[i]), y1 = hi(b[i]);
+      a[i] = pack_bf16x2(x0 * c[f] - y0 * s[f], x1 * c[f + 1] - y1 * s[f + 1]);
+      b[i] = pack_bf16x2(y0 * c[f] + x0 * s[f], y1 * c[f + 1] + x1 * s[f + 1]);
+    }
+  }
+}
+
+// One thread per (token, pair of chunks), walking the heads of q, k and v of
+// its token: the sines and cosines of its eight frequencies are computed once
+// per token. With few tokens the heads are spread over gridDim.y.
+template <int D, bool PAIRS>
+__global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
+  constexpr int NP = D / 16;  // chunk pairs of a head
+  const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  const int64_t tok = item / NP;
+  if (tok >= (int64_t)p.cache.batch * p.n) return;
+  const int c = (int)(item % NP);
+  const int b = (int)(tok / p.n), i = (int)(tok % p.n);
+  const int units = p.heads + 2 * p.cache.kv_heads;
+  // element offsets of the thread's two chunks within a head: halves rotation
+  // pairs chunk c with chunk c + rotary_dim / 16; everything else takes
+  // neighbouring chunks
+  const int nrot = p.rotary_dim / 16;
+  const bool rot = c < nrot;
+  const int ca = (rot && !PAIRS) ? c * 8 : 2 * c * 8;
+  const int cb = (rot && !PAIRS) ? (c + nrot) * 8 : ca + 8;
+  const int32_t len = __ldg(p.cache.lengths + b);
+  const int32_t nl = p.new_len ? __ldg(p.new_len + b) : p.n;
+  if (len < 0 || nl < 0 || nl > p.n) atomicOr(p.err, kErrBadCache);
+  const bool store = len >= 0 && i < nl;
+  const int64_t dst = store ? slot_offset(p.cache, b, (int64_t)len + i, D, p.err) : -1;
+  const int64_t head_step = (int64_t)D << p.cache.page_shift;
+  float cs[8], sn[8];
+  if (rot) {
+    const int64_t pos = p.positions ? (int64_t)__ldg(p.positions + tok) : (int64_t)len + i;
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      // the angle in turns modulo one, exact: the low 64 bits of the product
+      const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(p.rope + 8 * c + f);
+      const float x = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in units of pi, [-1, 1]
+      sincospif(x, &sn[f], &cs[f]);
+    }
+  }
+  const uint16_t* kb = p.k.data + (int64_t)b * p.k.sb + (int64_t)i * p.k.sn;
+  const uint16_t* vb = p.v.data + (int64_t)b * p.v.sb + (int64_t)i * p.v.sn;
+  for (int u = blockIdx.y; u < units; u += gridDim.y) {
+    const uint16_t* src;
+    uint16_t* out;
+    bool turn = rot;
+    if (u < p.heads) {
+      src = p.q.data + (int64_t)b * p.q.sb + (int64_t)u * p.q.sh + (int64_t)i * p.q.sn;
+      out = p.q_out + (((int64_t)b * p.heads + u) * p.n + i) * D;
+    } else {
+      if (dst < 0) break;
+      const int h = u - p.heads;
+      if (h < p.cache.kv_heads) {
+        src = kb + (int64_t)h * p.k.sh;
+        out = p.cache.k_pages + dst + h * head_step;
+      } else {
+        src = vb + (int64_t)(h - p.cache.kv_heads) * p.v.sh;
+        out = p.cache.v_pages + dst + (h - p.cache.kv_heads) * head_step;
+        turn = false;
+      }
+    }
+    ChunkPair x;
+    x.a = __ldg(reinterpret_cast<const uint4*>(src + ca));
+    x.b = __ldg(reinterpret_cast<const uint4*>(src + cb));
+    if (turn) rotate<PAIRS>(x, cs, sn);
+    *reinterpret_cast<uint4*>(out + ca) = x.a;
+    *reinterpret_cast<uint4*>(out + cb) = x.b;
+  }
+}
+
+// One thread per (sequence, pool, head, 16-byte chunk), walking the accepted
+// path in order. The path ascends strictly, so entry i >= i: a batch's loads
+// all come before its stores, and the stores of earlier entries (slots below
+// i) are never a later entry's source.
+__global__ void __launch_bounds__(128) accept_kernel(const AcceptLaunch p) {
+  constexpr int BATCH = 8;
+  const int chunks = p.head_dim / 8;
+  const int per_seq = 2 * p.cache.kv_heads * chunks;
+  const int b = blockIdx.y;
+  const int x = blockIdx.x * blockDim.x + threadIdx.x;
+  const int32_t len = __ldg(p.cache.lengths + b);
+  int32_t na = __ldg(p.n_accepted + b);
+  const int64_t room = ((int64_t)p.cache.max_pages << p.cache.page_shift) - len;
+  if (len < 0 || na < 0 || na > p.path_tokens || na > room) {
+    if (x == 0) atomicOr(p.err, kErrBadCache);
+    na = len < 0 ? 0 : max(0, (int32_t)min((int64_t)min(na, p.path_tokens), max(room, (int64_t)0)));
+  }
+  if (x == 0) p.new_lengths[b] = len + na;
+  if (p.path == nullptr || x >= per_seq || len < 0) return;
+  const int chunk = x % chunks, hp = x / chunks;
+  const int h = hp % p.cache.kv_heads;
+  uint16_t* pool = (hp < p.cache.kv_heads ? p.cache.k_pages : p.cache.v_pages) +
+                   (((int64_t)h * p.head_dim) << p.cache.page_shift) + chunk * 8;
+  const int32_t* path = p.path + (int64_t)b * p.path_tokens;
+  int32_t prev = -1;
+  for (int i0 = 0; i0 < na; i0 += BATCH) {
+    uint4 v[BATCH];
+    int64_t to[BATCH];
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k) {
+      to[k] = -1;
+      const int i = i0 + k;
+      if (i >= na) continue;
+      const int32_t src = __ldg(path + i);
+      if (src <= prev || src < i) {
+        atomicOr(p.err, kErrBadCache);
+        continue;
+      }
+      prev = src;
+      if (src == i) continue;  // already in its place
+      const int64_t from = slot_offset(p.cache, b, (int64_t)len + src, p.head_dim, p.err);
+      if (from < 0) continue;
+      v[k] = *reinterpret_cast<const uint4*>(pool + from);
+      to[k] = slot_offset(p.cache, b, (int64_t)len + i, p.head_dim, p.err);
+    }
+#pragma unroll
+    for (int k = 0; k < BATCH; ++k)
+      if (to[k] >= 0) *reinterpret_cast<uint4*>(pool + to[k]) = v[k];
+  }
+}
+
+template <int D>
+cudaError_t launch_append_d(const AppendLaunch& a, cudaStream_t stream) {
+  const int64_t items = (int64_t)a.cache.batch * a.n * (D / 16);
+  const int units = a.heads + 2 * a.cache.kv_heads;
+  const int64_t blocks = (items + 255) / 256;
+  // heads are spread until the grid holds about a full GPU of threads
+  constexpr int64_t kFull = 152 * 8;
+  int64_t ny = kFull / blocks;
+  ny = ny < 1 ? 1 : (ny > units ? units : ny);
+  const dim3 grid((unsigned)blocks, (unsigned)ny);
+  if (a.pairs) append_kernel<D, true><<<grid, 256, 0, stream>>>(a);
+  else append_kernel<D, false><<<grid, 256, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_cache_append(const AppendLaunch& a, cudaStream_t stream) {
+  switch (a.head_dim) {
+    case 64: return launch_append_d<64>(a, stream);
+    case 96: return launch_append_d<96>(a, stream);
+    default: return launch_append_d<128>(a, stream);
+  }
+}
+
+cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream) {
+  const int per_seq = 2 * a.cache.kv_heads * (a.head_dim / 8);
+  const dim3 grid((unsigned)((per_seq + 127) / 128), (unsigned)a.cache.batch);
+  accept_kernel<<<grid, 128, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace wise

@@ -131,4 +131,63 @@ struct DiagLaunch {
 cudaError_t launch_retained_mass(const DiagLaunch& d, cudaStream_t stream);
 cudaError_t launch_jaccard(const DiagLaunch& d, cudaStream_t stream);
 
+// A paged cache as the kernels see it (wise_paged_cache).
+struct CacheView {
+  int32_t batch, kv_heads, page_shift, max_pages;
+  int64_t n_pages;
+  uint16_t* k_pages;
+  uint16_t* v_pages;
+  const int32_t* page_table;
+  const int32_t* lengths;
+};
+// Rows [batch, heads, n, d] with strides in elements (wise_rows).
+struct RowsView {
+  const uint16_t* data;
+  int64_t sb, sh, sn;
+};
+
+// Cache maintenance (cache_kernel.cu).
+struct AppendLaunch {
+  CacheView cache;
+  int32_t head_dim, n;
+  RowsView k, v, q;
+  int32_t heads;  // query heads; 0 without q
+  uint16_t* q_out;
+  const int32_t* new_len;
+  const int32_t* positions;
+  const int64_t* rope;
+  int32_t rotary_dim;
+  int32_t pairs;  // rotate neighbouring values instead of halves
+  uint32_t* err;
+};
+cudaError_t launch_cache_append(const AppendLaunch& a, cudaStream_t stream);
+
+struct AcceptLaunch {
+  CacheView cache;
+  int32_t head_dim, path_tokens;
+  const int32_t* path;
+  const int32_t* n_accepted;
+  int32_t* new_lengths;
+  uint32_t* err;
+};
+cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream);
+
+// Attention of new tokens over a paged cache (tree_kernel.cu).
+constexpr int kTreeMaxTokens = 128;
+struct TreeLaunch {
+  CacheView cache;
+  int32_t head_dim, heads, n;
+  RowsView q;
+  const int32_t* new_len;
+  const int32_t* tree_mask;
+  float scale;
+  int32_t out_f32;
+  void* o;
+  float* lse;
+  void* workspace;
+  uint32_t* err;
+};
+int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim);
+cudaError_t launch_tree(const TreeLaunch& t, cudaStream_t stream);
+
 }  // namespace wise

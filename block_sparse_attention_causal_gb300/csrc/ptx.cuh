@@ -8,7 +8,7 @@
 namespace wise {
 
 // Bits of the device error word.
-enum : uint32_t { kErrBadSupport = 1u, kErrTimeout = 2u, kErrInternal = 4u };
+enum : uint32_t { kErrBadSupport = 1u, kErrTimeout = 2u, kErrInternal = 4u, kErrBadCache = 8u };
 
 // Every mbarrier wait in this library gives up after this long and reports
 // WISE_ERR_DEVICE_TIMEOUT instead of hanging the GPU.

@@ -239,6 +239,63 @@ uint8_t* select_scratch() {
   return g_scratch_ptr[dev];
 }
 
+// ------------------------------------------------------------- paged cache
+
+constexpr int64_t kMaxCacheTokens = 1ll << 30;  // per sequence
+
+// The shape of a cache; with `pointers`, its buffers too.
+int check_cache(const wise_paged_cache* c, bool pointers) {
+  if (!c) return WISE_ERR_INVALID_ARGUMENT;
+  if (c->batch < 1 || c->kv_heads < 1 || c->max_pages < 1 || c->n_pages < 1) return WISE_ERR_INVALID_ARGUMENT;
+  if (c->head_dim != 64 && c->head_dim != 96 && c->head_dim != 128) return WISE_ERR_UNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return WISE_ERR_UNSUPPORTED;
+  if (c->batch > 65535 || (int64_t)c->max_pages * c->page > kMaxCacheTokens || c->n_pages > INT32_MAX ||
+      (int64_t)c->kv_heads * c->page > INT32_MAX)
+    return WISE_ERR_UNSUPPORTED;
+  if (!pointers) return WISE_OK;
+  if (!c->k_pages || !c->v_pages || !c->page_table || !c->lengths) return WISE_ERR_INVALID_ARGUMENT;
+  if (!aligned16(c->k_pages) || !aligned16(c->v_pages) || (reinterpret_cast<uintptr_t>(c->page_table) & 3u) ||
+      (reinterpret_cast<uintptr_t>(c->lengths) & 3u))
+    return WISE_ERR_ALIGNMENT;
+  return WISE_OK;
+}
+
+int check_rows(const wise_rows* r) {
+  if (!r || !r->data) return WISE_ERR_INVALID_ARGUMENT;
+  for (int64_t s : r->stride) {
+    if (s < 0) return WISE_ERR_INVALID_ARGUMENT;
+    if (s % 8 != 0) return WISE_ERR_ALIGNMENT;  // 16-byte loads
+  }
+  return aligned16(r->data) ? WISE_OK : WISE_ERR_ALIGNMENT;
+}
+
+bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
+
+CacheView cache_view(const wise_paged_cache* c) {
+  CacheView v;
+  v.batch = c->batch;
+  v.kv_heads = c->kv_heads;
+  v.page_shift = c->page == 16 ? 4 : c->page == 32 ? 5 : c->page == 64 ? 6 : 7;
+  v.max_pages = c->max_pages;
+  v.n_pages = c->n_pages;
+  v.k_pages = static_cast<uint16_t*>(c->k_pages);
+  v.v_pages = static_cast<uint16_t*>(c->v_pages);
+  v.page_table = c->page_table;
+  v.lengths = c->lengths;
+  return v;
+}
+
+RowsView rows_view(const wise_rows* r) {
+  return RowsView{static_cast<const uint16_t*>(r->data), r->stride[0], r->stride[1], r->stride[2]};
+}
+
+int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
+  if (heads < 1 || heads % c->kv_heads != 0 || new_tokens < 1) return WISE_ERR_INVALID_ARGUMENT;
+  if (new_tokens > kTreeMaxTokens) return WISE_ERR_UNSUPPORTED;
+  if ((int64_t)c->batch * heads * new_tokens > INT32_MAX / 2) return WISE_ERR_UNSUPPORTED;
+  return WISE_OK;
+}
+
 // Self-check of the bounded wait: one thread waits on an mbarrier that
 // nothing arrives on, through the same wait routine as the attention kernels
 // but with a 20 ms limit. The wait expires, kErrTimeout is recorded, and the
@@ -273,6 +330,7 @@ const char* wise_status_str(int status) {
     case WISE_ERR_BAD_SUPPORT: return "malformed support (CSR) or schedule";
     case WISE_ERR_CUDA: return "CUDA error";
     case WISE_ERR_DEVICE_TIMEOUT: return "device wait timed out";
+    case WISE_ERR_BAD_CACHE: return "invalid entries in a paged cache or an accepted path";
     default: return "unknown status";
   }
 }
@@ -652,6 +710,104 @@ int wise_select_control(const wise_attn_desc* desc, const float* block_mass, int
   return e == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
 }
 
+int wise_cache_append(const wise_paged_cache* cache, int32_t new_tokens, const wise_rows* k, const wise_rows* v,
+                      int32_t heads, const wise_rows* q, void* q_out, const int32_t* new_len,
+                      const int32_t* positions, const int64_t* rope, int32_t rotary_dim, uint32_t flags,
+                      wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if (new_tokens < 1 || (q && (heads < 1 || !q_out)) || (flags & ~WISE_ROPE_PAIRS)) return WISE_ERR_INVALID_ARGUMENT;
+  if (rotary_dim < 0 || rotary_dim > cache->head_dim || rotary_dim % 16 != 0) return WISE_ERR_INVALID_ARGUMENT;
+  if (rotary_dim > 0 && !rope) return WISE_ERR_INVALID_ARGUMENT;
+  if (new_tokens > kMaxCacheTokens || (int64_t)cache->batch * new_tokens > INT32_MAX ||
+      2 * (int64_t)cache->kv_heads + (q ? heads : 0) > INT32_MAX)
+    return WISE_ERR_UNSUPPORTED;
+  if ((st = check_rows(k)) != WISE_OK || (st = check_rows(v)) != WISE_OK) return st;
+  if (q && (st = check_rows(q)) != WISE_OK) return st;
+  if ((q && !aligned16(q_out)) || misaligned4(new_len) || misaligned4(positions) ||
+      (reinterpret_cast<uintptr_t>(rope) & 7u))
+    return WISE_ERR_ALIGNMENT;
+  AppendLaunch a;
+  memset(&a, 0, sizeof(a));
+  a.err = error_word();
+  if (!a.err) return WISE_ERR_CUDA;
+  a.cache = cache_view(cache);
+  a.head_dim = cache->head_dim;
+  a.n = new_tokens;
+  a.k = rows_view(k);
+  a.v = rows_view(v);
+  if (q) {
+    a.q = rows_view(q);
+    a.heads = heads;
+    a.q_out = static_cast<uint16_t*>(q_out);
+  }
+  a.new_len = new_len;
+  a.positions = positions;
+  a.rope = rope;
+  a.rotary_dim = rotary_dim;
+  a.pairs = (flags & WISE_ROPE_PAIRS) != 0;
+  return launch_cache_append(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens) {
+  if (check_cache(cache, false) != WISE_OK || check_tree(cache, heads, new_tokens) != WISE_OK) return 0;
+  return (size_t)tree_workspace_bytes(cache->batch, cache->kv_heads, heads, new_tokens, cache->head_dim);
+}
+
+int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q,
+                   const int32_t* new_len, const int32_t* tree_mask, float scale, int32_t out_dtype, void* o,
+                   float* lse, void* workspace, size_t workspace_bytes, wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if ((st = check_tree(cache, heads, new_tokens)) != WISE_OK) return st;
+  if (!o || (out_dtype != WISE_BF16 && out_dtype != WISE_F32) || !(scale >= 0.f) || isinf(scale))
+    return WISE_ERR_INVALID_ARGUMENT;
+  if ((st = check_rows(q)) != WISE_OK) return st;
+  if (!aligned16(o) || misaligned4(lse) || misaligned4(new_len) || misaligned4(tree_mask)) return WISE_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < wise_attn_tree_workspace(cache, heads, new_tokens)) return WISE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WISE_ERR_ALIGNMENT;
+  TreeLaunch t;
+  memset(&t, 0, sizeof(t));
+  t.err = error_word();
+  if (!t.err) return WISE_ERR_CUDA;
+  t.cache = cache_view(cache);
+  t.head_dim = cache->head_dim;
+  t.heads = heads;
+  t.n = new_tokens;
+  t.q = rows_view(q);
+  t.new_len = new_len;
+  t.tree_mask = tree_mask;
+  t.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)cache->head_dim);
+  t.out_f32 = out_dtype == WISE_F32;
+  t.o = o;
+  t.lse = lse;
+  t.workspace = workspace;
+  return launch_tree(t, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,
+                      const int32_t* n_accepted, int32_t* new_lengths, wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if (!n_accepted || !new_lengths || path_tokens < 1 || path_tokens > kMaxCacheTokens) return WISE_ERR_INVALID_ARGUMENT;
+  if (misaligned4(path) || misaligned4(n_accepted) || misaligned4(new_lengths)) return WISE_ERR_ALIGNMENT;
+  // a block may read lengths[b] after another has written new_lengths[b]
+  const uintptr_t a0 = reinterpret_cast<uintptr_t>(cache->lengths), a1 = reinterpret_cast<uintptr_t>(new_lengths);
+  const uintptr_t span = (uintptr_t)cache->batch * 4;
+  if (a0 < a1 + span && a1 < a0 + span) return WISE_ERR_INVALID_ARGUMENT;
+  AcceptLaunch a;
+  memset(&a, 0, sizeof(a));
+  a.err = error_word();
+  if (!a.err) return WISE_ERR_CUDA;
+  a.cache = cache_view(cache);
+  a.head_dim = cache->head_dim;
+  a.path_tokens = path_tokens;
+  a.path = path;
+  a.n_accepted = n_accepted;
+  a.new_lengths = new_lengths;
+  return launch_cache_accept(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
 int wise_validate_support(const wise_attn_desc* desc, const int32_t* row_ptr, const int32_t* col_idx,
                           uint32_t flags) {
   int st = check_desc(desc);
@@ -707,6 +863,7 @@ int wise_device_status(wise_stream_t stream) {
   if (word & kErrTimeout) return WISE_ERR_DEVICE_TIMEOUT;
   if (word & kErrInternal) return WISE_ERR_CUDA;
   if (word & kErrBadSupport) return WISE_ERR_BAD_SUPPORT;
+  if (word & kErrBadCache) return WISE_ERR_BAD_CACHE;
   return WISE_OK;
 }
 

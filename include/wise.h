@@ -23,6 +23,18 @@
  *                        future attention mass") and Appendix C.2 Eq 24
  *                        (rolling working-set Jaccard stability).
  *
+ * Behind the prompt, a served model works from a cache:
+ *
+ *   wise_cache_append    keys and values of new tokens into a paged cache,
+ *                        the position rotation of keys and queries applied
+ *                        on the way;
+ *   wise_attn_tree       §3 Eq 2 for new tokens over that cache: a single
+ *                        next token, a run of tokens, or a tree of drafted
+ *                        tokens each of which sees the cache and its own
+ *                        ancestors;
+ *   wise_cache_accept    the drafted tokens that are kept become the cache's
+ *                        own.
+ *
  * Conventions shared by every call
  * --------------------------------
  * - Tensors are dense, row-major, in device memory owned by the caller:
@@ -55,7 +67,7 @@
  *   One graph must not be replayed on two streams at once.
  * - Argument, shape and alignment errors are reported before any launch and
  *   nothing is written. A failed launch returns WISE_ERR_CUDA. Kernel-side
- *   problems (a malformed support list, a wait that timed out) are recorded in
+ *   problems (a malformed support list or page table, a wait that timed out) are recorded in
  *   the device error word and read back with wise_device_status().
  */
 #ifndef WISE_H_
@@ -68,7 +80,7 @@
 extern "C" {
 #endif
 
-#define WISE_ABI_VERSION 5
+#define WISE_ABI_VERSION 6
 
 typedef struct CUstream_st* wise_stream_t; /* same type as cudaStream_t */
 
@@ -80,7 +92,9 @@ typedef enum wise_status {
   WISE_ERR_WORKSPACE = 4,        /* workspace missing or too small           */
   WISE_ERR_BAD_SUPPORT = 5,      /* support CSR malformed / over capacity    */
   WISE_ERR_CUDA = 6,             /* CUDA runtime or driver error             */
-  WISE_ERR_DEVICE_TIMEOUT = 7    /* a kernel wait exceeded its time limit    */
+  WISE_ERR_DEVICE_TIMEOUT = 7,   /* a kernel wait exceeded its time limit    */
+  WISE_ERR_BAD_CACHE = 8         /* a paged cache's lengths, page table or   */
+                                 /* accepted path hold invalid entries       */
 } wise_status;
 
 typedef enum wise_dtype { WISE_BF16 = 0, WISE_F32 = 1 } wise_dtype;
@@ -379,6 +393,137 @@ int wise_support_jaccard(const wise_attn_desc* desc, const int32_t* row_ptr_a, c
                          int64_t col_capacity_b, int32_t* row_counts, int64_t* batch_counts, double* batch_jaccard,
                          wise_stream_t stream);
 
+/*
+ * A paged key/value cache (all pointers in device memory, owned by the
+ * caller; no counterpart in the paper). Pools of pages hold `page` consecutive
+ * tokens of one sequence for every key/value head:
+ *   k_pages, v_pages : [n_pages, kv_heads, page, head_dim] bf16, dense;
+ *   page_table       : [batch, max_pages] int32: token t of sequence b lies in
+ *                      row t % page of page page_table[b][t / page]. Entries
+ *                      past a sequence's last token are never read. Sequences
+ *                      may share pages that no call writes;
+ *   lengths          : [batch] int32: the committed tokens of each sequence.
+ * New (drafted) tokens lie behind the committed ones: new token i of sequence
+ * b is token lengths[b] + i. No call changes `lengths`.
+ * head_dim in {64, 96, 128}; page in {16, 32, 64, 128};
+ * batch <= 65535; max_pages * page <= 2^30.
+ */
+typedef struct wise_paged_cache {
+  int32_t batch;
+  int32_t kv_heads;
+  int32_t head_dim;
+  int32_t page;
+  int32_t max_pages;
+  int32_t reserved; /* 0 */
+  int64_t n_pages;
+  void* k_pages;
+  void* v_pages;
+  const int32_t* page_table;
+  const int32_t* lengths;
+} wise_paged_cache;
+
+/* Rows [batch, heads, new_tokens, head_dim] of bf16 with strides (in
+ * elements, non-negative multiples of 8) of the first three axes; the last
+ * axis is contiguous and data is 16-byte aligned. */
+typedef struct wise_rows {
+  const void* data;
+  int64_t stride[3];
+} wise_rows;
+
+/* Position rotation of neighbouring values (x[2i], x[2i + 1]) instead of the
+ * two halves (x[i], x[i + rotary_dim / 2]). */
+#define WISE_ROPE_PAIRS 1u
+
+/*
+ * wise_cache_append -- writes the keys and values of new tokens behind the
+ * committed ones, keys (and, with q, queries) rotated by their positions:
+ * for each pair (x, y) i < rotary_dim / 2 of a head's first rotary_dim values
+ *     (x, y) -> (x cos a - y sin a, y cos a + x sin a),
+ *     a = 2 pi frac(position * rope[i] / 2^64).
+ * The angle is reduced in whole numbers, so it is exact to fp32 rounding at
+ * any position. The products are taken in fp32 and rounded once to bf16.
+ *   new_tokens : n, rows per sequence. n >= 1.
+ *   k, v       : [batch, kv_heads, n, head_dim].
+ *   heads, q, q_out : query heads and rows [batch, heads, n, head_dim]; q_out
+ *                dense, 16-byte aligned, not overlapping q. Every row of q is
+ *                rotated. q NULL: heads and q_out are ignored.
+ *   new_len    : [batch] int32 or NULL (n each): tokens i < new_len[b] are
+ *                written; no other slot of the cache changes.
+ *   positions  : [batch, n] int32 or NULL: lengths[b] + i.
+ *   rope       : [rotary_dim / 2] int64: turns per position in units of
+ *                2^-64 (modulo 2^64). May be NULL when rotary_dim is 0.
+ *   rotary_dim : multiple of 16, 0 <= rotary_dim <= head_dim; later values
+ *                are copied.
+ *   flags      : WISE_ROPE_PAIRS or 0.
+ * Two tokens of one call must not fall on one slot (sequences that are
+ * appended to own their last page). Tokens that do not fit the page table, or
+ * whose page is not in [0, n_pages), are skipped and flagged
+ * (WISE_ERR_BAD_CACHE in the device word), as are negative lengths and
+ * new_len outside 0 .. n. One launch.
+ */
+int wise_cache_append(const wise_paged_cache* cache, int32_t new_tokens, const wise_rows* k, const wise_rows* v,
+                      int32_t heads, const wise_rows* q, void* q_out, const int32_t* new_len,
+                      const int32_t* positions, const int64_t* rope, int32_t rotary_dim, uint32_t flags,
+                      wise_stream_t stream);
+
+/* Bytes of workspace wise_attn_tree needs for `heads` query heads and
+ * new_tokens rows per sequence; 0 when the arguments are invalid. Reads no
+ * device memory (cache pointers may be NULL). */
+size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens);
+
+/*
+ * wise_attn_tree -- attention (§3 Eq 2) of new tokens over a paged cache.
+ * Row i < new_len[b] of sequence b sees every committed token t < lengths[b]
+ * and the new tokens j < new_len[b] that its mask row lists:
+ *     O = softmax(q K^T * scale) V over the seen tokens, LSE its natural log
+ *     sum.
+ * A row that sees nothing (an empty mask row behind an empty cache, or
+ * i >= new_len[b]) gets O = 0 and LSE = -inf. Values of tokens that a row does
+ * not see have no influence on it, whatever they are (infinities, NaN).
+ *   heads      : query heads, a multiple of kv_heads; query head h reads
+ *                key/value head h / (heads / kv_heads).
+ *   new_tokens : n, 1 <= n <= 128 rows per sequence.
+ *   q          : [batch, heads, n, head_dim], rotated as the keys are.
+ *   new_len    : [batch] int32 or NULL (n each).
+ *   tree_mask  : [batch, n, ceil(n / 32)] int32 or NULL: bit j % 32 of word
+ *                j / 32 of row i says that token i sees token j (itself
+ *                included); bits j >= new_len[b] are ignored. NULL: token i
+ *                sees tokens j <= i (one next token; a run of tokens).
+ *   scale      : 0 => 1/sqrt(head_dim).
+ *   out_dtype  : WISE_BF16 or WISE_F32.
+ *   o, lse     : [batch, heads, n, head_dim] dense, 16-byte aligned; float32
+ *                [batch, heads, n] or NULL. Every row is written.
+ *   workspace  : wise_attn_tree_workspace bytes (device, 16-byte aligned;
+ *                scratch, needs no initialisation). Calls that may run at the
+ *                same time need workspaces of their own.
+ * Pages not in [0, n_pages) are not read (their tokens are not seen) and
+ * flagged (WISE_ERR_BAD_CACHE), as are negative lengths, new_len outside
+ * 0 .. n, and tokens past the page table. The sums of a long row are joined
+ * in a fixed order: repeated calls give the same bits.
+ */
+int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q,
+                   const int32_t* new_len, const int32_t* tree_mask, float scale, int32_t out_dtype, void* o,
+                   float* lse, void* workspace, size_t workspace_bytes, wise_stream_t stream);
+
+/*
+ * wise_cache_accept -- keeps drafted tokens: for i < n_accepted[b] the keys
+ * and values of new token path[b][i] move to token lengths[b] + i, and
+ * new_lengths[b] = lengths[b] + n_accepted[b]. Keys were rotated by their
+ * depth when they were appended, so they move as they are.
+ *   path       : [batch, path_tokens] int32, the first n_accepted[b] entries
+ *                strictly ascending (a path from the root in any order that
+ *                lists parents first), or NULL: tokens stay where they are
+ *                (new token i is kept as token i).
+ *   n_accepted : [batch] int32, 0 .. path_tokens.
+ *   new_lengths: [batch] int32; must not overlap cache->lengths.
+ * Entries that do not ascend, or whose slot does not fit the page table or
+ * lies in a page outside [0, n_pages), are not moved and flagged
+ * (WISE_ERR_BAD_CACHE); counts outside their range are clamped and flagged.
+ * One launch.
+ */
+int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,
+                      const int32_t* n_accepted, int32_t* new_lengths, wise_stream_t stream);
+
 /* Host-side check of a support CSR (host pointers): row_ptr monotone from 0,
  * every row strictly ascending with 0 <= b <= q, and, if the flags ask for
  * them, block 0 and block q present. Returns WISE_OK or
@@ -409,8 +554,9 @@ int wise_validate_schedule(const wise_attn_desc* desc, const int32_t* tile_order
 int wise_wait_expiry_check(wise_stream_t stream);
 
 /* Synchronises `stream`, then reads and clears the device error word of the
- * current device: WISE_OK, WISE_ERR_BAD_SUPPORT, WISE_ERR_DEVICE_TIMEOUT, or
- * WISE_ERR_CUDA if the synchronisation itself failed. */
+ * current device: WISE_OK, WISE_ERR_BAD_SUPPORT, WISE_ERR_BAD_CACHE,
+ * WISE_ERR_DEVICE_TIMEOUT, or WISE_ERR_CUDA if the synchronisation itself
+ * failed. */
 int wise_device_status(wise_stream_t stream);
 
 #ifdef __cplusplus
