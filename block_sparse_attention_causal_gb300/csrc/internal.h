@@ -172,7 +172,8 @@ struct AcceptLaunch {
 };
 cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream);
 
-// Attention of new tokens over a paged cache (tree_kernel.cu).
+// Attention of new tokens over a paged cache (tree_kernel.cu). The key tiles
+// of all units must number at most 2^31 - 1.
 constexpr int kTreeMaxTokens = 128;
 struct TreeLaunch {
   CacheView cache;
@@ -188,6 +189,8 @@ struct TreeLaunch {
   uint32_t* err;
 };
 int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim);
-cudaError_t launch_tree(const TreeLaunch& t, cudaStream_t stream);
+// maps = {K, V}: 3-D tensor maps [n_pages, kv_heads * page, d] with boxes of one
+// page of one head.
+cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream);
 
 }  // namespace wise

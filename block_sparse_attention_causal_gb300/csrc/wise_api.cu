@@ -289,10 +289,32 @@ RowsView rows_view(const wise_rows* r) {
   return RowsView{static_cast<const uint16_t*>(r->data), r->stride[0], r->stride[1], r->stride[2]};
 }
 
+// View [n_pages, kv_heads * page, head_dim] of a pool; boxes of one page of one
+// head and 64 (128B swizzle) or 32 (64B swizzle, head_dim 96) columns.
+int encode_pages(CUtensorMap* m, const void* ptr, const wise_paged_cache* c) {
+  auto enc = encoder();
+  if (!enc) return WISE_ERR_CUDA;
+  const int ch = (c->head_dim == 96) ? 32 : 64;
+  const cuuint64_t rows = (cuuint64_t)c->kv_heads * c->page;
+  cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, rows, (cuuint64_t)c->n_pages};
+  cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2, rows * c->head_dim * 2};
+  cuuint32_t box[3] = {(cuuint32_t)ch, (cuuint32_t)c->page, 1};
+  cuuint32_t es[3] = {1, 1, 1};
+  CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, ch == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? WISE_OK : WISE_ERR_UNSUPPORTED;
+}
+
 int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
   if (heads < 1 || heads % c->kv_heads != 0 || new_tokens < 1) return WISE_ERR_INVALID_ARGUMENT;
   if (new_tokens > kTreeMaxTokens) return WISE_ERR_UNSUPPORTED;
   if ((int64_t)c->batch * heads * new_tokens > INT32_MAX / 2) return WISE_ERR_UNSUPPORTED;
+  // key tiles of all units
+  const int64_t pairs = ((int64_t)(heads / c->kv_heads) * new_tokens + 255) / 256;
+  const int64_t tiles = ((int64_t)c->max_pages * c->page + 127) / 128;
+  if (c->kv_heads > INT32_MAX / c->batch || (int64_t)c->batch * c->kv_heads * pairs > INT32_MAX / tiles)
+    return WISE_ERR_UNSUPPORTED;
   return WISE_OK;
 }
 
@@ -782,7 +804,11 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
   t.o = o;
   t.lse = lse;
   t.workspace = workspace;
-  return launch_tree(t, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+  CUtensorMap maps[2];
+  st = encode_pages(&maps[0], cache->k_pages, cache);
+  if (st == WISE_OK) st = encode_pages(&maps[1], cache->v_pages, cache);
+  if (st != WISE_OK) return st;
+  return launch_tree(t, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
 }
 
 int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,
