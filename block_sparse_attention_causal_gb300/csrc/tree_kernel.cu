@@ -73,9 +73,9 @@ struct TreeCfg {
   static constexpr uint32_t STATS_BYTES = 2u * 3u * 128u * 4u;
   static constexpr uint32_t NF_BYTES = kNfRing * 16u;
   static constexpr int NBAR_FIXED = 2 + 2 + 2 + 2 + 2;  // q_full, s_full, p_full, o_final, drain
-  static constexpr uint32_t MISC_BYTES = 16u * 4u + 32u * 4u;
+  static constexpr uint32_t MISC_BYTES = 48u * 4u;
   static constexpr uint32_t OFF_RING = (PAIR ? 2u : 1u) * Q_BYTES;
-  static constexpr uint32_t FIXED = OFF_RING + STATS_BYTES + NF_BYTES + MISC_BYTES + (NBAR_FIXED + 3 * NS_MAX) * 8u + NS_MAX * 4u;
+  static constexpr uint32_t FIXED = OFF_RING + STATS_BYTES + NF_BYTES + MISC_BYTES + (NBAR_FIXED + 3 * NS_MAX) * 8u + 2 * NS_MAX * 4u;
   static constexpr int NS_FIT = (int)((LIMIT - FIXED) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
   static_assert(NS >= 4, "ring");
@@ -83,7 +83,7 @@ struct TreeCfg {
   static constexpr uint32_t OFF_NF = OFF_STATS + STATS_BYTES;
   static constexpr uint32_t OFF_BAR = OFF_NF + NF_BYTES;
   static constexpr uint32_t OFF_MISC = OFF_BAR + (NBAR_FIXED + 3 * NS_MAX) * 8u;
-  static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + NS_MAX * 4u;
+  static constexpr uint32_t SMEM_BYTES = OFF_MISC + MISC_BYTES + 2 * NS_MAX * 4u;
   static_assert(SMEM_BYTES <= LIMIT && OFF_RING % 1024 == 0 && KV_BYTES % 1024 == 0 && OFF_NF % 16 == 0, "shared memory");
   static constexpr uint32_t TMEM_COLS = 512;
   // Ring position pos (odd: a V tile) is its slot's use number pos / NS; with
@@ -178,6 +178,34 @@ __device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, u
       "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+// Wait until ring position `pos` is loaded. A wait for a barrier's phase parity
+// alone is not enough: the slot's use before may belong to the other stream,
+// and while that copy is still under way the barrier reads as done for the use
+// after it (copies may end in another order than they began). The producer
+// names the use that a slot is in, which says that every earlier one is over.
+template <int TAG>
+static __device__ __noinline__ bool wait_use_slow(const uint32_t* use, uint32_t want, volatile int* abort_flag,
+                                                  uint32_t* err) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (ld_acquire_smem(use) == want) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+template <int TAG>
+__device__ __forceinline__ bool wait_loaded(uint64_t* full, const uint32_t* uses, int ns, uint32_t pos,
+                                            volatile int* abort_flag, uint32_t* err) {
+  const uint32_t slot = pos % (uint32_t)ns;
+  if (ld_acquire_smem(&uses[slot]) != pos + 1u && !wait_use_slow<TAG>(&uses[slot], pos + 1u, abort_flag, err)) return false;
+  return mbar_wait<TAG>(&full[slot], (pos / (uint32_t)ns) & 1u, abort_flag, err);
+}
 __device__ __forceinline__ bool page_ok(const TreeLaunch& t, int32_t pg) { return pg >= 0 && (int64_t)pg < t.cache.n_pages; }
 
 // 32 bits from bit `off` (0 .. 127) of a 128-bit mask.
@@ -259,6 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   int* first = reinterpret_cast<int*>(misc + 2);          // the CTA's first segment: b, hk, pair, t0, tiles
   int* warp_sum = reinterpret_cast<int*>(misc + 16);      // [12]
   uint32_t* bad_boxes = misc + 48;                        // [NS] pages of the V tile that are not in the pool
+  uint32_t* uses = bad_boxes + C::NS_MAX;                 // [NS] one past the ring position that the slot is used for
   uint32_t* err = p.t.err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -280,6 +309,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&full[i], 1);
       mbar_init(&empty[i], PAIR ? 2 : 1);
       mbar_init(&guarded[i], 1);
+      uses[i] = 0u;
     }
     *abort_flag = 0;
     first[4] = 0;
@@ -405,6 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (!ok) break;
             if (lane == 0) {
               if (kv) bad_boxes[slot] = bad;
+              st_release_smem(&uses[slot], pos + 1u);
               mbar_arrive_expect_tx(&full[slot], (uint32_t)__popc(loads) * box_bytes);
             }
             __syncwarp();
@@ -436,7 +467,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         for (int t = w.t0; ok && t < w.t1; ++t, pos += 2) {
           const int slot = (int)(pos % NS);
-          ok = __all_sync(0xffffffffu, mbar_wait<2>(&full[slot], (pos / NS) & 1, abort_flag, err));
+          ok = __all_sync(0xffffffffu, wait_loaded<2>(full, uses, NS, pos, abort_flag, err));
           if (!ok) break;
           const uint32_t bad = bad_boxes[slot];
           const int kb = t * kTile;
@@ -503,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       auto issue_s = [&](uint32_t tile) -> bool {  // S_s = Q K^T of the CTA's tile `tile`
         const uint32_t pos = 2u * tile;
         const int slot = (int)(pos % NS);
-        if (!__all_sync(0xffffffffu, mbar_wait<3>(&full[slot], (pos / NS) & 1, abort_flag, err))) return false;
+        if (!__all_sync(0xffffffffu, wait_loaded<3>(full, uses, NS, pos, abort_flag, err))) return false;
         tc_fence_after();
         const uint64_t kd = kd_base + (uint64_t)((slot * C::KV_BYTES) >> 4);
         if (leader) {
@@ -530,9 +561,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (bool head = true; ok && i < nt; i += step, head = false) {
             const uint32_t pos = 2u * (tau + i) + 1u;
             const int slot = (int)(pos % NS);
-            // warp 1 passed the tile on (and the copy itself is seen directly)
-            ok = __all_sync(0xffffffffu, mbar_wait<3>(&guarded[slot], C::guard_phase(pos) & 1, abort_flag, err) &&
-                                             mbar_wait<3>(&full[slot], (pos / NS) & 1, abort_flag, err) &&
+            // V loaded (then every earlier use of the slot is over, and with
+            // it every earlier phase of `guarded`), passed on by warp 1, P written
+            ok = __all_sync(0xffffffffu, wait_loaded<3>(full, uses, NS, pos, abort_flag, err) &&
+                                             mbar_wait<3>(&guarded[slot], C::guard_phase(pos) & 1, abort_flag, err) &&
                                              mbar_wait<3>(&p_full[s], np & 1, abort_flag, err));
             if (!ok) break;
             ++np;

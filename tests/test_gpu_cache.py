@@ -162,6 +162,43 @@ def test_attention_of_a_long_cache(heads):
     assert all(torch.equal(x, y) for x, y in zip(a, b))  # joined in a fixed order
 
 
+@pytest.mark.parametrize("shape", [(64, 16, 4, 1, 1), (96, 32, 4, 4, 1), (128, 64, 8, 2, 1), (128, 128, 2, 1, 50),
+                                   (128, 16, 4, 1, 41), (96, 64, 3, 1, 90)], ids=lambda s: "d%d_p%d_h%d_%d_n%d" % s)
+def test_long_parts_of_the_line(shape):
+    """Every block works through more key tiles than its ring of slots holds,
+    over several sequences: 40 sequences, of which three are checked."""
+    d, page, h, hk, n = shape
+    rng = np.random.default_rng(d + n)
+    b, check = 40, [0, 17, 39]
+    lengths = [int(x) for x in rng.integers(2000, 6000, b)]
+    totals = [x + n for x in lengths]
+    table, n_pages = _table(rng, totals, page)
+    g = torch.Generator(device="cuda").manual_seed(d)
+    k, v = (torch.randn((n_pages, hk, page, d), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    cache = wise.PagedCache(k, v, _i32(table), _i32(lengths))
+    q = _bf16(rng.standard_normal((b, h, n, d)) * 1.5).cuda()
+    rows = [n - 1] if n == 1 else [0, n // 2, n - 1]  # rows of the checked sequences
+    o, lse = wise.tree_attention(q, cache, out_dtype=torch.float32)
+    wise.check_device()
+    for s in check:
+        pages = torch.from_numpy(table[s][:(totals[s] + page - 1) // page].astype(np.int64)).cuda()
+        kk, vv = (x[pages].transpose(0, 1).reshape(hk, -1, d)[:, :totals[s]].double().cpu().numpy() for x in (k, v))
+        for y in range(h):
+            for i in rows:
+                m = lengths[s] + i + 1
+                x = y // (h // hk)
+                qi = _np(q)[s, y, i]
+                sc = kk[x, :m] @ qi / np.sqrt(d)
+                p = np.exp(sc - sc.max())
+                want, weight = p @ vv[x, :m] / p.sum(), p @ np.abs(vv[x, :m]) / p.sum()
+                e_s = (d + 8) * F32 * (np.abs(kk[x, :m]) @ np.abs(qi)).max() / np.sqrt(d)
+                assert np.all(np.abs(_np(o)[s, y, i] - want) <= (2 * BF16 + 2 * e_s + 2.0 ** -20) * weight)
+                tol = e_s + 2.0 ** -20 + F32 * (64 + m / 8 + 2 * 12)
+                assert abs(float(lse[s, y, i]) - (sc.max() + np.log(p.sum()))) <= tol
+    again = wise.tree_attention(q, cache, out_dtype=torch.float32)
+    assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
+
+
 def test_many_sequences():
     rng = np.random.default_rng(7)
     b, page, d = 700, 16, 64
