@@ -1,0 +1,449 @@
+// Shared parts of the kernels that attend new tokens over a paged cache: WISE
+// ("Attention Routing Stabilizes Early: Working-Set Inference for Recurrent
+// Language Models") §3 Eq 2 for the rows behind the prompt -- a next token, a
+// run of tokens, a tree of drafted tokens.
+//
+//   O_i = sum_j a_ij v_j,  a_ij = exp(s_ij - LSE_i),  s_ij = scale q_i k_j,
+//   LSE_i = log sum_j exp(s_ij), over the committed tokens j and the drafted
+//   tokens that row i's mask lists.
+//
+// A unit is one (sequence, key head) and up to 256 of the rows that share its
+// keys: the queries of a group of heads times the new tokens, row = token *
+// group + head of the group. The key tiles (128 tokens) of all units form one
+// line of work that is cut into equal parts, one per CTA, so that lengths may
+// differ and one long sequence fills the GPU. A unit that a cut divides leaves
+// partial results (unnormalised O, running maximum, sum), which the join
+// kernel joins in the line's order.
+#pragma once
+#include "internal.h"
+#include "ptx.cuh"
+
+namespace wise {
+
+constexpr int kTile = 128;       // keys per tile
+constexpr int kTreeCtas = 152;   // SMs of a GB300
+constexpr int kNfRing = 16;      // segments whose taken-out values are remembered
+
+// A unit's partial results: CTA `first_cta`'s part `first_part`, then part
+// 2 c of each later CTA c; parts < 2: nothing to join.
+struct JoinRec {
+  int32_t parts, first_part, first_cta, b, hk, pair, pad0, pad1;
+};
+
+struct TreeParams {
+  TreeLaunch t;
+  int32_t group;        // query heads per key head
+  int32_t rows;         // rows of a (sequence, key head): group * n
+  int32_t pairs;        // units per (sequence, key head): ceil(rows / 256)
+  int32_t row_slots;    // rows of a partial result: min(rows, 256)
+  int32_t mask_words;   // words of a mask row
+  int32_t recs;         // join records: one per unit if there are at most kTreeCtas, else one per CTA
+  int32_t by_unit;
+  float scale_log2;
+  JoinRec* rec;
+  float* part_o;        // [2 * kTreeCtas][row_slots][d]
+  float* part_s;        // [2 * kTreeCtas][2][row_slots]: maximum (log2), sum
+};
+
+// Committed and new tokens of sequence b, clamped to what the page table
+// holds; true if nothing had to be clamped.
+__device__ __forceinline__ bool seq_counts(const TreeLaunch& t, int b, int& len, int& nl) {
+  const int64_t cap = (int64_t)t.cache.max_pages << t.cache.page_shift;
+  const int64_t l0 = __ldg(t.cache.lengths + b);
+  const int n0 = t.new_len ? __ldg(t.new_len + b) : t.n;
+  const int64_t l = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
+  int n = n0 < 0 ? 0 : (n0 > t.n ? t.n : n0);
+  if (l + n > cap) n = (int)(cap - l);
+  len = (int)l;
+  nl = n;
+  return l == l0 && n == n0;
+}
+// Key tiles (`full`) of a unit that holds a valid token's row, and how many
+// units of a key head do (`active`); each other unit counts one empty tile.
+__device__ __forceinline__ void seq_tiles(const TreeParams& p, int len, int nl, int& full, int& active) {
+  const int keys = len + nl;
+  full = keys > 0 ? (keys + kTile - 1) / kTile : 1;
+  active = (nl * p.group + 255) / 256;
+  if (active > p.pairs) active = p.pairs;
+}
+__device__ __forceinline__ int seq_line(const TreeParams& p, int full, int active) {
+  return p.t.cache.kv_heads * (active * full + (p.pairs - active));
+}
+
+// The line as one CTA sees it: its length, the number of CTAs with a part
+// [c total / ctas, (c + 1) total / ctas), and the CTA's first segment.
+struct LinePart {
+  int total, ctas;
+  int x0;    // first tile of the part
+  int left;  // its tiles (0: nothing to do)
+  int b, hk, pair, t0, len, nl, unit0;  // unit0: the first segment's unit's first tile on the line
+};
+
+// Every thread sums the tiles of consecutive sequences, the block scans the
+// sums, and the thread whose sequences hold the part's first tile finds it
+// there. Two block barriers; `scratch` holds warps + 12 words.
+template <int THREADS>
+__device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, LinePart& part) {
+  constexpr int WARPS = THREADS / 32;
+  int* sums = scratch;
+  int* found = scratch + WARPS;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int batch = p.t.cache.batch;
+  const int per = (batch + THREADS - 1) / THREADS;
+  const int b_lo = min(batch, (int)threadIdx.x * per), b_hi = min(batch, b_lo + per);
+  int mine = 0;
+  for (int b = b_lo; b < b_hi; ++b) {
+    int len, nl, fl, ac;
+    if (!seq_counts(p.t, b, len, nl) && blockIdx.x == 0) atomicOr(p.t.err, kErrBadCache);
+    seq_tiles(p, len, nl, fl, ac);
+    mine += seq_line(p, fl, ac);
+  }
+  int before = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xffffffffu, before, o);
+    if (lane >= o) before += v;
+  }
+  if (lane == 31) sums[warp] = before;
+  before -= mine;
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  int total = 0;
+#pragma unroll
+  for (int w = 0; w < WARPS; ++w) {
+    if (w < warp) before += sums[w];
+    total += sums[w];
+  }
+  const int ctas = min((int)gridDim.x, total);
+  const int cta = blockIdx.x;
+  const bool some = cta < ctas;
+  const int x0 = some ? (int)((int64_t)cta * total / ctas) : total;
+  const int x1 = some ? (int)((int64_t)(cta + 1) * total / ctas) : total;
+  if (x0 >= before && x0 < before + mine) {
+    int at = before;
+    for (int b = b_lo; b < b_hi; ++b) {
+      int len, nl, fl, ac;
+      seq_counts(p.t, b, len, nl);
+      seq_tiles(p, len, nl, fl, ac);
+      const int line = seq_line(p, fl, ac);
+      if (x0 >= at && x0 < at + line) {
+        const int per_head = ac * fl + (p.pairs - ac);
+        const int hk = (x0 - at) / per_head;
+        const int r = (x0 - at) % per_head;
+        found[0] = b;
+        found[1] = hk;
+        found[2] = r < ac * fl ? r / fl : ac + (r - ac * fl);
+        found[3] = r < ac * fl ? r % fl : 0;
+        found[4] = len;
+        found[5] = nl;
+        found[6] = x0 - found[3];
+        break;
+      }
+      at += line;
+    }
+  }
+  __syncthreads();
+  part.total = total;
+  part.ctas = ctas;
+  part.x0 = x0;
+  part.left = x1 - x0;
+  part.b = found[0];
+  part.hk = found[1];
+  part.pair = found[2];
+  part.t0 = found[3];
+  part.len = found[4];
+  part.nl = found[5];
+  part.unit0 = found[6];
+}
+
+// A CTA's walk over its part, a segment (consecutive key tiles of one unit) at
+// a time. Every role keeps its own.
+struct Walk {
+  int b, hk, pair;
+  int len, nl, full, active;
+  int t0, t1, nt;  // tiles [t0, t1) of the unit's nt
+  int keys;        // tokens that the unit's rows may see
+  int left;        // tiles of the part from t0 on
+  int seg;         // segments before this one
+
+  __device__ __forceinline__ void unit() {
+    const bool on = pair < active;
+    nt = on ? full : 1;
+    keys = on ? len + nl : 0;
+    t1 = min(nt, t0 + left);
+  }
+  __device__ __forceinline__ void start(const TreeParams& p, const LinePart& f) {
+    b = f.b;
+    hk = f.hk;
+    pair = f.pair;
+    len = f.len;
+    nl = f.nl;
+    t0 = f.t0;
+    left = f.left;
+    seg = 0;
+    seq_tiles(p, len, nl, full, active);
+    unit();
+  }
+  __device__ __forceinline__ bool next(const TreeParams& p) {
+    left -= t1 - t0;
+    if (left <= 0) return false;
+    ++seg;
+    t0 = 0;
+    if (++pair == p.pairs) {
+      pair = 0;
+      if (++hk == p.t.cache.kv_heads) {
+        hk = 0;
+        ++b;
+        seq_counts(p.t, b, len, nl);
+        seq_tiles(p, len, nl, full, active);
+      }
+    }
+    unit();
+    return true;
+  }
+  __device__ __forceinline__ bool whole() const { return t0 == 0 && t1 == nt; }
+  // partial result of this segment: 2 c for the part's first segment, 2 c + 1
+  // for its last
+  __device__ __forceinline__ int part() const { return 2 * (int)blockIdx.x + (seg == 0 ? 0 : 1); }
+};
+
+// The join record of the unit whose first tile lies in this segment (one
+// thread calls it for every segment); `last`: the part's last segment.
+__device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const Walk& w) {
+  const bool last = w.left == w.t1 - w.t0;
+  if (w.t0 == 0) {
+    JoinRec r = {1, 0, (int)blockIdx.x, w.b, w.hk, w.pair, 0, 0};
+    if (w.t1 < w.nt) {
+      // the CTA that holds the unit's last tile, which is w.nt - w.t1 tiles
+      // past the end of this part
+      const int64_t x = (int64_t)f.x0 + f.left + (w.nt - w.t1) - 1;
+      r.parts = (int)(((x + 1) * f.ctas - 1) / f.total) - (int)blockIdx.x + 1;
+      r.first_part = w.part();
+    }
+    if (p.by_unit) p.rec[(w.b * p.t.cache.kv_heads + w.hk) * p.pairs + w.pair] = r;
+    else if (last) p.rec[blockIdx.x] = r;
+  } else if (last && !p.by_unit) {
+    p.rec[blockIdx.x].parts = 0;
+  }
+}
+
+__device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ bool bar_or(uint32_t id, uint32_t nthreads, bool v) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbarrier.cta.red.or.pred q, %2, %3, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"((uint32_t)v), "r"(id), "r"(nthreads)
+      : "memory");
+  return r != 0;
+}
+__device__ __forceinline__ void tma_load_3d(void* dst, const CUtensorMap* map, uint64_t* bar, int32_t x, int32_t y,
+                                            int32_t z) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4, %5}], "
+      "[%2];" ::"r"(smem_u32(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(smem_u32(bar)), "r"(x), "r"(y), "r"(z)
+      : "memory");
+}
+__device__ __forceinline__ bool page_ok(const TreeLaunch& t, int32_t pg) { return pg >= 0 && (int64_t)pg < t.cache.n_pages; }
+
+// Wait until ring position `pos` is loaded. A wait for a barrier's phase parity
+// alone is not enough where a consumer skips uses of a slot: while the use
+// before is still being copied the barrier reads as done for the use after it
+// (copies may end in another order than they began). The producer names the
+// use that a slot is in, which says that every earlier one is over.
+template <int TAG>
+static __device__ __noinline__ bool wait_use_slow(const uint32_t* use, uint32_t want, volatile int* abort_flag,
+                                                  uint32_t* err) {
+  const uint64_t t0 = global_timer_ns();
+  for (uint32_t it = 1;; ++it) {
+    if (ld_acquire_smem(use) == want) return true;
+    if ((it & 63u) == 0) {
+      if (*abort_flag) return false;
+      if (global_timer_ns() - t0 > kWaitLimitNs) {
+        *abort_flag = 1;
+        atomicOr(err, kErrTimeout);
+        return false;
+      }
+    }
+  }
+}
+template <int TAG>
+__device__ __forceinline__ bool wait_loaded(uint64_t* full, const uint32_t* uses, int ns, uint32_t pos,
+                                            volatile int* abort_flag, uint32_t* err) {
+  const uint32_t slot = pos % (uint32_t)ns;
+  if (ld_acquire_smem(&uses[slot]) != pos + 1u && !wait_use_slow<TAG>(&uses[slot], pos + 1u, abort_flag, err)) return false;
+  return mbar_wait<TAG>(&full[slot], (pos / (uint32_t)ns) & 1u, abort_flag, err);
+}
+
+// The ring of K and V tiles in shared memory: position 2 tau holds K of the
+// CTA's tile tau, 2 tau + 1 its V, position x in slot x % NS.
+template <int D, int NS>
+struct RingCfg {
+  static constexpr int CH = (D == 96) ? 32 : 64;         // elements per swizzled row
+  static constexpr int NCH = D / CH;                     // TMA boxes per page
+  static constexpr uint32_t SWZ = (CH == 64) ? 2u : 4u;  // descriptor code: 128B / 64B swizzle
+  static constexpr uint32_t ROWB = CH * 2;               // bytes per swizzled row
+  static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
+  // Ring position pos (odd: a V tile) is its slot's use number pos / NS; with
+  // an odd number of slots every other use of a slot is a V tile.
+  __device__ static constexpr uint32_t guard_phase(uint32_t pos) { return (NS & 1) ? (pos / NS) >> 1 : pos / NS; }
+};
+struct Ring {
+  uint8_t* tiles;
+  uint64_t* full;       // [NS] tile loaded
+  uint64_t* empty;      // [NS] tile no longer needed
+  uint64_t* guarded;    // [NS] V tile passed by the guard
+  uint32_t* bad_boxes;  // [NS] pages of the V tile that are not in the pool
+  uint32_t* uses;       // [NS] one past the ring position that the slot is used for
+};
+
+// The warp that loads the ring, page by page (whole warp; lane i issues the
+// tile's page i).
+template <int D, int NS, int TAG>
+__device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const Ring& ring, const CUtensorMap* tm_k,
+                                              const CUtensorMap* tm_v, volatile int* abort_flag, int lane) {
+  using C = RingCfg<D, NS>;
+  uint32_t* err = p.t.err;
+  const int page = 1 << p.t.cache.page_shift;
+  const int boxes = kTile >> p.t.cache.page_shift;  // pages per tile
+  const uint32_t box_bytes = (uint32_t)page * D * 2u;
+  uint32_t pos = 0;
+  bool ok = true, flagged = false;
+  do {
+    const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
+    const int last_page = (w.keys - 1) >> p.t.cache.page_shift;  // -1: none
+    int have = -1;  // first page-table column that the lanes hold
+    int32_t held = -1;
+    for (int t = w.t0; ok && t < w.t1; ++t) {
+      const int col = t * boxes;
+      if (have < 0 || col + boxes > have + 32) {
+        have = col;
+        held = (col + lane <= last_page) ? __ldg(table + col + lane) : -1;
+      }
+      const int32_t pg = __shfl_sync(0xffffffffu, held, (col - have + lane) & 31);
+      const bool in = lane < boxes && col + lane <= last_page;
+      const bool good = in && page_ok(p.t, pg);
+      const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+      const uint32_t loads = __ballot_sync(0xffffffffu, good);
+      if (bad != 0u && !flagged) {
+        flagged = true;
+        if (lane == 0) atomicOr(err, kErrBadCache);
+      }
+      for (int kv = 0; kv < 2 && ok; ++kv, ++pos) {
+        const int slot = (int)(pos % NS);
+        if (pos >= (uint32_t)NS)
+          ok = __all_sync(0xffffffffu, mbar_wait<TAG>(&ring.empty[slot], ((pos / NS) - 1) & 1, abort_flag, err));
+        if (!ok) break;
+        if (lane == 0) {
+          if (kv) ring.bad_boxes[slot] = bad;
+          st_release_smem(&ring.uses[slot], pos + 1u);
+          mbar_arrive_expect_tx(&ring.full[slot], (uint32_t)__popc(loads) * box_bytes);
+        }
+        __syncwarp();
+        if (good) {
+          uint8_t* dst = ring.tiles + slot * C::KV_BYTES + (uint32_t)(lane * page) * C::ROWB;
+#pragma unroll
+          for (int c = 0; c < C::NCH; ++c)
+            tma_load_3d(dst + c * kTile * C::ROWB, kv ? tm_v : tm_k, &ring.full[slot], c * C::CH, w.hk * page, pg);
+        }
+        __syncwarp();
+      }
+    }
+  } while (ok && w.next(p));
+  // No copy into this CTA's shared memory may outlive the CTA.
+  if (lane == 0) {
+    int none = 0;
+    for (uint32_t i = (pos > (uint32_t)NS ? pos - NS : 0u); i < pos; ++i)
+      mbar_wait<TAG>(&ring.full[i % NS], (i / NS) & 1, &none, err);
+  }
+  __syncwarp();
+}
+
+// The warp that guards V: in tiles that hold drafted tokens or end past the
+// last token, rows that nobody may see are cleared (0 times what lies there
+// could be NaN), and infinities and NaN of drafted tokens are taken out, since
+// 0 times them would reach rows that do not see them. nf[seg % kNfRing][4]
+// names those tokens; their values are put back at the end for the rows that
+// see them. The ring holds fewer than kNfRing tiles, so a list is not reused
+// before its segment's results are out.
+template <int D, int NS, int TAG>
+__device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ring& ring, uint32_t* nf,
+                                           volatile int* abort_flag, int lane) {
+  using C = RingCfg<D, NS>;
+  static_assert(NS / 2 + 2 < kNfRing, "nf ring");
+  const int page = 1 << p.t.cache.page_shift;
+  uint32_t pos = 1;
+  bool ok = true;
+  do {
+    uint32_t* seg_nf = nf + (w.seg % kNfRing) * 4;
+    if (lane < 4) seg_nf[lane] = 0u;
+    __syncwarp();
+    for (int t = w.t0; ok && t < w.t1; ++t, pos += 2) {
+      const int slot = (int)(pos % NS);
+      ok = __all_sync(0xffffffffu, wait_loaded<TAG>(ring.full, ring.uses, NS, pos, abort_flag, p.t.err));
+      if (!ok) break;
+      const uint32_t bad = ring.bad_boxes[slot];
+      const int kb = t * kTile;
+      uint8_t* v = ring.tiles + slot * C::KV_BYTES;
+      if (bad != 0u || kb + kTile > w.len || w.keys == 0) {
+        const int rows = max(0, min(w.keys - kb, kTile));
+        const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+        for (int c = 0; c < C::NCH; ++c) {
+          uint8_t* vc = v + c * kTile * C::ROWB;
+          for (uint32_t x = rows * C::ROWB + lane * 16; x < kTile * C::ROWB; x += 512) *reinterpret_cast<uint4*>(vc + x) = zero;
+          for (uint32_t m = bad; m != 0u; m &= m - 1u) {
+            const uint32_t at = (uint32_t)((__ffs(m) - 1) * page) * C::ROWB;
+            for (uint32_t x = lane * 16; x < page * C::ROWB; x += 512) *reinterpret_cast<uint4*>(vc + at + x) = zero;
+          }
+        }
+        __syncwarp();
+        // drafted tokens' rows of the tile (the swizzle permutes 16-byte
+        // units within a row, so a row's units are visited in any order)
+        constexpr int U = C::ROWB / 16;
+        for (int x = max(0, w.len - kb) * U + lane; x < rows * U; x += 32)
+          for (int c = 0; c < C::NCH; ++c) {
+            uint4* at = reinterpret_cast<uint4*>(v + c * kTile * C::ROWB) + x;
+            uint4 q = *at;
+            uint32_t* e = &q.x;
+            bool hit = false;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              if ((e[i] & 0x7f80u) == 0x7f80u) {
+                e[i] &= 0xffff0000u;
+                hit = true;
+              }
+              if ((e[i] & 0x7f800000u) == 0x7f800000u) {
+                e[i] &= 0xffffu;
+                hit = true;
+              }
+            }
+            if (hit) {
+              *at = q;
+              const int j = kb + x / U - w.len;
+              atomicOr(&seg_nf[j >> 5], 1u << (j & 31));
+            }
+          }
+        fence_proxy_async();
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&ring.guarded[slot]);
+    }
+  } while (ok && w.next(p));
+  __syncwarp();
+}
+
+// Row pointer of drafted token j's values in the pool, or null.
+__device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {
+  const int64_t tok = (int64_t)len + j;
+  const int32_t pg = __ldg(t.cache.page_table + (int64_t)b * t.cache.max_pages + (tok >> t.cache.page_shift));
+  if (!page_ok(t, pg)) return nullptr;
+  return t.cache.v_pages + ((((int64_t)pg * t.cache.kv_heads + hk) << t.cache.page_shift) +
+                            (tok & ((1 << t.cache.page_shift) - 1))) * d;
+}
+
+// tree_narrow.cu: up to 64 rows per unit.
+cudaError_t launch_tree_narrow(const TreeParams& p, const CUtensorMap* maps, cudaStream_t stream);
+
+}  // namespace wise
