@@ -24,7 +24,6 @@ library on a CUDA device these functions raise.
 """
 from __future__ import annotations
 
-import contextlib
 import dataclasses
 import math
 from typing import Optional, Sequence, Tuple
@@ -44,8 +43,9 @@ _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return s.cuda_stream
+    if stream is None:  # the current stream's handle without a Stream object (3 us on the host)
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    return stream.cuda_stream
 
 
 def _ptr(t: Optional[torch.Tensor]) -> Optional[int]:
@@ -552,8 +552,8 @@ def pack_tree_mask(mask: torch.Tensor) -> torch.Tensor:
 
 def _check_array(name: str, t: torch.Tensor, dtype: torch.dtype, shape: Tuple[int, ...], dev: int) -> int:
     """Address of a dense array of exactly this type and shape on device `dev`."""
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {tuple(shape)}")
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
     return t.data_ptr()
@@ -566,15 +566,16 @@ def _check_cache(cache: PagedCache) -> Tuple[_lib.PagedCacheDesc, int]:
     kp, table = cache.k_pages, cache.page_table
     if not isinstance(kp, torch.Tensor) or kp.dim() != 4 or not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("cache.k_pages must be [n_pages, kv_heads, page, head_dim] and cache.page_table [batch, max_pages]")
-    _check_device("cache.k_pages", kp)
+    if not kp.is_cuda or kp.get_device() != torch.cuda.current_device():
+        _check_device("cache.k_pages", kp)
     dev = kp.get_device()
-    shape = tuple(kp.shape)
+    shape, rows = kp.shape, table.shape
     n_pages, hk, page, d = shape
-    b, max_pages = table.shape
+    b, max_pages = rows
     return _lib.PagedCacheDesc(b, hk, d, page, max_pages, 0, n_pages,
                                _check_array("cache.k_pages", kp, torch.bfloat16, shape, dev),
                                _check_array("cache.v_pages", cache.v_pages, torch.bfloat16, shape, dev),
-                               _check_array("cache.page_table", table, torch.int32, (b, max_pages), dev),
+                               _check_array("cache.page_table", table, torch.int32, rows, dev),
                                _check_array("cache.lengths", cache.lengths, torch.int32, (b,), dev)), dev
 
 
@@ -584,21 +585,32 @@ def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d:
         raise ValueError(f"{name} must be a bfloat16 [batch, heads, tokens, head_dim] tensor")
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
-    shape, stride = t.shape, t.stride()
-    if shape[0] != batch or shape[3] != d or shape[2] < 1 or (heads is not None and shape[1] != heads):
-        raise ValueError(f"{name} of shape {tuple(shape)} does not fit the cache (batch {batch}, "
+    b, h, n, last = t.shape
+    if b != batch or last != d or n < 1 or (heads is not None and h != heads):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} does not fit the cache (batch {batch}, "
                          + (f"{heads} heads, " if heads is not None else "") + f"head_dim {d})")
-    if stride[3] != 1:
+    sb, sh, sn, sd = t.stride()
+    if sd != 1:
         raise ValueError(f"{name} must be contiguous in its last axis")
-    r = _lib.Rows(t.data_ptr())
-    for a in range(3):
-        r.stride[a] = stride[a] if shape[a] > 1 else 0
-    return r
+    # the stride of an axis of length 1 says nothing
+    return _lib.Rows(t.data_ptr(), (sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0))
 
 
-def _on_stream(stream: Optional[torch.cuda.Stream]):
-    """Buffers allocated for a call on another stream belong to that stream."""
-    return contextlib.nullcontext() if stream is None else torch.cuda.stream(stream)
+def _check_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
+    """Handle of the stream that a call on device `dev` runs on."""
+    if stream is None:
+        return _stream_handle(None)
+    if stream.device_index != dev:
+        raise ValueError(f"stream is on {stream.device}, not on the current device cuda:{dev}")
+    return stream.cuda_stream
+
+
+def _empty(shape, dtype: torch.dtype, dev: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+    """A new buffer; one for a call on another stream belongs to that stream."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=dev)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -614,6 +626,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
     are multiples of 8 with a contiguous last axis. `lengths` does not
     change: see :func:`cache_accept`."""
     desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
     lib = _lib.load()
     b, hk, d = desc.batch, desc.kv_heads, desc.head_dim
     kr, vr = _check_rows("k", k, b, hk, d, dev), _check_rows("v", v, b, hk, d, dev)
@@ -627,9 +640,10 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
         if q.shape[2] != n:
             raise ValueError("q and k must hold the same number of tokens")
         if q_out is None:
-            with _on_stream(stream):
-                q_out = torch.empty((b, heads, n, d), dtype=torch.bfloat16, device=q.device)
-        qo = _check_array("q_out", q_out, torch.bfloat16, (b, heads, n, d), dev)
+            q_out = _empty((b, heads, n, d), torch.bfloat16, dev, stream)
+            qo = q_out.data_ptr()
+        else:
+            qo = _check_array("q_out", q_out, torch.bfloat16, (b, heads, n, d), dev)
     elif q_out is not None:
         raise ValueError("q_out without q")
     nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
@@ -639,7 +653,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
         rotary = 2 * rope.steps.numel()
         steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
         flags = _lib.WISE_ROPE_PAIRS if rope.pairs else 0
-    st = lib.wise_cache_append(desc, n, kr, vr, heads, qr, qo, nl, pos, steps, rotary, flags, _stream_handle(stream))
+    st = lib.wise_cache_append(desc, n, kr, vr, heads, qr, qo, nl, pos, steps, rotary, flags, handle)
     _lib.check(st, "wise_cache_append")
     return q_out
 
@@ -658,6 +672,7 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
     (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None); rows that
     see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf."""
     desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
     lib = _lib.load()
     b, d = desc.batch, desc.head_dim
     qr = _check_rows("q", q, b, None, d, dev)
@@ -668,19 +683,26 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
         raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
     nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
     mask = None if tree_mask is None else _check_array("tree_mask", tree_mask, torch.int32, (b, n, (n + 31) // 32), dev)
-    nbytes = int(lib.wise_attn_tree_workspace(desc, heads, n))
-    with _on_stream(stream):
-        if out is None:
-            out = torch.empty((b, heads, n, d), dtype=out_dtype, device=q.device)
-        if want_lse and lse is None:
-            lse = torch.empty((b, heads, n), dtype=torch.float32, device=q.device)
-        if workspace is None:
-            workspace = torch.empty(max(nbytes, 16), dtype=torch.uint8, device=q.device)
-    o_ptr = _check_array("out", out, out_dtype, (b, heads, n, d), dev)
-    lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev) if want_lse else None
-    _check_bytes("workspace", workspace, nbytes, q.device)
+    nbytes = lib.wise_attn_tree_workspace(desc, heads, n)
+    if out is None:
+        out = _empty((b, heads, n, d), out_dtype, dev, stream)
+        o_ptr = out.data_ptr()
+    else:
+        o_ptr = _check_array("out", out, out_dtype, (b, heads, n, d), dev)
+    lse_ptr = None
+    if want_lse:
+        if lse is None:
+            lse = _empty((b, heads, n), torch.float32, dev, stream)
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev)
+    if workspace is None:
+        workspace = _empty(nbytes, torch.uint8, dev, stream)
+    else:
+        _check_bytes("workspace", workspace, nbytes, q.device)
+        nbytes = workspace.numel()
     st = lib.wise_attn_tree(desc, heads, n, qr, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr, workspace.data_ptr(),
-                            workspace.numel(), _stream_handle(stream))
+                            nbytes, handle)
     _lib.check(st, "wise_attn_tree")
     return out, (lse if want_lse else None)
 
@@ -694,6 +716,7 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
     kept where they are. Returns the new lengths (int32 [batch], not
     cache.lengths itself: assign them, or copy them in place)."""
     desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
     lib = _lib.load()
     b = desc.batch
     na = _check_array("n_accepted", n_accepted, torch.int32, (b,), dev)
@@ -704,10 +727,11 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
         tokens = path.shape[1]
         path_ptr = _check_array("path", path, torch.int32, (b, tokens), dev)
     if new_lengths is None:
-        with _on_stream(stream):
-            new_lengths = torch.empty(b, dtype=torch.int32, device=cache.lengths.device)
-    out = _check_array("new_lengths", new_lengths, torch.int32, (b,), dev)
-    st = lib.wise_cache_accept(desc, tokens, path_ptr, na, out, _stream_handle(stream))
+        new_lengths = _empty(b, torch.int32, dev, stream)
+        out = new_lengths.data_ptr()
+    else:
+        out = _check_array("new_lengths", new_lengths, torch.int32, (b,), dev)
+    st = lib.wise_cache_accept(desc, tokens, path_ptr, na, out, handle)
     _lib.check(st, "wise_cache_accept")
     return new_lengths
 

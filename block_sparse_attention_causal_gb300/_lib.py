@@ -137,6 +137,8 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
     """Load libwise.so (building it first if it is missing or stale and nvcc
     is available). Raises if the library cannot be had."""
     global _handle
+    if _handle is not None:
+        return _handle
     with _lock:
         if _handle is not None:
             return _handle

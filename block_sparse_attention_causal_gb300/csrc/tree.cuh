@@ -33,17 +33,35 @@ struct JoinRec {
 struct TreeParams {
   TreeLaunch t;
   int32_t group;        // query heads per key head
+  uint32_t group_mul;   // ceil(2^32 / group), for rows / group
   int32_t rows;         // rows of a (sequence, key head): group * n
   int32_t pairs;        // units per (sequence, key head): ceil(rows / 256)
-  int32_t row_slots;    // rows of a partial result: min(rows, 256)
+  int32_t row_slots;    // rows of a partial result: min(rows, 256), in whole blocks of 32 for wide units
   int32_t mask_words;   // words of a mask row
   int32_t recs;         // join records: one per unit if there are at most kTreeCtas, else one per CTA
   int32_t by_unit;
   float scale_log2;
   JoinRec* rec;
-  float* part_o;        // [2 * kTreeCtas][row_slots][d]
+  // [2 * kTreeCtas][row_slots * d]: rows of d values for narrow units; for wide
+  // ones, whose threads hold a row each, blocks of 32 rows with four values of
+  // each row next to each other: [row / 32][d / 4][row % 32][4]
+  float* part_o;
   float* part_s;        // [2 * kTreeCtas][2][row_slots]: maximum (log2), sum
 };
+
+// row / group; exact for row * group < 2^32 (wise_attn_tree admits groups of at
+// most 4096 heads and 128 tokens).
+__device__ __forceinline__ int row_token(const TreeParams& p, int row) {
+  return p.group == 1 ? row : (int)__umulhi((uint32_t)row, p.group_mul);
+}
+
+// Asynchronous 16-byte copy into shared memory (no registers, nothing to wait
+// for between copies, so the loop over them stays small: a kernel that runs
+// for a few microseconds spends much of them on fetching its own code).
+__device__ __forceinline__ void copy16(void* dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
+}
+__device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 // Committed and new tokens of sequence b, clamped to what the page table
 // holds; true if nothing had to be clamped.

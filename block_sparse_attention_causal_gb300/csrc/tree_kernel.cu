@@ -90,13 +90,6 @@ static __device__ __noinline__ void rescale_row(uint32_t tO, int ncols, float fa
   }
 }
 
-// 32 consecutive bytes (a full sector) at a 32-byte aligned address.
-__device__ __forceinline__ void store32(float* dst, const uint32_t* x) {
-  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(dst), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]),
-               "r"(x[4]), "r"(x[5]), "r"(x[6]), "r"(x[7])
-               : "memory");
-}
-
 template <int D, int QROWS>
 __global__ void __launch_bounds__(kThreads, 1)
     tree_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const TreeParams p) {
@@ -316,38 +309,43 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int nrows = max(0, min(p.rows - row0, 128));
         const bool warp_on = quarter * 32 < nrows;
         const int row = row0 + r;
-        const int tok = row / p.group, g = row - tok * p.group;
+        const int tok = row_token(p, row), g = row - tok * p.group;
         const bool live = r < nrows && tok < w.nl;
         const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
         // Q of the segment (its previous readers, the S MMAs of the segment
         // before, are done), swizzled as TMA would write it
         {
-          // eight loads in flight per thread: one after the other, they took
-          // longer than ten key tiles
-          constexpr int UNITS = D / 8, LANES = PAIR ? 128 : 256, BATCH = PAIR ? D / 16 : D / 32;
-          static_assert(128 * UNITS % (LANES * BATCH) == 0, "Q");
+          constexpr int UNITS = D / 8, LANES = PAIR ? 128 : 256;
           const int first_unit = PAIR ? wg_thread : (int)threadIdx.x - 128;
           uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES;
-          for (int x0 = first_unit; x0 < nrows * UNITS; x0 += LANES * BATCH) {
-            uint4 q[BATCH];
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-              const int x = x0 + i * LANES, qr = x / UNITS, u = x % UNITS;
-              const int qt = (row0 + qr) / p.group, qg = (row0 + qr) - qt * p.group;
-              if (qr < nrows)
-                q[i] = __ldg(reinterpret_cast<const uint4*>(p.t.q.data + (int64_t)w.b * p.t.q.sb +
-                                                            (int64_t)(w.hk * p.group + qg) * p.t.q.sh +
-                                                            (int64_t)qt * p.t.q.sn + u * 8));
-            }
-#pragma unroll
-            for (int i = 0; i < BATCH; ++i) {
-              const int x = x0 + i * LANES, qr = x / UNITS, u = x % UNITS;
-              const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
-              const int sw = (R::CH == 64) ? (uc ^ (qr & 7)) : (uc ^ ((qr >> 1) & 3));
-              if (qr < nrows) *reinterpret_cast<uint4*>(sq + c * 128 * ROWB + qr * ROWB + sw * 16) = q[i];
-            }
+          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
+#pragma unroll 1
+          for (int x = first_unit; x < nrows * UNITS; x += LANES) {
+            const int qr = x / UNITS, u = x % UNITS;
+            const int qt = row_token(p, row0 + qr), qg = (row0 + qr) - qt * p.group;
+            const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
+            const int sw = (R::CH == 64) ? (uc ^ (qr & 7)) : (uc ^ ((qr >> 1) & 3));
+            copy16(sq + c * 128 * ROWB + qr * ROWB + sw * 16, src + (int64_t)qg * p.t.q.sh + (int64_t)qt * p.t.q.sn + u * 8);
           }
         }
+        // the row's mask words (drafted tokens it sees)
+        uint32_t mrow[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          mrow[i] = tok >= 32 * i + 31 ? 0xffffffffu : tok < 32 * i ? 0u : (2u << (tok - 32 * i)) - 1u;
+          if (p.t.tree_mask) mrow[i] = 0u;
+          if (p.t.tree_mask && live && i < p.mask_words)
+            mrow[i] = (uint32_t)__ldg(p.t.tree_mask + ((int64_t)w.b * p.t.n + tok) * p.mask_words + i);
+        }
+        // pages outside the pool (their tokens are not seen): looked up here
+        // once, and tile by tile only where there are any
+        bool bad_page = false;
+        {
+          const int c0 = (w.t0 * kTile) >> page_shift;
+          const int c1 = min((w.t1 * kTile) >> page_shift, (w.keys + (1 << page_shift) - 1) >> page_shift);
+          for (int c = c0 + wg_thread; c < c1; c += 128) bad_page |= !page_ok(p.t, __ldg(table + c));
+        }
+        copy16_wait();
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) {
@@ -358,28 +356,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (w.t1 - w.t0 > 1) mbar_arrive(&q_full[1]);
           }
         }
-        // the row's mask words (drafted tokens it sees)
-        uint32_t mrow[4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          uint32_t m = 0u;
-          if (live && 32 * i < w.nl) {
-            if (p.t.tree_mask)
-              m = i < p.mask_words ? (uint32_t)__ldg(p.t.tree_mask + ((int64_t)w.b * p.t.n + tok) * p.mask_words + i) : 0u;
-            else
-              m = tok >= 32 * i + 31 ? 0xffffffffu : tok < 32 * i ? 0u : (2u << (tok - 32 * i)) - 1u;
-            if (w.nl < 32 * i + 32) m &= (1u << (w.nl - 32 * i)) - 1u;
-          }
-          mrow[i] = m;
-        }
-        // pages outside the pool (their tokens are not seen): looked up here
-        // once, and tile by tile only where there are any
-        bool bad_page = false;
-        {
-          const int c0 = (w.t0 * kTile) >> page_shift;
-          const int c1 = min((w.t1 * kTile) >> page_shift, (w.keys + (1 << page_shift) - 1) >> page_shift);
-          for (int c = c0 + wg_thread; c < c1; c += 128) bad_page |= !page_ok(p.t, __ldg(table + c));
-        }
+        for (int i = 0; i < 4; ++i)  // tokens past the sequence's new ones, and rows of such
+          mrow[i] &= !live || w.nl <= 32 * i ? 0u : w.nl < 32 * i + 32 ? (1u << (w.nl - 32 * i)) - 1u : 0xffffffffu;
         bad_page = bar_or(bar_id, bar_n, bad_page);
         float m_ref = -INFINITY, l = 0.f;
         int cnt = 0;
@@ -528,9 +507,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
               for (int q = 0; q < 16; ++q) o[q] = zero ? 0u : __float_as_uint(__uint_as_float(o[q]) * inv);
               if (!whole) {
-                float* dst = p.part_o + ((int64_t)pi * p.row_slots + (row - w.pair * 256)) * D + c;
-                store32(dst, o);
-                store32(dst + 8, o + 8);
+                const int pr = row - w.pair * 256;
+                uint4* dst = reinterpret_cast<uint4*>(p.part_o + (int64_t)pi * p.row_slots * D) +
+                             ((pr >> 5) * (D / 4) + c / 4) * 32 + lane;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) dst[32 * q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
               } else if (p.t.out_f32) {
                 float* dst = static_cast<float*>(p.t.o) + out_row * D + c;
 #pragma unroll
@@ -567,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   tc_fence_before();
   __syncthreads();
-  if (warp == 3) {
+  if (warp == 2) {
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
@@ -575,7 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // Joins the partial results of a row whose unit was cut, in the line's order,
 // whatever the order in which they were written. grid.x: join records, grid.y:
-// rows (WARPS of them per block, or one whose parts the warps share).
+// rows (kJoinWarps of them per block, or one whose parts the warps share).
 constexpr int kJoinWarps = 4;
 template <int D, bool SHARE>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreeParams p) {
@@ -659,7 +640,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
     }
     m = top;
   }
-  const int tok = row / p.group, h = hk * p.group + (row - tok * p.group);
+  const int tok = row_token(p, row), h = hk * p.group + (row - tok * p.group);
   const int64_t out_row = ((int64_t)b * p.t.heads + h) * p.t.n + tok;
   const float inv = 1.f / l;
 #pragma unroll
@@ -676,6 +657,75 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
   if (lane == 0 && p.t.lse) p.t.lse[out_row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * 0.69314718055994531f;
 }
 
+// The same for wide units: a lane holds a row, a warp eight columns of a block
+// of 32 rows.
+template <int D>
+__global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const TreeParams p) {
+  constexpr int BATCH = 8;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int job = (int)blockIdx.y * kJoinWarps + warp;
+  const int rb = job / (D / 8), col = (job % (D / 8)) * 8;
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  const int4 ra = *reinterpret_cast<const int4*>(&p.rec[blockIdx.x]);
+  const int4 rc = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
+  const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rc.x;
+  const int r = rb * 32 + lane, row = rc.y * 256 + r;
+  if (parts < 2 || r >= p.row_slots || row >= p.rows) return;
+  float m = -INFINITY, l = 0.f, acc[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+  for (int k0 = 0; k0 < parts; k0 += BATCH) {
+    float pm[BATCH], pl[BATCH];
+    float4 x[BATCH], y[BATCH];
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      const int k = k0 + i;
+      pl[i] = 0.f;
+      if (k < parts) {
+        const int64_t at = k == 0 ? first_part : 2 * (first_cta + k);
+        const float* st = p.part_s + at * 2 * p.row_slots + r;
+        pm[i] = st[0];
+        pl[i] = st[p.row_slots];
+        const float4* o = reinterpret_cast<const float4*>(p.part_o + at * p.row_slots * D) + (rb * (D / 4) + col / 4) * 32 + lane;
+        x[i] = o[0];
+        y[i] = o[32];
+      }
+    }
+    float top = m;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i)
+      if (pl[i] != 0.f) top = fmaxf(top, pm[i]);
+    const float f = l == 0.f ? 0.f : fast_exp2(m - top);
+    m = top;
+    l *= f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+    for (int i = 0; i < BATCH; ++i) {
+      if (pl[i] == 0.f) continue;  // saw nothing
+      const float g = fast_exp2(pm[i] - m);
+      l += pl[i] * g;
+      acc[0] += x[i].x * g, acc[1] += x[i].y * g, acc[2] += x[i].z * g, acc[3] += x[i].w * g;
+      acc[4] += y[i].x * g, acc[5] += y[i].y * g, acc[6] += y[i].z * g, acc[7] += y[i].w * g;
+    }
+  }
+  const int tok = row_token(p, row), h = hk * p.group + (row - tok * p.group);
+  const int64_t out_row = ((int64_t)b * p.t.heads + h) * p.t.n + tok;
+  const float inv = 1.f / l;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
+  if (p.t.out_f32) {
+    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.t.o) + out_row * D + col);
+    o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
+    o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
+  } else {
+    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.t.o) + out_row * D + col) =
+        make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
+                   pack_bf16x2(acc[6], acc[7]));
+  }
+  if (col == 0 && p.t.lse) p.t.lse[out_row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * 0.69314718055994531f;
+}
+
 struct WorkspaceLayout {
   int64_t recs, row_slots, part_o, part_s, bytes;  // offsets in bytes
 };
@@ -683,7 +733,7 @@ WorkspaceLayout workspace_layout(int64_t batch, int64_t kv_heads, int64_t rows, 
   WorkspaceLayout w;
   const int64_t units = batch * kv_heads * ((rows + 255) / 256);
   w.recs = units < kTreeCtas ? units : kTreeCtas;
-  w.row_slots = rows < 256 ? rows : 256;
+  w.row_slots = rows <= 64 ? rows : rows < 256 ? (rows + 31) / 32 * 32 : 256;
   w.part_o = w.recs * (int64_t)sizeof(JoinRec);
   w.part_s = w.part_o + 2 * kTreeCtas * w.row_slots * d * 4;
   w.bytes = w.part_s + 2 * kTreeCtas * 2 * w.row_slots * 4 + 16;  // the base is rounded up to 32 bytes
@@ -720,13 +770,17 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   // few rows: a row's parts are shared by a block's warps
+  const bool wide = p.rows > 64;
   const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
-  cfg.gridDim = dim3((unsigned)p.recs, (unsigned)(share ? p.row_slots : (p.row_slots + kJoinWarps - 1) / kJoinWarps));
+  const int jobs = wide ? p.row_slots / 32 * (D / 8) : share ? p.row_slots * kJoinWarps : p.row_slots;
+  cfg.gridDim = dim3((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
   cfg.blockDim = dim3(32 * kJoinWarps);
   cfg.stream = stream;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  e = share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, true>, p) : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, false>, p);
+  e = wide    ? cudaLaunchKernelEx(&cfg, tree_join_wide_kernel<D>, p)
+      : share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, true>, p)
+              : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, false>, p);
   if (e != cudaSuccess) return e;
   return cudaGetLastError();
 }
@@ -741,6 +795,7 @@ cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream
   TreeParams p;
   p.t = t;
   p.group = t.heads / t.cache.kv_heads;
+  p.group_mul = (uint32_t)((0x100000000ull + p.group - 1) / p.group);
   p.rows = p.group * t.n;
   p.pairs = (p.rows + 255) / 256;
   p.mask_words = (t.n + 31) / 32;

@@ -34,8 +34,8 @@ struct NarrowCfg {
   static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
   static constexpr int NS_MAX = 12;
   static constexpr int NBAR = 12 + 3 * NS_MAX;
-  // thr[N], ref[N], fac[N], out[N], wmax[4][N], wsum[4][N]; seen[2][64][2]; nf; barriers; words
-  static constexpr uint32_t SMALL = 12u * N * 4u + 2u * 64u * 8u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
+  // thr[N], ref[N], fac[N], out[N], wmax[4][N], wsum[4][N]; seen[2][64][2]; words[128]; nf; barriers; words
+  static constexpr uint32_t SMALL = 12u * N * 4u + 2u * 64u * 8u + 128u * 4u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
   static constexpr uint32_t FIXED = 2u * Q_BYTES + NP * P_BYTES + SMALL;
   static constexpr int NS_FIT = (int)((kSmemLimit - FIXED) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
@@ -66,6 +66,15 @@ __device__ __forceinline__ void tmem_ld_n(uint32_t t, uint32_t (&r)[N]) {
   for (int c = 0; c < N; c += 16) tmem_ld_x16(t + c, *reinterpret_cast<uint32_t(*)[16]>(&r[c]));
 #pragma unroll
   for (int c = 0; c < N; c += 16) tmem_wait_ld16(*reinterpret_cast<uint32_t(*)[16]>(&r[c]));
+}
+
+// 8 columns, loaded and waited for.
+__device__ __forceinline__ void tmem_ld_x8(uint32_t t, uint32_t (&r)[8]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+      : "r"(t)
+      : "memory");
 }
 
 // Sums of N values over the warp's lanes by halving: each step sends half of
@@ -118,7 +127,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* wmax = res + N;                                       // [4][N]
   float* wsum = wmax + 4 * N;                                  // [4][N]
   uint32_t* seen = reinterpret_cast<uint32_t*>(wsum + 4 * N);  // [2][64][2] rows that see drafted token j (of even and odd segments)
-  uint32_t* nf = seen + 256;                                   // [kNfRing][4]
+  uint32_t* words = seen + 256;                                // [128] mask words of the segment
+  uint32_t* nf = words + 128;                                   // [kNfRing][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(nf + kNfRing * 4);
   uint64_t* q_full = bars;         // [2] Q of a segment loaded
   uint64_t* q_empty = bars + 2;    // [2] its last S MMA done
@@ -277,38 +287,25 @@ __global__ void __launch_bounds__(kThreads, 1)
       // Rows of the segment's unit, swizzled as TMA would write them; rows past
       // the last are zero (what lay there could be read as large scores).
       constexpr int UNITS = N * (D / 8);
-      constexpr int PER = UNITS / 32;
-      constexpr int BATCH = PER < 16 ? PER : PER % 16 == 0 ? 16 : 12;
-      static_assert(UNITS % 32 == 0 && PER % BATCH == 0, "Q");
+      static_assert(UNITS % 32 == 0, "Q");
       bool ok = true;
       do {
         const int buf = w.seg & 1;
         if (w.seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait<1>(&q_empty[buf], ((w.seg >> 1) - 1) & 1, abort_flag, err));
         if (!ok) break;
         uint8_t* sq = smem + C::OFF_Q + buf * C::Q_BYTES;
-        for (int x0 = 0; x0 < PER; x0 += BATCH) {
-          uint4 v[BATCH];
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int x = (x0 + i) * 32 + lane;
-            const int r = x / (D / 8), u = x % (D / 8);
-            v[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (r < p.rows) {
-              const int tok = r / p.group, g = r - tok * p.group;
-              v[i] = __ldg(reinterpret_cast<const uint4*>(p.t.q.data + (int64_t)w.b * p.t.q.sb +
-                                                          (int64_t)(w.hk * p.group + g) * p.t.q.sh +
-                                                          (int64_t)tok * p.t.q.sn + u * 8));
-            }
-          }
-#pragma unroll
-          for (int i = 0; i < BATCH; ++i) {
-            const int x = (x0 + i) * 32 + lane;
-            const int r = x / (D / 8), u = x % (D / 8);
-            const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
-            const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
-            *reinterpret_cast<uint4*>(sq + c * N * ROWB + r * ROWB + sw * 16) = v[i];
-          }
+        const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
+#pragma unroll 1
+        for (int x = lane; x < UNITS; x += 32) {
+          const int r = x / (D / 8), u = x % (D / 8);
+          const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
+          const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
+          uint8_t* dst = sq + c * N * ROWB + r * ROWB + sw * 16;
+          const int tok = row_token(p, r), g = r - tok * p.group;
+          if (r < p.rows) copy16(dst, src + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn + u * 8);
+          else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
         }
+        copy16_wait();
         fence_proxy_async();
         __syncwarp();
         if (lane == 0) mbar_arrive(&q_full[buf]);
@@ -332,22 +329,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
         const bool tail = w.t1 * kTile > w.len;
         uint32_t* sees = seen + (w.seg & 1) * 128;
-        // rows that see each drafted token
-        if (tail && tid < w.nl) {
-          const int j = tid;
-          uint64_t m = 0ull;
-          const uint64_t token = (p.group == 64) ? ~0ull : (1ull << p.group) - 1ull;
-          if (p.t.tree_mask) {
-            const int32_t* col = p.t.tree_mask + (int64_t)w.b * p.t.n * p.mask_words + (j >> 5);
-#pragma unroll 8
-            for (int i = 0; i < w.nl; ++i)
-              if ((__ldg(col + (int64_t)i * p.mask_words) >> (j & 31)) & 1) m |= token << (i * p.group);
-          } else {
-            m = ~0ull << (j * p.group);
-          }
-          sees[2 * j] = (uint32_t)m;
-          sees[2 * j + 1] = (uint32_t)(m >> 32);
-        }
+        // the mask's words, one per thread (at most 64 tokens of two words)
+        if (tail && p.t.tree_mask && tid < w.nl * p.mask_words)
+          words[tid] = (uint32_t)__ldg(p.t.tree_mask + (int64_t)w.b * p.t.n * p.mask_words + tid);
         // pages outside the pool (their tokens are not seen): looked up here
         // once, and tile by tile only where there are any
         bool bad_page = false;
@@ -357,6 +341,23 @@ __global__ void __launch_bounds__(kThreads, 1)
           for (int c = c0 + tid; c < c1; c += 128) bad_page |= !page_ok(p.t, __ldg(table + c));
         }
         bad_page = bar_or(1, 128, bad_page);
+        if (tail) {
+          // turned round: the rows that see each drafted token
+          if (tid < w.nl) {
+            const int j = tid;
+            uint64_t m = ~0ull << (j * p.group);
+            if (p.t.tree_mask) {
+              const uint64_t token = (p.group == 64) ? ~0ull : (1ull << p.group) - 1ull;
+              m = 0ull;
+#pragma unroll 1
+              for (int i = 0; i < w.nl; ++i)
+                if ((words[i * p.mask_words + (j >> 5)] >> (j & 31)) & 1u) m |= token << (i * p.group);
+            }
+            sees[2 * j] = (uint32_t)m;
+            sees[2 * j + 1] = (uint32_t)(m >> 32);
+          }
+          bar_or(1, 128, false);
+        }
         float l[N];
 #pragma unroll
         for (int i = 0; i < N; ++i) l[i] = 0.f;
@@ -472,7 +473,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         float* po = p.part_o + (int64_t)w.part() * p.row_slots * D;
         if (tid < N) {
           const float sum = (wsum[tid] + wsum[N + tid]) + (wsum[2 * N + tid] + wsum[3 * N + tid]);
-          const int tok = tid / p.group, g = tid - tok * p.group;
+          const int tok = row_token(p, tid), g = tid - tok * p.group;
           const bool zero = tok >= w.nl || sum == 0.f;  // sees nothing
           res[tid] = zero ? -1.f : whole ? 1.f / sum : 1.f;
           if (tid < p.rows) {
@@ -489,40 +490,45 @@ __global__ void __launch_bounds__(kThreads, 1)
         bar_or(1, 128, false);
         // O^T: one dimension per thread, a row's dimensions next to each other
         if (quarter * 32 < D) {
-          uint32_t o[N];
-          tmem_ld_n<N>(tO, o);
           const uint32_t* seg_nf = nf + (w.seg % kNfRing) * 4;
-          if (tail && (seg_nf[0] | seg_nf[1]) != 0u) {
-            // non-finite values of drafted tokens, for the rows that see them
-#pragma unroll 1
-            for (int j = 0; j < w.nl; ++j) {
-              if (!((seg_nf[j >> 5] >> (j & 31)) & 1u)) continue;
-              const uint16_t* v = draft_value(p.t, D, w.b, w.hk, w.len, j);
-              const uint32_t x = v ? v[key] : 0u;
-              if ((x & 0x7f80u) != 0x7f80u) continue;
-#pragma unroll
-              for (int i = 0; i < N; ++i)
-                if ((sees[2 * j + (i >> 5)] >> (i & 31)) & 1u)
-                  o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x << 16));
-            }
-            __syncwarp();
-          }
+          const bool back = tail && (seg_nf[0] | seg_nf[1]) != 0u;
+          const bool wide = !whole || p.t.out_f32;  // fp32 values
           int g = 0;
           int64_t row = head0 * p.t.n;  // row of (head, token) in the outputs
           const int64_t step_tok = 1 - (int64_t)(p.group - 1) * p.t.n;
+#pragma unroll 1
+          for (int i0 = 0; i0 < p.rows; i0 += 8) {
+            __syncwarp();
+            uint32_t o[8];
+            tmem_ld_x8(tO + i0, o);
+            if (back) {
+              // non-finite values of drafted tokens, for the rows that see them
+#pragma unroll 1
+              for (int j = 0; j < w.nl; ++j) {
+                if (!((seg_nf[j >> 5] >> (j & 31)) & 1u)) continue;
+                const uint16_t* v = draft_value(p.t, D, w.b, w.hk, w.len, j);
+                const uint32_t x = v ? v[key] : 0u;
+                if ((x & 0x7f80u) != 0x7f80u) continue;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            if (i < p.rows) {
-              const float f = res[i];
-              const float x = f < 0.f ? 0.f : __uint_as_float(o[i]) * f;
-              if (!whole) po[(int64_t)i * D + key] = x;
-              else if (p.t.out_f32) static_cast<float*>(p.t.o)[row * D + key] = x;
-              else static_cast<uint16_t*>(p.t.o)[row * D + key] = (uint16_t)pack_bf16x2(x, 0.f);
-              if (++g == p.group) {
-                g = 0;
-                row += step_tok;
-              } else {
-                row += p.t.n;
+                for (int i = 0; i < 8; ++i)
+                  if ((sees[2 * j + (i0 >> 5)] >> ((i0 & 31) + i)) & 1u)
+                    o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x << 16));
+              }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+              if (i0 + i < p.rows) {
+                const float f = res[i0 + i];
+                const float x = f < 0.f ? 0.f : __uint_as_float(o[i]) * f;
+                if (wide) {
+                  float* dst = whole ? static_cast<float*>(p.t.o) + row * D : po + (int64_t)(i0 + i) * D;
+                  dst[key] = x;
+                } else {
+                  static_cast<uint16_t*>(p.t.o)[row * D + key] = (uint16_t)pack_bf16x2(x, 0.f);
+                }
+                ++g;
+                row += g == p.group ? step_tok : (int64_t)p.t.n;
+                if (g == p.group) g = 0;
               }
             }
           }

@@ -308,7 +308,7 @@ int encode_pages(CUtensorMap* m, const void* ptr, const wise_paged_cache* c) {
 
 int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
   if (heads < 1 || heads % c->kv_heads != 0 || new_tokens < 1) return WISE_ERR_INVALID_ARGUMENT;
-  if (new_tokens > kTreeMaxTokens) return WISE_ERR_UNSUPPORTED;
+  if (new_tokens > kTreeMaxTokens || heads / c->kv_heads > 4096) return WISE_ERR_UNSUPPORTED;
   if ((int64_t)c->batch * heads * new_tokens > INT32_MAX / 2) return WISE_ERR_UNSUPPORTED;
   // key tiles of all units
   const int64_t pairs = ((int64_t)(heads / c->kv_heads) * new_tokens + 255) / 256;

@@ -480,8 +480,8 @@ size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, in
  * A row that sees nothing (an empty mask row behind an empty cache, or
  * i >= new_len[b]) gets O = 0 and LSE = -inf. Values of tokens that a row does
  * not see have no influence on it, whatever they are (infinities, NaN).
- *   heads      : query heads, a multiple of kv_heads; query head h reads
- *                key/value head h / (heads / kv_heads).
+ *   heads      : query heads, a multiple of kv_heads (at most 4096 times);
+ *                query head h reads key/value head h / (heads / kv_heads).
  *   new_tokens : n, 1 <= n <= 128 rows per sequence.
  *   q          : [batch, heads, n, head_dim], rotated as the keys are.
  *   new_len    : [batch] int32 or NULL (n each).
