@@ -61,6 +61,8 @@ __device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const 
 template <int D, bool PAIRS>
 __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
   constexpr int NP = D / 16;  // chunk pairs of a head
+  grid_wait();
+  grid_trigger();
   const int64_t item = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
   const int64_t tok = item / NP;
   if (tok >= (int64_t)p.cache.batch * p.n) return;
@@ -127,6 +129,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
 // i) are never a later entry's source.
 __global__ void __launch_bounds__(128) accept_kernel(const AcceptLaunch p) {
   constexpr int BATCH = 8;
+  grid_wait();
+  grid_trigger();
   const int chunks = p.head_dim / 8;
   const int per_seq = 2 * p.cache.kv_heads * chunks;
   const int b = blockIdx.y;
@@ -182,9 +186,7 @@ cudaError_t launch_append_d(const AppendLaunch& a, cudaStream_t stream) {
   int64_t ny = kFull / blocks;
   ny = ny < 1 ? 1 : (ny > units ? units : ny);
   const dim3 grid((unsigned)blocks, (unsigned)ny);
-  if (a.pairs) append_kernel<D, true><<<grid, 256, 0, stream>>>(a);
-  else append_kernel<D, false><<<grid, 256, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(a.pairs ? append_kernel<D, true> : append_kernel<D, false>, grid, dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -200,8 +202,7 @@ cudaError_t launch_cache_append(const AppendLaunch& a, cudaStream_t stream) {
 cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream) {
   const int per_seq = 2 * a.cache.kv_heads * (a.head_dim / 8);
   const dim3 grid((unsigned)((per_seq + 127) / 128), (unsigned)a.cache.batch);
-  accept_kernel<<<grid, 128, 0, stream>>>(a);
-  return cudaGetLastError();
+  return launch_chained(accept_kernel, grid, dim3(128), 0, stream, a);
 }
 
 }  // namespace wise

@@ -6,6 +6,28 @@
 
 namespace wise {
 
+// The paged-cache kernels are launched as programmatic dependents of whatever
+// precedes them in the stream: a kernel that has triggered (grid_trigger) lets
+// the next one's blocks start and set themselves up while it still runs. Every
+// block calls grid_wait before its first access to global memory, which waits
+// until the kernels before it are complete and their writes visible.
+template <class... P, class... A>
+inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                                  const A&... args) {
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, args...);
+  return e != cudaSuccess ? e : cudaGetLastError();
+}
+
 struct AttnParams {
   int32_t bh_count;     // batch * heads
   int32_t heads;        // query heads per batch element

@@ -311,6 +311,11 @@ __device__ __forceinline__ void named_bar_sync(uint32_t id, uint32_t nthreads) {
   asm volatile("bar.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
 
+// Programmatic dependent launch: wait for the kernels before this one; let the
+// next one's blocks start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 // One lane of the (converged) warp, chosen by the hardware; the rest get false.
 __device__ __forceinline__ bool elect_one() {
   uint32_t pred = 0;

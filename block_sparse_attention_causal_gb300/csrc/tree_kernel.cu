@@ -121,9 +121,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* err = p.t.err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-  // 128B-swizzled TMA tiles need 1024-byte aligned destinations
-  if ((smem_u32(smem) & 1023u) != 0u) {
+  if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
+    grid_wait();
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
     return;
   }
@@ -144,14 +143,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 2) {
-    tmem_alloc(tmem_base_slot, C::TMEM_COLS);
-    tmem_relinquish();
-  }
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  grid_wait();
+  // tensor memory only now: a kernel before this one that still runs could wait
+  // for what this one holds
+  if (warp == 2) {
+    tmem_alloc(tmem_base_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  grid_trigger();
   LinePart part;
   find_part<kThreads>(p, scratch, part);
   const uint32_t tbase = *tmem_base_slot;
@@ -313,19 +316,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = r < nrows && tok < w.nl;
         const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
         // Q of the segment (its previous readers, the S MMAs of the segment
-        // before, are done), swizzled as TMA would write it
+        // before, are done), swizzled as TMA would write it: a thread copies its
+        // row (or half of it, where two groups of threads have the same rows)
         {
-          constexpr int UNITS = D / 8, LANES = PAIR ? 128 : 256;
-          const int first_unit = PAIR ? wg_thread : (int)threadIdx.x - 128;
-          uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES;
-          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
-#pragma unroll 1
-          for (int x = first_unit; x < nrows * UNITS; x += LANES) {
-            const int qr = x / UNITS, u = x % UNITS;
-            const int qt = row_token(p, row0 + qr), qg = (row0 + qr) - qt * p.group;
-            const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
-            const int sw = (R::CH == 64) ? (uc ^ (qr & 7)) : (uc ^ ((qr >> 1) & 3));
-            copy16(sq + c * 128 * ROWB + qr * ROWB + sw * 16, src + (int64_t)qg * p.t.q.sh + (int64_t)qt * p.t.q.sn + u * 8);
+          constexpr int UNITS = PAIR ? D / 8 : D / 16;
+          const int u0 = PAIR ? 0 : s * UNITS;
+          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + ((int64_t)w.hk * p.group + g) * p.t.q.sh +
+                                (int64_t)tok * p.t.q.sn + u0 * 8;
+          uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES + r * ROWB;
+          if (r < nrows) {
+#pragma unroll
+            for (int i = 0; i < UNITS; ++i) {
+              const int u = u0 + i, c = u / (R::CH / 8), uc = u % (R::CH / 8);
+              const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
+              copy16(sq + c * 128 * ROWB + sw * 16, src + i * 8);
+            }
           }
         }
         // the row's mask words (drafted tokens it sees)
@@ -482,10 +487,10 @@ __global__ void __launch_bounds__(kThreads, 1)
           // without PAIR each stream writes half of the columns
           constexpr int NCOL = PAIR ? D : D / 2;
           const int col0 = PAIR ? 0 : s * NCOL;
-#pragma unroll 1
-          for (int c = col0; c < col0 + NCOL; c += 16) {
+          const int pr = row - w.pair * 256;
+          uint4* part_row = reinterpret_cast<uint4*>(p.part_o + (int64_t)pi * p.row_slots * D) + (pr >> 5) * (D / 4) * 32 + lane;
+          auto load = [&](int c, uint32_t (&o)[16]) {
             __syncwarp();
-            uint32_t o[16];
             if (PAIR) {
               tmem_ld_x16(tO + c, o);
               tmem_wait_ld16(o);
@@ -502,32 +507,43 @@ __global__ void __launch_bounds__(kThreads, 1)
                 o[q] = __float_as_uint(w1 == 0.f ? a : a + __uint_as_float(o1[q]) * w1);
               }
             }
-            if (nonfin && !zero) put_back(p.t, D, w.b, w.hk, w.len, c, back[0], back[1], back[2], back[3], o);
-            if (r < nrows) {
+          };
+          auto store = [&](int c, const uint32_t (&o)[16]) {
+            float x[16];
 #pragma unroll
-              for (int q = 0; q < 16; ++q) o[q] = zero ? 0u : __float_as_uint(__uint_as_float(o[q]) * inv);
-              if (!whole) {
-                const int pr = row - w.pair * 256;
-                uint4* dst = reinterpret_cast<uint4*>(p.part_o + (int64_t)pi * p.row_slots * D) +
-                             ((pr >> 5) * (D / 4) + c / 4) * 32 + lane;
+            for (int q = 0; q < 16; ++q) x[q] = zero ? 0.f : __uint_as_float(o[q]) * inv;
+            if (r >= nrows) return;
+            if (!whole) {
 #pragma unroll
-                for (int q = 0; q < 4; ++q) dst[32 * q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-              } else if (p.t.out_f32) {
-                float* dst = static_cast<float*>(p.t.o) + out_row * D + c;
+              for (int q = 0; q < 4; ++q)
+                part_row[(c / 4 + q) * 32] = make_uint4(__float_as_uint(x[4 * q]), __float_as_uint(x[4 * q + 1]),
+                                                        __float_as_uint(x[4 * q + 2]), __float_as_uint(x[4 * q + 3]));
+            } else if (p.t.out_f32) {
+              float4* dst = reinterpret_cast<float4*>(static_cast<float*>(p.t.o) + out_row * D + c);
 #pragma unroll
-                for (int q = 0; q < 4; ++q) reinterpret_cast<uint4*>(dst)[q] = make_uint4(o[4 * q], o[4 * q + 1], o[4 * q + 2], o[4 * q + 3]);
-              } else {
-                uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.t.o) + out_row * D + c);
+              for (int q = 0; q < 4; ++q) dst[q] = make_float4(x[4 * q], x[4 * q + 1], x[4 * q + 2], x[4 * q + 3]);
+            } else {
+              uint4* dst = reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.t.o) + out_row * D + c);
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                  uint4 x;
-                  x.x = pack_bf16x2(__uint_as_float(o[8 * q + 0]), __uint_as_float(o[8 * q + 1]));
-                  x.y = pack_bf16x2(__uint_as_float(o[8 * q + 2]), __uint_as_float(o[8 * q + 3]));
-                  x.z = pack_bf16x2(__uint_as_float(o[8 * q + 4]), __uint_as_float(o[8 * q + 5]));
-                  x.w = pack_bf16x2(__uint_as_float(o[8 * q + 6]), __uint_as_float(o[8 * q + 7]));
-                  dst[q] = x;
-                }
-              }
+              for (int q = 0; q < 2; ++q)
+                dst[q] = make_uint4(pack_bf16x2(x[8 * q], x[8 * q + 1]), pack_bf16x2(x[8 * q + 2], x[8 * q + 3]),
+                                    pack_bf16x2(x[8 * q + 4], x[8 * q + 5]), pack_bf16x2(x[8 * q + 6], x[8 * q + 7]));
+            }
+          };
+          if (__any_sync(0xffffffffu, nonfin)) {
+#pragma unroll 1
+            for (int c = col0; c < col0 + NCOL; c += 16) {
+              uint32_t o[16];
+              load(c, o);
+              if (nonfin && !zero) put_back(p.t, D, w.b, w.hk, w.len, c, back[0], back[1], back[2], back[3], o);
+              store(c, o);
+            }
+          } else {
+#pragma unroll 1
+            for (int c = col0; c < col0 + NCOL; c += 16) {
+              uint32_t o[16];
+              load(c, o);
+              store(c, o);
             }
           }
           if (r < nrows && (PAIR || s == 0)) {
@@ -566,7 +582,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int r = SHARE ? (int)blockIdx.y : (int)blockIdx.y * kJoinWarps + warp;  // row of the unit
   // every block waits: this grid must not end before the one it follows
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_trigger();
   const int4 ra = *reinterpret_cast<const int4*>(&p.rec[blockIdx.x]);
   const int4 rb = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rb.x;
@@ -665,7 +682,8 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int job = (int)blockIdx.y * kJoinWarps + warp;
   const int rb = job / (D / 8), col = (job % (D / 8)) * 8;
-  asm volatile("griddepcontrol.wait;" ::: "memory");
+  grid_wait();
+  grid_trigger();
   const int4 ra = *reinterpret_cast<const int4*>(&p.rec[blockIdx.x]);
   const int4 rc = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rc.x;
@@ -753,8 +771,7 @@ cudaError_t launch_rows(const TreeParams& p, const CUtensorMap* maps, cudaStream
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  tree_kernel<D, QROWS><<<kTreeCtas, kThreads, C::SMEM_BYTES, stream>>>(maps[0], maps[1], p);
-  return cudaGetLastError();
+  return launch_chained(tree_kernel<D, QROWS>, dim3(kTreeCtas), dim3(kThreads), C::SMEM_BYTES, stream, maps[0], maps[1], p);
 }
 
 template <int D>
@@ -763,26 +780,13 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
                   : p.rows > 64 ? launch_rows<D, 128>(p, maps, stream)
                                 : launch_tree_narrow(p, maps, stream);
   if (e != cudaSuccess) return e;
-  // a programmatic dependent launch: its blocks wait on the GPU when the last
-  // part is written
-  cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
   // few rows: a row's parts are shared by a block's warps
   const bool wide = p.rows > 64;
   const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
   const int jobs = wide ? p.row_slots / 32 * (D / 8) : share ? p.row_slots * kJoinWarps : p.row_slots;
-  cfg.gridDim = dim3((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
-  cfg.blockDim = dim3(32 * kJoinWarps);
-  cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
-  e = wide    ? cudaLaunchKernelEx(&cfg, tree_join_wide_kernel<D>, p)
-      : share ? cudaLaunchKernelEx(&cfg, tree_join_kernel<D, true>, p)
-              : cudaLaunchKernelEx(&cfg, tree_join_kernel<D, false>, p);
-  if (e != cudaSuccess) return e;
-  return cudaGetLastError();
+  const dim3 grid((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
+  auto join = wide ? tree_join_wide_kernel<D> : share ? tree_join_kernel<D, true> : tree_join_kernel<D, false>;
+  return launch_chained(join, grid, dim3(32 * kJoinWarps), 0, stream, p);
 }
 
 }  // namespace

@@ -34,8 +34,8 @@ struct NarrowCfg {
   static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
   static constexpr int NS_MAX = 12;
   static constexpr int NBAR = 12 + 3 * NS_MAX;
-  // thr[N], ref[N], fac[N], out[N], wmax[4][N], wsum[4][N]; seen[2][64][2]; words[128]; nf; barriers; words
-  static constexpr uint32_t SMALL = 12u * N * 4u + 2u * 64u * 8u + 128u * 4u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
+  // thr[N], ref[N], fac[N], res[N], offs[N], wmax[4][N], wsum[4][N]; seen[2][64][2]; words[128]; nf; barriers; words
+  static constexpr uint32_t SMALL = 14u * N * 4u + 2u * 64u * 8u + 128u * 4u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
   static constexpr uint32_t FIXED = 2u * Q_BYTES + NP * P_BYTES + SMALL;
   static constexpr int NS_FIT = (int)((kSmemLimit - FIXED) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* ref = thr + N;                                        // [N] the row's reference (log2 domain)
   float* fac = ref + N;                                        // [N] factor of a moved reference
   float* res = fac + N;                                        // [N] factor of the results (< 0: the row sees nothing)
-  float* wmax = res + N;                                       // [4][N]
+  int64_t* offs = reinterpret_cast<int64_t*>(res + N);         // [N] the row's place in the outputs
+  float* wmax = reinterpret_cast<float*>(offs + N);                                       // [4][N]
   float* wsum = wmax + 4 * N;                                  // [4][N]
   uint32_t* seen = reinterpret_cast<uint32_t*>(wsum + 4 * N);  // [2][64][2] rows that see drafted token j (of even and odd segments)
   uint32_t* words = seen + 256;                                // [128] mask words of the segment
@@ -150,8 +151,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   uint32_t* err = p.t.err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
   if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
+    grid_wait();
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
     return;
   }
@@ -173,14 +174,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     *abort_flag = 0;
     fence_mbar_init();
   }
-  if (warp == 2) {
-    tmem_alloc(tmem_base_slot, C::TMEM_COLS);
-    tmem_relinquish();
-  }
   if (threadIdx.x == 0) {
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  grid_wait();
+  // tensor memory only now: a kernel before this one that still runs could wait
+  // for what this one holds
+  if (warp == 2) {
+    tmem_alloc(tmem_base_slot, C::TMEM_COLS);
+    tmem_relinquish();
+  }
+  grid_trigger();
   LinePart part;
   find_part<kThreads>(p, scratch, part);
   const uint32_t tbase = *tmem_base_slot;
@@ -286,24 +291,28 @@ __global__ void __launch_bounds__(kThreads, 1)
       // ------------------------------------------------------------------- Q
       // Rows of the segment's unit, swizzled as TMA would write them; rows past
       // the last are zero (what lay there could be read as large scores).
-      constexpr int UNITS = N * (D / 8);
-      static_assert(UNITS % 32 == 0, "Q");
       bool ok = true;
       do {
         const int buf = w.seg & 1;
         if (w.seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait<1>(&q_empty[buf], ((w.seg >> 1) - 1) & 1, abort_flag, err));
         if (!ok) break;
         uint8_t* sq = smem + C::OFF_Q + buf * C::Q_BYTES;
-        const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
+        // each lane copies one row, or the lanes of a half-warp half of it
+        constexpr int HALVES = N == 16 ? 2 : 1, ROWS = 32 / HALVES, UNITS = D / 8 / HALVES;
 #pragma unroll 1
-        for (int x = lane; x < UNITS; x += 32) {
-          const int r = x / (D / 8), u = x % (D / 8);
-          const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
-          const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
-          uint8_t* dst = sq + c * N * ROWB + r * ROWB + sw * 16;
-          const int tok = row_token(p, r), g = r - tok * p.group;
-          if (r < p.rows) copy16(dst, src + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn + u * 8);
-          else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+        for (int r = lane % ROWS; r < N; r += ROWS) {
+          const int tok = row_token(p, r), g = r - tok * p.group, u0 = lane / ROWS * UNITS;
+          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + ((int64_t)w.hk * p.group + g) * p.t.q.sh +
+                                (int64_t)tok * p.t.q.sn + u0 * 8;
+          uint8_t* row = sq + r * ROWB;
+#pragma unroll
+          for (int i = 0; i < UNITS; ++i) {
+            const int u = u0 + i, c = u / (R::CH / 8), uc = u % (R::CH / 8);
+            const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
+            uint8_t* dst = row + c * N * ROWB + sw * 16;
+            if (r < p.rows) copy16(dst, src + i * 8);
+            else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
+          }
         }
         copy16_wait();
         fence_proxy_async();
@@ -476,6 +485,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tok = row_token(p, tid), g = tid - tok * p.group;
           const bool zero = tok >= w.nl || sum == 0.f;  // sees nothing
           res[tid] = zero ? -1.f : whole ? 1.f / sum : 1.f;
+          offs[tid] = whole ? ((head0 + g) * p.t.n + tok) * D : (int64_t)tid * D;
           if (tid < p.rows) {
             if (!whole) {
               float* st = p.part_s + (int64_t)w.part() * 2 * p.row_slots + tid;
@@ -492,12 +502,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (quarter * 32 < D) {
           const uint32_t* seg_nf = nf + (w.seg % kNfRing) * 4;
           const bool back = tail && (seg_nf[0] | seg_nf[1]) != 0u;
-          const bool wide = !whole || p.t.out_f32;  // fp32 values
-          int g = 0;
-          int64_t row = head0 * p.t.n;  // row of (head, token) in the outputs
-          const int64_t step_tok = 1 - (int64_t)(p.group - 1) * p.t.n;
-#pragma unroll 1
-          for (int i0 = 0; i0 < p.rows; i0 += 8) {
+          float* of = whole ? static_cast<float*>(p.t.o) : po;
+          uint16_t* oh = static_cast<uint16_t*>(p.t.o);
+          auto rows8 = [&](int i0, auto put) {
             __syncwarp();
             uint32_t o[8];
             tmem_ld_x8(tO + i0, o);
@@ -515,22 +522,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                     o[i] = __float_as_uint(__uint_as_float(o[i]) + __uint_as_float(x << 16));
               }
             }
+            float x[8];
+            int64_t at[8];
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-              if (i0 + i < p.rows) {
-                const float f = res[i0 + i];
-                const float x = f < 0.f ? 0.f : __uint_as_float(o[i]) * f;
-                if (wide) {
-                  float* dst = whole ? static_cast<float*>(p.t.o) + row * D : po + (int64_t)(i0 + i) * D;
-                  dst[key] = x;
-                } else {
-                  static_cast<uint16_t*>(p.t.o)[row * D + key] = (uint16_t)pack_bf16x2(x, 0.f);
-                }
-                ++g;
-                row += g == p.group ? step_tok : (int64_t)p.t.n;
-                if (g == p.group) g = 0;
-              }
+              const float f = res[i0 + i];
+              x[i] = f < 0.f ? 0.f : __uint_as_float(o[i]) * f;
+              at[i] = offs[i0 + i] + key;
             }
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              if (i0 + i < p.rows) put(at[i], x[i]);
+          };
+          if (!whole || p.t.out_f32) {
+#pragma unroll 1
+            for (int i0 = 0; i0 < p.rows; i0 += 8) rows8(i0, [&](int64_t at, float x) { of[at] = x; });
+          } else {
+#pragma unroll 1
+            for (int i0 = 0; i0 < p.rows; i0 += 8)
+              rows8(i0, [&](int64_t at, float x) { oh[at] = (uint16_t)pack_bf16x2(x, 0.f); });
           }
         }
         tc_fence_before();
@@ -558,8 +568,7 @@ cudaError_t launch(const TreeParams& p, const CUtensorMap* maps, cudaStream_t st
     if (e != cudaSuccess) return e;
     configured[dev] = true;
   }
-  tree_narrow_kernel<D, N><<<kTreeCtas, kThreads, C::SMEM_BYTES, stream>>>(maps[0], maps[1], p);
-  return cudaGetLastError();
+  return launch_chained(tree_narrow_kernel<D, N>, dim3(kTreeCtas), dim3(kThreads), C::SMEM_BYTES, stream, maps[0], maps[1], p);
 }
 
 template <int D>
