@@ -40,6 +40,7 @@ __all__ = ["discover", "select_support", "sparse", "Support", "device_status", "
            "pack_tree_mask", "cache_append", "tree_attention", "cache_accept"]
 
 _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
+_BF16, _I32 = torch.bfloat16, torch.int32
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
@@ -563,20 +564,27 @@ def _check_cache(cache: PagedCache) -> Tuple[_lib.PagedCacheDesc, int]:
     """The C descriptor of a cache and its device (the current one)."""
     if not isinstance(cache, PagedCache):
         raise ValueError("cache must be a PagedCache")
-    kp, table = cache.k_pages, cache.page_table
+    kp, vp, table, lengths = cache.k_pages, cache.v_pages, cache.page_table, cache.lengths
     if not isinstance(kp, torch.Tensor) or kp.dim() != 4 or not isinstance(table, torch.Tensor) or table.dim() != 2:
         raise ValueError("cache.k_pages must be [n_pages, kv_heads, page, head_dim] and cache.page_table [batch, max_pages]")
-    if not kp.is_cuda or kp.get_device() != torch.cuda.current_device():
-        _check_device("cache.k_pages", kp)
-    dev = kp.get_device()
-    shape, rows = kp.shape, table.shape
+    shape = kp.shape
     n_pages, hk, page, d = shape
-    b, max_pages = rows
-    return _lib.PagedCacheDesc(b, hk, d, page, max_pages, 0, n_pages,
-                               _check_array("cache.k_pages", kp, torch.bfloat16, shape, dev),
-                               _check_array("cache.v_pages", cache.v_pages, torch.bfloat16, shape, dev),
-                               _check_array("cache.page_table", table, torch.int32, rows, dev),
-                               _check_array("cache.lengths", cache.lengths, torch.int32, (b,), dev)), dev
+    b, max_pages = table.shape
+    dev = kp.get_device()
+    # everything at once (a call of a few microseconds notices each check); what
+    # fails is named below
+    if not (isinstance(vp, torch.Tensor) and isinstance(lengths, torch.Tensor) and dev >= 0
+            and dev == vp.get_device() == table.get_device() == lengths.get_device() == torch.cuda.current_device()
+            and kp.dtype == vp.dtype == _BF16 and table.dtype == lengths.dtype == _I32
+            and vp.shape == shape and lengths.shape == (b,)
+            and kp.is_contiguous() and vp.is_contiguous() and table.is_contiguous() and lengths.is_contiguous()):
+        _check_device("cache.k_pages", kp)
+        _check_array("cache.k_pages", kp, torch.bfloat16, shape, dev)
+        _check_array("cache.v_pages", vp, torch.bfloat16, shape, dev)
+        _check_array("cache.page_table", table, torch.int32, (b, max_pages), dev)
+        _check_array("cache.lengths", lengths, torch.int32, (b,), dev)
+    return _lib.PagedCacheDesc(b, hk, d, page, max_pages, 0, n_pages, kp.data_ptr(), vp.data_ptr(), table.data_ptr(),
+                               lengths.data_ptr()), dev
 
 
 def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d: int, dev: int) -> _lib.Rows:
@@ -599,7 +607,7 @@ def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d:
 def _check_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     """Handle of the stream that a call on device `dev` runs on."""
     if stream is None:
-        return _stream_handle(None)
+        return torch._C._cuda_getCurrentRawStream(dev)
     if stream.device_index != dev:
         raise ValueError(f"stream is on {stream.device}, not on the current device cuda:{dev}")
     return stream.cuda_stream

@@ -58,7 +58,10 @@ __device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const 
 // One thread per (token, pair of chunks), walking the heads of q, k and v of
 // its token: the sines and cosines of its eight frequencies are computed once
 // per token. With few tokens the heads are spread over gridDim.y.
-template <int D, bool PAIRS>
+// AHEAD heads are loaded before the first is stored (four where a thread has
+// that many: a prompt of 32K took 134 us with one, 128 us with four; with few
+// tokens the longer code costs more than it gives, 3.4 us against 3.1 us).
+template <int D, bool PAIRS, int AHEAD>
 __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
   constexpr int NP = D / 16;  // chunk pairs of a head
   grid_wait();
@@ -83,52 +86,61 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
   const int64_t dst = store ? slot_offset(p.cache, b, (int64_t)len + i, D, p.err) : -1;
   const int64_t head_step = (int64_t)D << p.cache.page_shift;
   float cs[8], sn[8];
-  if (rot) {
-    const int64_t pos = p.positions ? (int64_t)__ldg(p.positions + tok) : (int64_t)len + i;
-#pragma unroll
-    for (int f = 0; f < 8; ++f) {
-      // the angle in turns modulo one, exact: the low 64 bits of the product
-      const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(p.rope + 8 * c + f);
-      const float x = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in units of pi, [-1, 1]
-      sincospif(x, &sn[f], &cs[f]);
-    }
-  }
   const uint16_t* kb = p.k.data + (int64_t)b * p.k.sb + (int64_t)i * p.k.sn;
   const uint16_t* vb = p.v.data + (int64_t)b * p.v.sb + (int64_t)i * p.v.sn;
-  for (int u = blockIdx.y; u < units; u += gridDim.y) {
-    const uint16_t* src;
-    uint16_t* out;
-    bool turn = rot;
-    if (u < p.heads) {
-      src = p.q.data + (int64_t)b * p.q.sb + (int64_t)u * p.q.sh + (int64_t)i * p.q.sn;
-      out = p.q_out + (((int64_t)b * p.heads + u) * p.n + i) * D;
-    } else {
-      if (dst < 0) break;
-      const int h = u - p.heads;
-      if (h < p.cache.kv_heads) {
-        src = kb + (int64_t)h * p.k.sh;
-        out = p.cache.k_pages + dst + h * head_step;
-      } else {
-        src = vb + (int64_t)(h - p.cache.kv_heads) * p.v.sh;
-        out = p.cache.v_pages + dst + (h - p.cache.kv_heads) * head_step;
-        turn = false;
+  for (int u0 = blockIdx.y; u0 < units; u0 += AHEAD * gridDim.y) {
+    ChunkPair x[AHEAD];
+    uint16_t* out[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      const int u = u0 + k * gridDim.y;
+      const uint16_t* src;
+      out[k] = nullptr;
+      if (u < p.heads) {
+        src = p.q.data + (int64_t)b * p.q.sb + (int64_t)u * p.q.sh + (int64_t)i * p.q.sn;
+        out[k] = p.q_out + (((int64_t)b * p.heads + u) * p.n + i) * D;
+      } else if (dst >= 0 && u < units) {
+        const int h = u - p.heads;
+        const bool key = h < p.cache.kv_heads;
+        const int hv = key ? h : h - p.cache.kv_heads;
+        src = (key ? kb : vb) + (int64_t)hv * (key ? p.k.sh : p.v.sh);
+        out[k] = (key ? p.cache.k_pages : p.cache.v_pages) + dst + hv * head_step;
+      }
+      if (out[k]) {
+        x[k].a = __ldg(reinterpret_cast<const uint4*>(src + ca));
+        x[k].b = __ldg(reinterpret_cast<const uint4*>(src + cb));
       }
     }
-    ChunkPair x;
-    x.a = __ldg(reinterpret_cast<const uint4*>(src + ca));
-    x.b = __ldg(reinterpret_cast<const uint4*>(src + cb));
-    if (turn) rotate<PAIRS>(x, cs, sn);
-    *reinterpret_cast<uint4*>(out + ca) = x.a;
-    *reinterpret_cast<uint4*>(out + cb) = x.b;
+    if (u0 == (int)blockIdx.y && rot) {
+      // after the first loads are on their way
+      const int64_t pos = p.positions ? (int64_t)__ldg(p.positions + tok) : (int64_t)len + i;
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+        // the angle in turns modulo one, exact: the low 64 bits of the product
+        const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(p.rope + 8 * c + f);
+        const float t = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in units of pi, [-1, 1]
+        sincospif(t, &sn[f], &cs[f]);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < AHEAD; ++k) {
+      if (!out[k]) continue;
+      if (rot && u0 + k * (int)gridDim.y < p.heads + p.cache.kv_heads) rotate<PAIRS>(x[k], cs, sn);
+      *reinterpret_cast<uint4*>(out[k] + ca) = x[k].a;
+      *reinterpret_cast<uint4*>(out[k] + cb) = x[k].b;
+    }
   }
 }
 
-// One thread per (sequence, pool, head, 16-byte chunk), walking the accepted
-// path in order. The path ascends strictly, so entry i >= i: a batch's loads
-// all come before its stores, and the stores of earlier entries (slots below
-// i) are never a later entry's source.
-__global__ void __launch_bounds__(128) accept_kernel(const AcceptLaunch p) {
+// One thread per (sequence, pool, head, 16-byte chunk). The block first looks up
+// where the path's tokens lie (up to 128 at a time), then each thread moves its
+// chunk of them in order. An entry that is kept ascends and is at least its
+// place i: a batch's loads all come before its stores, and the stores of
+// earlier entries (slots below i) are never a later entry's source.
+constexpr int kAcceptThreads = 128;
+__global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptLaunch p) {
   constexpr int BATCH = 8;
+  __shared__ int64_t from[kAcceptThreads], to[kAcceptThreads];
   grid_wait();
   grid_trigger();
   const int chunks = p.head_dim / 8;
@@ -143,36 +155,40 @@ __global__ void __launch_bounds__(128) accept_kernel(const AcceptLaunch p) {
     na = len < 0 ? 0 : max(0, (int32_t)min((int64_t)min(na, p.path_tokens), max(room, (int64_t)0)));
   }
   if (x == 0) p.new_lengths[b] = len + na;
-  if (p.path == nullptr || x >= per_seq || len < 0) return;
+  if (p.path == nullptr || len < 0) return;
   const int chunk = x % chunks, hp = x / chunks;
   const int h = hp % p.cache.kv_heads;
   uint16_t* pool = (hp < p.cache.kv_heads ? p.cache.k_pages : p.cache.v_pages) +
                    (((int64_t)h * p.head_dim) << p.cache.page_shift) + chunk * 8;
   const int32_t* path = p.path + (int64_t)b * p.path_tokens;
-  int32_t prev = -1;
-  for (int i0 = 0; i0 < na; i0 += BATCH) {
-    uint4 v[BATCH];
-    int64_t to[BATCH];
-#pragma unroll
-    for (int k = 0; k < BATCH; ++k) {
-      to[k] = -1;
-      const int i = i0 + k;
-      if (i >= na) continue;
-      const int32_t src = __ldg(path + i);
-      if (src <= prev || src < i) {
+  for (int i0 = 0; i0 < na; i0 += kAcceptThreads) {
+    const int mine = i0 + threadIdx.x;
+    int64_t f = -1, t = -1;
+    if (mine < na) {
+      const int32_t src = __ldg(path + mine), prev = mine > 0 ? __ldg(path + mine - 1) : -1;
+      if (src <= prev || src < mine) {
         atomicOr(p.err, kErrBadCache);
-        continue;
+      } else if (src != mine) {  // else already in its place
+        f = slot_offset(p.cache, b, (int64_t)len + src, p.head_dim, p.err);
+        t = slot_offset(p.cache, b, (int64_t)len + mine, p.head_dim, p.err);
       }
-      prev = src;
-      if (src == i) continue;  // already in its place
-      const int64_t from = slot_offset(p.cache, b, (int64_t)len + src, p.head_dim, p.err);
-      if (from < 0) continue;
-      v[k] = *reinterpret_cast<const uint4*>(pool + from);
-      to[k] = slot_offset(p.cache, b, (int64_t)len + i, p.head_dim, p.err);
     }
+    from[threadIdx.x] = f;
+    to[threadIdx.x] = f < 0 ? -1 : t;
+    __syncthreads();
+    const int some = min(na - i0, kAcceptThreads);
+    if (x < per_seq) {
+      for (int i = 0; i < some; i += BATCH) {
+        uint4 v[BATCH];
 #pragma unroll
-    for (int k = 0; k < BATCH; ++k)
-      if (to[k] >= 0) *reinterpret_cast<uint4*>(pool + to[k]) = v[k];
+        for (int k = 0; k < BATCH; ++k)
+          if (i + k < some && to[i + k] >= 0) v[k] = *reinterpret_cast<const uint4*>(pool + from[i + k]);
+#pragma unroll
+        for (int k = 0; k < BATCH; ++k)
+          if (i + k < some && to[i + k] >= 0) *reinterpret_cast<uint4*>(pool + to[i + k]) = v[k];
+      }
+    }
+    __syncthreads();
   }
 }
 
@@ -186,7 +202,9 @@ cudaError_t launch_append_d(const AppendLaunch& a, cudaStream_t stream) {
   int64_t ny = kFull / blocks;
   ny = ny < 1 ? 1 : (ny > units ? units : ny);
   const dim3 grid((unsigned)blocks, (unsigned)ny);
-  return launch_chained(a.pairs ? append_kernel<D, true> : append_kernel<D, false>, grid, dim3(256), 0, stream, a);
+  auto kernel = ny * 4 <= units ? (a.pairs ? append_kernel<D, true, 4> : append_kernel<D, false, 4>)
+                                : (a.pairs ? append_kernel<D, true, 1> : append_kernel<D, false, 1>);
+  return launch_chained(kernel, grid, dim3(256), 0, stream, a);
 }
 
 }  // namespace
@@ -201,8 +219,8 @@ cudaError_t launch_cache_append(const AppendLaunch& a, cudaStream_t stream) {
 
 cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream) {
   const int per_seq = 2 * a.cache.kv_heads * (a.head_dim / 8);
-  const dim3 grid((unsigned)((per_seq + 127) / 128), (unsigned)a.cache.batch);
-  return launch_chained(accept_kernel, grid, dim3(128), 0, stream, a);
+  const dim3 grid((unsigned)((per_seq + kAcceptThreads - 1) / kAcceptThreads), (unsigned)a.cache.batch);
+  return launch_chained(accept_kernel, grid, dim3(kAcceptThreads), 0, stream, a);
 }
 
 }  // namespace wise

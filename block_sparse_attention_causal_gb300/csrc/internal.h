@@ -194,9 +194,10 @@ struct AcceptLaunch {
 };
 cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream);
 
-// Attention of new tokens over a paged cache (tree_kernel.cu). The key tiles
-// of all units must number at most 2^31 - 1.
+// Attention of new tokens over a paged cache (tree_kernel.cu). The key
+// tiles and kTreeOverhead places of each unit must number at most 2^31 - 1.
 constexpr int kTreeMaxTokens = 128;
+constexpr int kTreeOverhead = 8;  // at most this many places of the line of work per unit, besides its key tiles
 struct TreeLaunch {
   CacheView cache;
   int32_t head_dim, heads, n;

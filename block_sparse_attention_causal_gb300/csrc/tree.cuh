@@ -13,7 +13,10 @@
 // line of work that is cut into equal parts, one per CTA, so that lengths may
 // differ and one long sequence fills the GPU. A unit that a cut divides leaves
 // partial results (unnormalised O, running maximum, sum), which the join
-// kernel joins in the line's order.
+// kernel joins in the line's order. Each unit's tiles follow `overhead` places
+// of the line that stand for the change from one unit to the next (results
+// out, Q in, the pipeline filled again), so that a CTA whose part holds such a
+// change has fewer tiles.
 #pragma once
 #include "internal.h"
 #include "ptx.cuh"
@@ -40,6 +43,7 @@ struct TreeParams {
   int32_t mask_words;   // words of a mask row
   int32_t recs;         // join records: one per unit if there are at most kTreeCtas, else one per CTA
   int32_t by_unit;
+  int32_t overhead;     // places of the line before a unit's tiles
   float scale_log2;
   JoinRec* rec;
   // [2 * kTreeCtas][row_slots * d]: rows of d values for narrow units; for wide
@@ -85,16 +89,24 @@ __device__ __forceinline__ void seq_tiles(const TreeParams& p, int len, int nl, 
   if (active > p.pairs) active = p.pairs;
 }
 __device__ __forceinline__ int seq_line(const TreeParams& p, int full, int active) {
-  return p.t.cache.kv_heads * (active * full + (p.pairs - active));
+  return p.t.cache.kv_heads * (active * full + (p.pairs - active) + p.pairs * p.overhead);
 }
 
-// The line as one CTA sees it: its length, the number of CTAs with a part
-// [c total / ctas, (c + 1) total / ctas), and the CTA's first segment.
+// The line as one CTA sees it: CTA c's part begins at place c * per + c * more
+// / ctas (= c * total / ctas); and the CTA's first segment.
 struct LinePart {
-  int total, ctas;
-  int x0;    // first tile of the part
-  int left;  // its tiles (0: nothing to do)
-  int b, hk, pair, t0, len, nl, unit0;  // unit0: the first segment's unit's first tile on the line
+  int per, more, ctas;
+  int x1;    // end of the part
+  int left;  // places from the first segment's first tile on (<= 0: nothing to do)
+  int b, hk, pair, t0, len, nl;
+  __device__ __forceinline__ int begin(int c) const { return c * per + c * more / ctas; }
+  // the CTA whose part holds place x
+  __device__ __forceinline__ int owner(int x) const {
+    int c = min((int)((float)x / ((float)per + (float)more / (float)ctas)), ctas - 1);
+    while (c > 0 && begin(c) > x) --c;
+    while (c + 1 < ctas && begin(c + 1) <= x) ++c;
+    return c;
+  }
 };
 
 // Every thread sums the tiles of consecutive sequences, the block scans the
@@ -107,6 +119,13 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
   int* found = scratch + WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int batch = p.t.cache.batch;
+  {
+    // the page table into L2, a line per thread of the grid, while the lengths
+    // are read: the loads that follow from them then find it there
+    const int64_t line = (int64_t)threadIdx.x * gridDim.x + blockIdx.x;
+    const int64_t entries = (int64_t)batch * p.t.cache.max_pages;
+    if (line * 32 < entries) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.t.cache.page_table + line * 32));
+  }
   const int per = (batch + THREADS - 1) / THREADS;
   const int b_lo = min(batch, (int)threadIdx.x * per), b_hi = min(batch, b_lo + per);
   int mine = 0;
@@ -133,12 +152,13 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
     if (w < warp) before += sums[w];
     total += sums[w];
   }
-  const int ctas = min((int)gridDim.x, total);
   const int cta = blockIdx.x;
-  const bool some = cta < ctas;
-  const int x0 = some ? (int)((int64_t)cta * total / ctas) : total;
-  const int x1 = some ? (int)((int64_t)(cta + 1) * total / ctas) : total;
-  if (x0 >= before && x0 < before + mine) {
+  part.ctas = min((int)gridDim.x, total);
+  part.per = total / part.ctas;
+  part.more = total - part.per * part.ctas;
+  const int x0 = cta < part.ctas ? part.begin(cta) : total;
+  const int x1 = cta < part.ctas ? part.begin(cta + 1) : total;
+  if (x0 >= before && x0 < before + mine) {  // (x0 is the line's end without a part)
     int at = before;
     for (int b = b_lo; b < b_hi; ++b) {
       int len, nl, fl, ac;
@@ -146,33 +166,37 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
       seq_tiles(p, len, nl, fl, ac);
       const int line = seq_line(p, fl, ac);
       if (x0 >= at && x0 < at + line) {
-        const int per_head = ac * fl + (p.pairs - ac);
+        const int ov = p.overhead, per_head = line / p.t.cache.kv_heads;
         const int hk = (x0 - at) / per_head;
-        const int r = (x0 - at) % per_head;
+        int r = x0 - at - hk * per_head, pair;
+        if (r < ac * (fl + ov)) {
+          pair = r / (fl + ov);
+          r -= pair * (fl + ov);
+        } else {
+          pair = ac + (r - ac * (fl + ov)) / (1 + ov);
+          r -= ac * (fl + ov) + (pair - ac) * (1 + ov);
+        }
         found[0] = b;
         found[1] = hk;
-        found[2] = r < ac * fl ? r / fl : ac + (r - ac * fl);
-        found[3] = r < ac * fl ? r % fl : 0;
-        found[4] = len;
-        found[5] = nl;
-        found[6] = x0 - found[3];
+        found[2] = pair;
+        found[3] = max(r - ov, 0);               // first tile
+        found[4] = x1 - x0 - max(ov - r, 0);     // places from there on
+        found[5] = len;
+        found[6] = nl;
         break;
       }
       at += line;
     }
   }
   __syncthreads();
-  part.total = total;
-  part.ctas = ctas;
-  part.x0 = x0;
-  part.left = x1 - x0;
+  part.x1 = x1;
+  part.left = x1 > x0 ? found[4] : 0;
   part.b = found[0];
   part.hk = found[1];
   part.pair = found[2];
   part.t0 = found[3];
-  part.len = found[4];
-  part.nl = found[5];
-  part.unit0 = found[6];
+  part.len = found[5];
+  part.nl = found[6];
 }
 
 // A CTA's walk over its part, a segment (consecutive key tiles of one unit) at
@@ -182,7 +206,7 @@ struct Walk {
   int len, nl, full, active;
   int t0, t1, nt;  // tiles [t0, t1) of the unit's nt
   int keys;        // tokens that the unit's rows may see
-  int left;        // tiles of the part from t0 on
+  int left;        // places of the part from tile t0 on
   int seg;         // segments before this one
 
   __device__ __forceinline__ void unit() {
@@ -204,7 +228,7 @@ struct Walk {
     unit();
   }
   __device__ __forceinline__ bool next(const TreeParams& p) {
-    left -= t1 - t0;
+    left -= t1 - t0 + p.overhead;
     if (left <= 0) return false;
     ++seg;
     t0 = 0;
@@ -227,23 +251,22 @@ struct Walk {
 };
 
 // The join record of the unit whose first tile lies in this segment (one
-// thread calls it for every segment); `last`: the part's last segment.
+// thread calls it for every segment, and first clear_rec).
+__device__ __forceinline__ void clear_rec(const TreeParams& p) {
+  if (!p.by_unit) p.rec[blockIdx.x].parts = 0;
+}
 __device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const Walk& w) {
-  const bool last = w.left == w.t1 - w.t0;
-  if (w.t0 == 0) {
-    JoinRec r = {1, 0, (int)blockIdx.x, w.b, w.hk, w.pair, 0, 0};
-    if (w.t1 < w.nt) {
-      // the CTA that holds the unit's last tile, which is w.nt - w.t1 tiles
-      // past the end of this part
-      const int64_t x = (int64_t)f.x0 + f.left + (w.nt - w.t1) - 1;
-      r.parts = (int)(((x + 1) * f.ctas - 1) / f.total) - (int)blockIdx.x + 1;
-      r.first_part = w.part();
-    }
-    if (p.by_unit) p.rec[(w.b * p.t.cache.kv_heads + w.hk) * p.pairs + w.pair] = r;
-    else if (last) p.rec[blockIdx.x] = r;
-  } else if (last && !p.by_unit) {
-    p.rec[blockIdx.x].parts = 0;
+  if (w.t0 != 0) return;
+  const bool cut = w.t1 < w.nt;
+  JoinRec r = {1, 0, (int)blockIdx.x, w.b, w.hk, w.pair, 0, 0};
+  if (cut) {
+    // up to the CTA that holds the unit's last tile, w.nt - w.t1 places past
+    // the end of this part
+    r.parts = f.owner(f.x1 + (w.nt - w.t1) - 1) - (int)blockIdx.x + 1;
+    r.first_part = w.part();
   }
+  if (p.by_unit) p.rec[(w.b * p.t.cache.kv_heads + w.hk) * p.pairs + w.pair] = r;
+  else if (cut) p.rec[blockIdx.x] = r;
 }
 
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }

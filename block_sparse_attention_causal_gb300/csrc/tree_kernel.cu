@@ -16,6 +16,8 @@ namespace wise {
 namespace {
 
 constexpr int kThreads = 384;
+constexpr int kWideOverhead = 6, kNarrowOverhead = 1;
+static_assert(kWideOverhead <= kTreeOverhead && kNarrowOverhead <= kTreeOverhead, "wise_attn_tree's bound on the line");
 
 template <int D, int QROWS>
 struct TreeCfg {
@@ -159,6 +161,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   find_part<kThreads>(p, scratch, part);
   const uint32_t tbase = *tmem_base_slot;
   const bool any = part.left > 0;
+  if (threadIdx.x == 128) clear_rec(p);
   Walk w;
   if (any) w.start(p, part);
 
@@ -316,21 +319,24 @@ __global__ void __launch_bounds__(kThreads, 1)
         const bool live = r < nrows && tok < w.nl;
         const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
         // Q of the segment (its previous readers, the S MMAs of the segment
-        // before, are done), swizzled as TMA would write it: a thread copies its
-        // row (or half of it, where two groups of threads have the same rows)
+        // before, are done), swizzled as TMA would write it. Neighbouring
+        // lanes copy neighbouring 16-byte units, so that a warp asks for whole
+        // lines: a row per lane took 5 us for the 128 rows of a cold Q.
         {
-          constexpr int UNITS = PAIR ? D / 8 : D / 16;
-          const int u0 = PAIR ? 0 : s * UNITS;
-          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + ((int64_t)w.hk * p.group + g) * p.t.q.sh +
-                                (int64_t)tok * p.t.q.sn + u0 * 8;
-          uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES + r * ROWB;
-          if (r < nrows) {
-#pragma unroll
-            for (int i = 0; i < UNITS; ++i) {
-              const int u = u0 + i, c = u / (R::CH / 8), uc = u % (R::CH / 8);
-              const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
-              copy16(sq + c * 128 * ROWB + sw * 16, src + i * 8);
-            }
+          constexpr int UNITS = D / 8, GROUP = UNITS > 8 ? 16 : 8;  // lanes per row
+          constexpr int STEP = (PAIR ? 128 : 256) / GROUP;          // rows per round
+          const int u = lane % GROUP;
+          const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
+          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh + u * 8;
+          uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES + c * 128 * ROWB;
+          const int qr0 = (PAIR ? wg_thread : (int)threadIdx.x - 128) / GROUP;
+#pragma unroll 4
+          for (int k = 0; k < 128 / STEP; ++k) {
+            const int qr = qr0 + k * STEP;
+            const int qt = row_token(p, row0 + qr), qg = (row0 + qr) - qt * p.group;
+            const int sw = (R::CH == 64) ? (uc ^ (qr & 7)) : (uc ^ ((qr >> 1) & 3));
+            if (qr < nrows && u < UNITS)
+              copy16(sq + qr * ROWB + sw * 16, src + (int64_t)qg * p.t.q.sh + (int64_t)qt * p.t.q.sn);
           }
         }
         // the row's mask words (drafted tokens it sees)
@@ -804,6 +810,10 @@ cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream
   p.pairs = (p.rows + 255) / 256;
   p.mask_words = (t.n + 31) / 32;
   p.scale_log2 = t.scale * 1.4426950408889634f;
+  // a change of units costs a wide unit about as much as six key tiles
+  // (128 KB of partial results out, Q in behind the loads of K and V), a narrow
+  // one about as much as one
+  p.overhead = p.rows > 64 ? kWideOverhead : kNarrowOverhead;
   const WorkspaceLayout w = workspace_layout(t.cache.batch, t.cache.kv_heads, p.rows, t.head_dim);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(t.workspace) + 31) / 32 * 32);
   p.recs = (int32_t)w.recs;

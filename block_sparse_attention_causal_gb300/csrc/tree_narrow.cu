@@ -189,6 +189,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   LinePart part;
   find_part<kThreads>(p, scratch, part);
   const uint32_t tbase = *tmem_base_slot;
+  if (threadIdx.x == 128) clear_rec(p);
   Walk w;
   if (part.left > 0) {
     w.start(p, part);
@@ -209,16 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         const uint64_t q_desc = smem_desc(smem_u32(smem + C::OFF_Q), 16, 8 * ROWB, R::SWZ);
         const uint64_t p_desc = smem_desc(smem_u32(smem + C::OFF_P), 16, 8 * 128, 2u);
         const uint32_t dO = tbase + 2 * N;
-        const uint32_t tiles = (uint32_t)part.left;
-        uint32_t ts = 0, tp = 0;
+        uint32_t ts = 0, tp = 0;  // tiles whose S and PV are issued
+        bool more = true;         // tiles whose S is not
         Walk ws = w, wp = w;
         int s_at = w.t0, p_at = w.t0;  // tiles within the segments
         uint64_t t0 = 0;
         uint32_t idle = 0;  // rounds without work
         bool ok = true;
-        while (tp < tiles && ok) {
+        while ((more || tp < ts) && ok) {
           bool moved = false;
-          if (ts < tiles && ts < tp + 2u) {
+          if (more && ts < tp + 2u) {
             const uint32_t pos = 2u * ts;
             const int slot = (int)(pos % NS);
             const bool head = s_at == ws.t0;
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               ++ts;
               if (++s_at == ws.t1) {
                 umma_commit(&q_empty[ws.seg & 1]);
-                ws.next(p);
+                more = ws.next(p);
                 s_at = ws.t0;
               }
               moved = true;
@@ -496,7 +497,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        if (tid == 0) write_rec(p, part, w);
+        if (threadIdx.x == 128) write_rec(p, part, w);
         bar_or(1, 128, false);
         // O^T: one dimension per thread, a row's dimensions next to each other
         if (quarter * 32 < D) {

@@ -312,7 +312,7 @@ int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
   if ((int64_t)c->batch * heads * new_tokens > INT32_MAX / 2) return WISE_ERR_UNSUPPORTED;
   // key tiles of all units
   const int64_t pairs = ((int64_t)(heads / c->kv_heads) * new_tokens + 255) / 256;
-  const int64_t tiles = ((int64_t)c->max_pages * c->page + 127) / 128;
+  const int64_t tiles = ((int64_t)c->max_pages * c->page + 127) / 128 + kTreeOverhead;
   if (c->kv_heads > INT32_MAX / c->batch || (int64_t)c->batch * c->kv_heads * pairs > INT32_MAX / tiles)
     return WISE_ERR_UNSUPPORTED;
   return WISE_OK;
