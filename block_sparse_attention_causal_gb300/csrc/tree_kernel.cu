@@ -680,74 +680,83 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
   if (lane == 0 && p.t.lse) p.t.lse[out_row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * 0.69314718055994531f;
 }
 
-// The same for wide units: a lane holds a row, a warp eight columns of a block
-// of 32 rows.
+// The same for wide units: a lane holds a row, a warp four columns of a block of
+// 32 rows, the block's warps 16 columns. The first partial results are asked for
+// before the maxima and sums that weigh them are known.
 template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const TreeParams p) {
-  constexpr int BATCH = 8;
+  constexpr int BATCH = 10;
+  __shared__ float ss[kJoinWarps][2][32];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int job = (int)blockIdx.y * kJoinWarps + warp;
-  const int rb = job / (D / 8), col = (job % (D / 8)) * 8;
+  const int rb = (int)blockIdx.y / (D / 16), c4 = (int)blockIdx.y % (D / 16) * kJoinWarps + warp;
   grid_wait();
   grid_trigger();
   const int4 ra = *reinterpret_cast<const int4*>(&p.rec[blockIdx.x]);
   const int4 rc = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rc.x;
   const int r = rb * 32 + lane, row = rc.y * 256 + r;
-  if (parts < 2 || r >= p.row_slots || row >= p.rows) return;
-  float m = -INFINITY, l = 0.f, acc[8];
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-  for (int k0 = 0; k0 < parts; k0 += BATCH) {
-    float pm[BATCH], pl[BATCH];
-    float4 x[BATCH], y[BATCH];
+  if (parts < 2 || rc.y * 256 + rb * 32 >= p.rows) return;
+  auto part_at = [&](int k) -> int64_t { return k == 0 ? first_part : 2 * (first_cta + k); };
+  const float* st = p.part_s + r;
+  const float4* po = reinterpret_cast<const float4*>(p.part_o) + (rb * (D / 4) + c4) * 32 + lane;
+  float pm[BATCH], pl[BATCH];
+  float4 x[BATCH];
+  auto fetch = [&](int k0) {
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      const int k = k0 + i;
       pl[i] = 0.f;
-      if (k < parts) {
-        const int64_t at = k == 0 ? first_part : 2 * (first_cta + k);
-        const float* st = p.part_s + at * 2 * p.row_slots + r;
-        pm[i] = st[0];
-        pl[i] = st[p.row_slots];
-        const float4* o = reinterpret_cast<const float4*>(p.part_o + at * p.row_slots * D) + (rb * (D / 4) + col / 4) * 32 + lane;
-        x[i] = o[0];
-        y[i] = o[32];
+      if (k0 + i < parts) {
+        const int64_t at = part_at(k0 + i) * p.row_slots;
+        x[i] = po[at * (D / 4)];
+        pm[i] = st[at * 2];
+        pl[i] = st[at * 2 + p.row_slots];
       }
     }
-    float top = m;
-#pragma unroll
-    for (int i = 0; i < BATCH; ++i)
-      if (pl[i] != 0.f) top = fmaxf(top, pm[i]);
-    const float f = l == 0.f ? 0.f : fast_exp2(m - top);
+  };
+  fetch(0);
+  // the row's maximum and sum: every warp over its share of the parts
+  float m = -INFINITY, l = 0.f;
+#pragma unroll 4
+  for (int k = warp; k < parts; k += kJoinWarps) {
+    const int64_t at = part_at(k) * p.row_slots;
+    const float mk = st[at * 2], lk = st[at * 2 + p.row_slots];
+    if (lk == 0.f) continue;  // saw nothing
+    const float top = fmaxf(m, mk);
+    l = (l == 0.f ? 0.f : l * fast_exp2(m - top)) + lk * fast_exp2(mk - top);
     m = top;
-    l *= f;
+  }
+  ss[warp][0][lane] = m;
+  ss[warp][1][lane] = l;
+  __syncthreads();
+  float top = -INFINITY, sum = 0.f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] *= f;
+  for (int k = 0; k < kJoinWarps; ++k)
+    if (ss[k][1][lane] != 0.f) top = fmaxf(top, ss[k][0][lane]);
+#pragma unroll
+  for (int k = 0; k < kJoinWarps; ++k)
+    if (ss[k][1][lane] != 0.f) sum += ss[k][1][lane] * fast_exp2(ss[k][0][lane] - top);
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  for (int k0 = 0; k0 < parts; k0 += BATCH) {
+    if (k0 > 0) fetch(k0);
 #pragma unroll
     for (int i = 0; i < BATCH; ++i) {
-      if (pl[i] == 0.f) continue;  // saw nothing
-      const float g = fast_exp2(pm[i] - m);
-      l += pl[i] * g;
-      acc[0] += x[i].x * g, acc[1] += x[i].y * g, acc[2] += x[i].z * g, acc[3] += x[i].w * g;
-      acc[4] += y[i].x * g, acc[5] += y[i].y * g, acc[6] += y[i].z * g, acc[7] += y[i].w * g;
+      if (pl[i] == 0.f) continue;
+      const float g = fast_exp2(pm[i] - top);
+      acc.x += x[i].x * g, acc.y += x[i].y * g, acc.z += x[i].z * g, acc.w += x[i].w * g;
     }
   }
+  if (row >= p.rows) return;
   const int tok = row_token(p, row), h = hk * p.group + (row - tok * p.group);
   const int64_t out_row = ((int64_t)b * p.t.heads + h) * p.t.n + tok;
-  const float inv = 1.f / l;
-#pragma unroll
-  for (int e = 0; e < 8; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
-  if (p.t.out_f32) {
-    float4* o = reinterpret_cast<float4*>(static_cast<float*>(p.t.o) + out_row * D + col);
-    o[0] = make_float4(acc[0], acc[1], acc[2], acc[3]);
-    o[1] = make_float4(acc[4], acc[5], acc[6], acc[7]);
-  } else {
-    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.t.o) + out_row * D + col) =
-        make_uint4(pack_bf16x2(acc[0], acc[1]), pack_bf16x2(acc[2], acc[3]), pack_bf16x2(acc[4], acc[5]),
-                   pack_bf16x2(acc[6], acc[7]));
-  }
-  if (col == 0 && p.t.lse) p.t.lse[out_row] = l == 0.f ? -INFINITY : (m + fast_log2(l)) * 0.69314718055994531f;
+  const float inv = sum == 0.f ? 0.f : 1.f / sum;
+  const bool zero = sum == 0.f;
+  const float4 o = make_float4(zero ? 0.f : acc.x * inv, zero ? 0.f : acc.y * inv, zero ? 0.f : acc.z * inv,
+                               zero ? 0.f : acc.w * inv);
+  if (p.t.out_f32) reinterpret_cast<float4*>(static_cast<float*>(p.t.o) + out_row * D)[c4] = o;
+  else
+    reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.t.o) + out_row * D)[c4] =
+        make_uint2(pack_bf16x2(o.x, o.y), pack_bf16x2(o.z, o.w));
+  if (c4 == 0 && p.t.lse) p.t.lse[out_row] = zero ? -INFINITY : (top + fast_log2(sum)) * 0.69314718055994531f;
 }
 
 struct WorkspaceLayout {
@@ -789,7 +798,7 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
   // few rows: a row's parts are shared by a block's warps
   const bool wide = p.rows > 64;
   const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
-  const int jobs = wide ? p.row_slots / 32 * (D / 8) : share ? p.row_slots * kJoinWarps : p.row_slots;
+  const int jobs = wide ? p.row_slots / 32 * (D / 4) : share ? p.row_slots * kJoinWarps : p.row_slots;
   const dim3 grid((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
   auto join = wide ? tree_join_wide_kernel<D> : share ? tree_join_kernel<D, true> : tree_join_kernel<D, false>;
   return launch_chained(join, grid, dim3(32 * kJoinWarps), 0, stream, p);
