@@ -109,6 +109,22 @@ struct LinePart {
   }
 };
 
+// The lengths and the page table into L2 while the kernel before this one may
+// still run (nothing is read; a line that it writes is written there). The
+// first tiles wait for three loads in a row -- lengths, page table, keys --
+// each of which takes a microsecond or two from a cold memory.
+__device__ __forceinline__ void prefetch_tables(const TreeParams& p) {
+  auto prefetch = [](const void* a) { asm volatile("prefetch.global.L2 [%0];" ::"l"(a)); };
+  const int64_t line = (int64_t)threadIdx.x * 32;  // 32 entries of 4 bytes
+  if (line < p.t.cache.batch) {
+    prefetch(p.t.cache.lengths + line);
+    if (p.t.new_len) prefetch(p.t.new_len + line);
+  }
+  // the table: a line per thread of the grid
+  const int64_t at = line * gridDim.x + (int64_t)blockIdx.x * 32;
+  if (at < (int64_t)p.t.cache.batch * p.t.cache.max_pages) prefetch(p.t.cache.page_table + at);
+}
+
 // Every thread sums the tiles of consecutive sequences, the block scans the
 // sums, and the thread whose sequences hold the part's first tile finds it
 // there. Two block barriers; `scratch` holds warps + 12 words.
@@ -119,13 +135,6 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
   int* found = scratch + WARPS;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int batch = p.t.cache.batch;
-  {
-    // the page table into L2, a line per thread of the grid, while the lengths
-    // are read: the loads that follow from them then find it there
-    const int64_t line = (int64_t)threadIdx.x * gridDim.x + blockIdx.x;
-    const int64_t entries = (int64_t)batch * p.t.cache.max_pages;
-    if (line * 32 < entries) asm volatile("prefetch.global.L2 [%0];" ::"l"(p.t.cache.page_table + line * 32));
-  }
   const int per = (batch + THREADS - 1) / THREADS;
   const int b_lo = min(batch, (int)threadIdx.x * per), b_hi = min(batch, b_lo + per);
   int mine = 0;

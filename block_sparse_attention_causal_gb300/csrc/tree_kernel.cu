@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     tma_prefetch_desc(&tm_k);
     tma_prefetch_desc(&tm_v);
   }
+  prefetch_tables(p);
   grid_wait();
   // tensor memory only now: a kernel before this one that still runs could wait
   // for what this one holds
