@@ -329,13 +329,24 @@ __device__ __forceinline__ bool wait_loaded(uint64_t* full, const uint32_t* uses
 
 // The ring of K and V tiles in shared memory: position 2 tau holds K of the
 // CTA's tile tau, 2 tau + 1 its V, position x in slot x % NS.
+// A tile's rows lie in chunks of 64 values (128 swizzled bytes). For 96
+// dimensions the second chunk's upper half lies past the tensor and is filled
+// with zeros: chunks of 32 values would need no room for them, but half as many
+// copy requests again (rows of 64 bytes).
+constexpr uint32_t kRowBytes = 128u;
+constexpr uint32_t kSwizzle128 = 2u;  // descriptor code
+template <int D>
+__host__ __device__ constexpr int row_chunks() { return (D + 63) / 64; }
+template <int D>
+__host__ __device__ constexpr uint32_t tile_bytes(int rows) { return (uint32_t)rows * row_chunks<D>() * kRowBytes; }
+// Byte offset of a row's 16-byte unit u in a tile of `rows` rows.
+__device__ __forceinline__ uint32_t unit_offset(int rows, int row, int u) {
+  return (uint32_t)((u >> 3) * rows + row) * kRowBytes + (uint32_t)((u & 7) ^ (row & 7)) * 16u;
+}
 template <int D, int NS>
 struct RingCfg {
-  static constexpr int CH = (D == 96) ? 32 : 64;         // elements per swizzled row
-  static constexpr int NCH = D / CH;                     // TMA boxes per page
-  static constexpr uint32_t SWZ = (CH == 64) ? 2u : 4u;  // descriptor code: 128B / 64B swizzle
-  static constexpr uint32_t ROWB = CH * 2;               // bytes per swizzled row
-  static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
+  static constexpr int NCH = row_chunks<D>();  // TMA boxes per page
+  static constexpr uint32_t KV_BYTES = tile_bytes<D>(kTile);
   // Ring position pos (odd: a V tile) is its slot's use number pos / NS; with
   // an odd number of slots every other use of a slot is a V tile.
   __device__ static constexpr uint32_t guard_phase(uint32_t pos) { return (NS & 1) ? (pos / NS) >> 1 : pos / NS; }
@@ -345,9 +356,32 @@ struct Ring {
   uint64_t* full;       // [NS] tile loaded
   uint64_t* empty;      // [NS] tile no longer needed
   uint64_t* guarded;    // [NS] V tile passed by the guard
-  uint32_t* bad_boxes;  // [NS] pages of the V tile that are not in the pool
   uint32_t* uses;       // [NS] one past the ring position that the slot is used for
+  uint32_t* flags;      // [kTileFlags] see tile_bad
 };
+
+// Pages of the CTA's tile `tile` that are not in the pool (bit i: page i of the
+// tile), as the producer found them. Its word names the tile, so that a reader
+// knows the word for its own; the ring holds far fewer than kTileFlags tiles.
+constexpr int kTileFlags = 16;
+__device__ __forceinline__ uint32_t tile_word(uint32_t tile, uint32_t bad) { return ((tile + 1u) << 8) | bad; }
+template <int TAG>
+static __device__ __noinline__ uint32_t tile_bad_slow(const uint32_t* flag, uint32_t tile, volatile int* abort_flag) {
+  for (;;) {
+    const uint32_t v = ld_acquire_smem(flag);
+    if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
+    if (*abort_flag) return 0u;
+  }
+}
+// (called once the tile's copies or MMAs were seen done, so the word is there
+// or a few cycles away)
+template <int TAG>
+__device__ __forceinline__ uint32_t tile_bad(const Ring& ring, uint32_t tile, volatile int* abort_flag) {
+  const uint32_t* flag = &ring.flags[tile % kTileFlags];
+  const uint32_t v = ld_acquire_smem(flag);
+  if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
+  return tile_bad_slow<TAG>(flag, tile, abort_flag);
+}
 
 // The warp that loads the ring, page by page (whole warp; lane i issues the
 // tile's page i).
@@ -358,19 +392,23 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
   uint32_t* err = p.t.err;
   const int page = 1 << p.t.cache.page_shift;
   const int boxes = kTile >> p.t.cache.page_shift;  // pages per tile
-  const uint32_t box_bytes = (uint32_t)page * D * 2u;
+  const uint32_t box_bytes = tile_bytes<D>(page);
   uint32_t pos = 0;
   bool ok = true, flagged = false;
   do {
     const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
     const int last_page = (w.keys - 1) >> p.t.cache.page_shift;  // -1: none
-    int have = -1;  // first page-table column that the lanes hold
-    int32_t held = -1;
+    // the lanes hold 32 columns of the page table from `have` on, and the 32
+    // after them, which are under way while these are used
+    int have = w.t0 * boxes;
+    auto columns = [&](int c) -> int32_t { return c + lane <= last_page ? __ldg(table + c + lane) : -1; };
+    int32_t held = columns(have), ahead = columns(have + 32);
     for (int t = w.t0; ok && t < w.t1; ++t) {
       const int col = t * boxes;
-      if (have < 0 || col + boxes > have + 32) {
-        have = col;
-        held = (col + lane <= last_page) ? __ldg(table + col + lane) : -1;
+      if (col >= have + 32) {  // (32 columns are whole tiles)
+        have += 32;
+        held = ahead;
+        ahead = columns(have + 32);
       }
       const int32_t pg = __shfl_sync(0xffffffffu, held, (col - have + lane) & 31);
       const bool in = lane < boxes && col + lane <= last_page;
@@ -381,22 +419,22 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
         flagged = true;
         if (lane == 0) atomicOr(err, kErrBadCache);
       }
+      if (lane == 0) st_release_smem(&ring.flags[(pos >> 1) % kTileFlags], tile_word(pos >> 1, bad));
       for (int kv = 0; kv < 2 && ok; ++kv, ++pos) {
         const int slot = (int)(pos % NS);
         if (pos >= (uint32_t)NS)
           ok = __all_sync(0xffffffffu, mbar_wait<TAG>(&ring.empty[slot], ((pos / NS) - 1) & 1, abort_flag, err));
         if (!ok) break;
         if (lane == 0) {
-          if (kv) ring.bad_boxes[slot] = bad;
           st_release_smem(&ring.uses[slot], pos + 1u);
           mbar_arrive_expect_tx(&ring.full[slot], (uint32_t)__popc(loads) * box_bytes);
         }
         __syncwarp();
         if (good) {
-          uint8_t* dst = ring.tiles + slot * C::KV_BYTES + (uint32_t)(lane * page) * C::ROWB;
+          uint8_t* dst = ring.tiles + slot * C::KV_BYTES + (uint32_t)(lane * page) * kRowBytes;
 #pragma unroll
           for (int c = 0; c < C::NCH; ++c)
-            tma_load_3d(dst + c * kTile * C::ROWB, kv ? tm_v : tm_k, &ring.full[slot], c * C::CH, w.hk * page, pg);
+            tma_load_3d(dst + c * kTile * kRowBytes, kv ? tm_v : tm_k, &ring.full[slot], c * 64, w.hk * page, pg);
         }
         __syncwarp();
       }
@@ -422,7 +460,7 @@ template <int D, int NS, int TAG>
 __device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ring& ring, uint32_t* nf,
                                            volatile int* abort_flag, int lane) {
   using C = RingCfg<D, NS>;
-  static_assert(NS / 2 + 2 < kNfRing, "nf ring");
+  static_assert(NS / 2 + 2 < kNfRing && NS / 2 + 4 < kTileFlags, "nf ring, tile flags");
   const int page = 1 << p.t.cache.page_shift;
   uint32_t pos = 1;
   bool ok = true;
@@ -434,27 +472,27 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ri
       const int slot = (int)(pos % NS);
       ok = __all_sync(0xffffffffu, wait_loaded<TAG>(ring.full, ring.uses, NS, pos, abort_flag, p.t.err));
       if (!ok) break;
-      const uint32_t bad = ring.bad_boxes[slot];
+      const uint32_t bad = tile_bad<TAG>(ring, pos >> 1, abort_flag);
       const int kb = t * kTile;
       uint8_t* v = ring.tiles + slot * C::KV_BYTES;
       if (bad != 0u || kb + kTile > w.len || w.keys == 0) {
         const int rows = max(0, min(w.keys - kb, kTile));
         const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
         for (int c = 0; c < C::NCH; ++c) {
-          uint8_t* vc = v + c * kTile * C::ROWB;
-          for (uint32_t x = rows * C::ROWB + lane * 16; x < kTile * C::ROWB; x += 512) *reinterpret_cast<uint4*>(vc + x) = zero;
+          uint8_t* vc = v + c * kTile * kRowBytes;
+          for (uint32_t x = rows * kRowBytes + lane * 16; x < kTile * kRowBytes; x += 512) *reinterpret_cast<uint4*>(vc + x) = zero;
           for (uint32_t m = bad; m != 0u; m &= m - 1u) {
-            const uint32_t at = (uint32_t)((__ffs(m) - 1) * page) * C::ROWB;
-            for (uint32_t x = lane * 16; x < page * C::ROWB; x += 512) *reinterpret_cast<uint4*>(vc + at + x) = zero;
+            const uint32_t at = (uint32_t)((__ffs(m) - 1) * page) * kRowBytes;
+            for (uint32_t x = lane * 16; x < page * kRowBytes; x += 512) *reinterpret_cast<uint4*>(vc + at + x) = zero;
           }
         }
         __syncwarp();
         // drafted tokens' rows of the tile (the swizzle permutes 16-byte
         // units within a row, so a row's units are visited in any order)
-        constexpr int U = C::ROWB / 16;
+        constexpr int U = kRowBytes / 16;
         for (int x = max(0, w.len - kb) * U + lane; x < rows * U; x += 32)
           for (int c = 0; c < C::NCH; ++c) {
-            uint4* at = reinterpret_cast<uint4*>(v + c * kTile * C::ROWB) + x;
+            uint4* at = reinterpret_cast<uint4*>(v + c * kTile * kRowBytes) + x;
             uint4 q = *at;
             uint32_t* e = &q.x;
             bool hit = false;

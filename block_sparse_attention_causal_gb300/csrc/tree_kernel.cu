@@ -16,20 +16,20 @@ namespace wise {
 namespace {
 
 constexpr int kThreads = 384;
-constexpr int kWideOverhead = 6, kNarrowOverhead = 1;
+constexpr int kWideOverhead = 8, kNarrowOverhead = 2;
 static_assert(kWideOverhead <= kTreeOverhead && kNarrowOverhead <= kTreeOverhead, "wise_attn_tree's bound on the line");
 
 template <int D, int QROWS>
 struct TreeCfg {
   static constexpr bool PAIR = QROWS == 256;
-  static constexpr uint32_t Q_BYTES = 128u * D * 2u;
-  static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
+  static constexpr uint32_t Q_BYTES = tile_bytes<D>(128);
+  static constexpr uint32_t KV_BYTES = tile_bytes<D>(kTile);
   static constexpr uint32_t LIMIT = 232448u;
   static constexpr int NS_MAX = 12;
   static constexpr int NBAR = 9 + 3 * NS_MAX;
   static constexpr uint32_t OFF_RING = (PAIR ? 2u : 1u) * Q_BYTES;
-  // stats[2][2][128]; nf; barriers; words
-  static constexpr uint32_t SMALL = 2u * 2u * 128u * 4u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
+  // stats[2][2][2][128]; nf; barriers; words
+  static constexpr uint32_t SMALL = 2u * 2u * 2u * 128u * 4u + kNfRing * 16u + NBAR * 8u + (NS_MAX + kTileFlags) * 4u + 40u * 4u;
   static constexpr int NS_FIT = (int)((LIMIT - OFF_RING - SMALL) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
   static_assert(NS >= 4, "ring");
@@ -99,10 +99,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   using R = RingCfg<D, C::NS>;
   constexpr bool PAIR = C::PAIR;
   constexpr int NS = C::NS;
-  constexpr uint32_t ROWB = R::ROWB;
   extern __shared__ __align__(1024) uint8_t smem[];
-  float* stats = reinterpret_cast<float*>(smem + C::OFF_SMALL);  // [2][2][128] reference and sum of each stream's rows
-  uint32_t* nf = reinterpret_cast<uint32_t*>(stats + 512);       // [kNfRing][4]
+  // [2][2][2][128] of even and odd segments, each stream: references and sums of its rows
+  float* stats = reinterpret_cast<float*>(smem + C::OFF_SMALL);
+  uint32_t* nf = reinterpret_cast<uint32_t*>(stats + 1024);  // [kNfRing][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(nf + kNfRing * 4);
   uint64_t* q_full = bars;           // [2] Q of a segment in which stream s has tiles is in shared memory
   uint64_t* s_full = q_full + 2;     // [2] S_s computed
@@ -114,9 +114,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   ring.full = drain + 1;
   ring.empty = ring.full + C::NS_MAX;
   ring.guarded = ring.empty + C::NS_MAX;
-  ring.bad_boxes = reinterpret_cast<uint32_t*>(bars + C::NBAR);
-  ring.uses = ring.bad_boxes + C::NS_MAX;
-  uint32_t* misc = ring.uses + C::NS_MAX;
+  ring.uses = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  ring.flags = ring.uses + C::NS_MAX;
+  uint32_t* misc = ring.flags + kTileFlags;
   uint32_t* tmem_base_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   int* scratch = reinterpret_cast<int*>(misc + 4);  // [12 + 12]
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ring.guarded[i], 1);
       ring.uses[i] = 0u;
     }
+    for (int i = 0; i < kTileFlags; ++i) ring.flags[i] = 0u;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -184,9 +185,9 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, kTile, 0, 0);
         constexpr uint32_t IDESC_O = idesc_bf16_f32(128, D, 0, 1);
-        const uint64_t q_desc = smem_desc(smem_u32(smem), 16, 8 * ROWB, R::SWZ);
-        const uint64_t kd_base = smem_desc(smem_u32(ring.tiles), 16, 8 * ROWB, R::SWZ);
-        const uint64_t vd_base = smem_desc(smem_u32(ring.tiles), kTile * ROWB, 8 * ROWB, R::SWZ);
+        const uint64_t q_desc = smem_desc(smem_u32(smem), 16, 8 * kRowBytes, kSwizzle128);
+        const uint64_t kd_base = smem_desc(smem_u32(ring.tiles), 16, 8 * kRowBytes, kSwizzle128);
+        const uint64_t vd_base = smem_desc(smem_u32(ring.tiles), kTile * kRowBytes, 8 * kRowBytes, kSwizzle128);
         constexpr int STEP = PAIR ? 1 : 2;
         struct Stream {
           Walk w;
@@ -233,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool head = st.i < STEP;
 #pragma unroll
             for (int kk = 0; kk < kTile / 16; ++kk)
-              umma_ts(tbase + C::o_col(s), dS + kk * 8, vd + (uint64_t)((kk * 16 * ROWB) >> 4), IDESC_O,
+              umma_ts(tbase + C::o_col(s), dS + kk * 8, vd + (uint64_t)((kk * 16 * kRowBytes) >> 4), IDESC_O,
                       (head && kk == 0) ? 0u : 1u);
             umma_commit(&ring.empty[slot]);
             st.want_s = true;
@@ -256,9 +257,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const uint64_t kd = kd_base + (uint64_t)((slot * C::KV_BYTES) >> 4);
 #pragma unroll
           for (int kk = 0; kk < D / 16; ++kk) {
-            const int c = kk / (R::CH / 16), wd = kk % (R::CH / 16);
-            umma_ss(dS, qd + (uint64_t)((c * 128 * ROWB + wd * 32) >> 4),
-                    kd + (uint64_t)((c * kTile * ROWB + wd * 32) >> 4), IDESC_S, kk > 0);
+            const int c = kk / 4, wd = kk % 4;
+            umma_ss(dS, qd + (uint64_t)((c * 128 * kRowBytes + wd * 32) >> 4),
+                    kd + (uint64_t)((c * kTile * kRowBytes + wd * 32) >> 4), IDESC_S, kk > 0);
           }
           umma_commit(&s_full[s]);
           umma_commit(&ring.empty[slot]);
@@ -308,9 +309,45 @@ __global__ void __launch_bounds__(kThreads, 1)
       const uint32_t tO = trow + C::o_col(s);
       const float sl2 = p.scale_log2;
       const int page_shift = p.t.cache.page_shift;
-      uint32_t ne = 0, nfin = 0;
+      uint32_t ne = 0, nfin = 0, tau0 = 0;
       bool ok = true;
-      do {
+      // Q of a segment, swizzled as TMA would write it. Neighbouring lanes copy
+      // neighbouring 16-byte units, so that a warp asks for whole lines (a row
+      // per lane took 5 us for the 128 rows of a cold Q).
+      auto load_q = [&](const Walk& x) {
+        constexpr int UNITS = D / 8, GROUP = UNITS > 8 ? 16 : 8;  // lanes per row
+        constexpr int STEP = (PAIR ? 128 : 256) / GROUP;          // rows per round
+        const int row0 = x.pair * 256 + (PAIR ? 128 * s : 0), nrows = min(p.rows - row0, 128);
+        const int u = lane % GROUP;
+        const uint16_t* src = p.t.q.data + (int64_t)x.b * p.t.q.sb + (int64_t)x.hk * p.group * p.t.q.sh + u * 8;
+        uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES;
+        const int qr0 = (PAIR ? wg_thread : (int)threadIdx.x - 128) / GROUP;
+#pragma unroll 4
+        for (int k = 0; k < 128 / STEP; ++k) {
+          const int qr = qr0 + k * STEP;
+          const int qt = row_token(p, row0 + qr), qg = (row0 + qr) - qt * p.group;
+          if (qr < nrows && u < UNITS)
+            copy16(sq + unit_offset(128, qr, u), src + (int64_t)qg * p.t.q.sh + (int64_t)qt * p.t.q.sn);
+        }
+      };
+      auto publish_q = [&](const Walk& x) {
+        copy16_wait();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) {
+          if (PAIR) {
+            mbar_arrive(&q_full[s]);
+          } else {
+            mbar_arrive(&q_full[0]);
+            if (x.t1 - x.t0 > 1) mbar_arrive(&q_full[1]);
+          }
+        }
+      };
+      load_q(w);
+      publish_q(w);
+      for (;;) {
+        Walk wn = w;
+        const bool more = wn.next(p);
         // rows of this tile: row = token * group + head of the group
         const int row0 = w.pair * 256 + (PAIR ? 128 * s : 0);
         const int nrows = max(0, min(p.rows - row0, 128));
@@ -318,28 +355,6 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int row = row0 + r;
         const int tok = row_token(p, row), g = row - tok * p.group;
         const bool live = r < nrows && tok < w.nl;
-        const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
-        // Q of the segment (its previous readers, the S MMAs of the segment
-        // before, are done), swizzled as TMA would write it. Neighbouring
-        // lanes copy neighbouring 16-byte units, so that a warp asks for whole
-        // lines: a row per lane took 5 us for the 128 rows of a cold Q.
-        {
-          constexpr int UNITS = D / 8, GROUP = UNITS > 8 ? 16 : 8;  // lanes per row
-          constexpr int STEP = (PAIR ? 128 : 256) / GROUP;          // rows per round
-          const int u = lane % GROUP;
-          const int c = u / (R::CH / 8), uc = u % (R::CH / 8);
-          const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh + u * 8;
-          uint8_t* sq = smem + (PAIR ? s : 0) * C::Q_BYTES + c * 128 * ROWB;
-          const int qr0 = (PAIR ? wg_thread : (int)threadIdx.x - 128) / GROUP;
-#pragma unroll 4
-          for (int k = 0; k < 128 / STEP; ++k) {
-            const int qr = qr0 + k * STEP;
-            const int qt = row_token(p, row0 + qr), qg = (row0 + qr) - qt * p.group;
-            const int sw = (R::CH == 64) ? (uc ^ (qr & 7)) : (uc ^ ((qr >> 1) & 3));
-            if (qr < nrows && u < UNITS)
-              copy16(sq + qr * ROWB + sw * 16, src + (int64_t)qg * p.t.q.sh + (int64_t)qt * p.t.q.sn);
-          }
-        }
         // the row's mask words (drafted tokens it sees)
         uint32_t mrow[4];
 #pragma unroll
@@ -349,29 +364,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (p.t.tree_mask && live && i < p.mask_words)
             mrow[i] = (uint32_t)__ldg(p.t.tree_mask + ((int64_t)w.b * p.t.n + tok) * p.mask_words + i);
         }
-        // pages outside the pool (their tokens are not seen): looked up here
-        // once, and tile by tile only where there are any
-        bool bad_page = false;
-        {
-          const int c0 = (w.t0 * kTile) >> page_shift;
-          const int c1 = min((w.t1 * kTile) >> page_shift, (w.keys + (1 << page_shift) - 1) >> page_shift);
-          for (int c = c0 + wg_thread; c < c1; c += 128) bad_page |= !page_ok(p.t, __ldg(table + c));
-        }
-        copy16_wait();
-        fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          if (PAIR) {
-            mbar_arrive(&q_full[s]);
-          } else {
-            mbar_arrive(&q_full[0]);
-            if (w.t1 - w.t0 > 1) mbar_arrive(&q_full[1]);
-          }
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)  // tokens past the sequence's new ones, and rows of such
-          mrow[i] &= !live || w.nl <= 32 * i ? 0u : w.nl < 32 * i + 32 ? (1u << (w.nl - 32 * i)) - 1u : 0xffffffffu;
-        bad_page = bar_or(bar_id, bar_n, bad_page);
+        // word i of it without tokens past the sequence's new ones
+        auto sees = [&](int i) -> uint32_t {
+          return mrow[i] &
+                 (!live || w.nl <= 32 * i ? 0u : w.nl < 32 * i + 32 ? (1u << (w.nl - 32 * i)) - 1u : 0xffffffffu);
+        };
         float m_ref = -INFINITY, l = 0.f;
         int cnt = 0;
         const int nt = w.t1 - w.t0;
@@ -380,27 +377,31 @@ __global__ void __launch_bounds__(kThreads, 1)
           if (!ok) break;
           ++ne;
           if (!warp_on) {
+            if (PAIR && more && i + 1 == nt) load_q(wn);
             if (lane == 0) mbar_arrive(&p_full[s]);
             continue;
           }
           tc_fence_after();
+          // the stream's last S MMA of the segment has read Q: the next
+          // segment's comes in while this tile is worked on
+          if (PAIR && more && i + 1 == nt) load_q(wn);
+          const uint32_t bad = tile_bad<4>(ring, tau0 + (uint32_t)i, abort_flag);
           uint32_t v[4][32];
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) tmem_ld_x32(tS + cc * 32, v[cc]);
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) tmem_wait_ld(v[cc]);
           const int kb = (w.t0 + i) * kTile;
-          if (kb + kTile > w.len || bad_page) {
+          if (kb + kTile > w.len || bad != 0u) {
+            const uint32_t m[4] = {sees(0), sees(1), sees(2), sees(3)};
 #pragma unroll
             for (int cc = 0; cc < 4; ++cc) {
-              uint32_t see = seen32(mrow, kb + 32 * cc, w.len);
-              if (bad_page) {
-                // the pages of 32 tokens: one, or two of 16
-                const int c = (kb + 32 * cc) >> page_shift;
-                const int cols = (w.keys + (1 << page_shift) - 1) >> page_shift;
-                if (c < cols && !page_ok(p.t, __ldg(table + c))) see &= page_shift == 4 ? 0xffff0000u : 0u;
-                if (page_shift == 4 && c + 1 < cols && !page_ok(p.t, __ldg(table + c + 1))) see &= 0xffffu;
-              }
+              uint32_t see = seen32(m, kb + 32 * cc, w.len);
+              // the pages of 32 tokens: one, or two of 16; those outside the
+              // pool are not seen
+              const int box = (32 * cc) >> page_shift;
+              if ((bad >> box) & 1u) see &= page_shift == 4 ? 0xffff0000u : 0u;
+              if (page_shift == 4 && ((bad >> (box + 1)) & 1u)) see &= 0xffffu;
 #pragma unroll
               for (int q = 0; q < 32; ++q) v[cc][q] = ((see >> q) & 1u) ? v[cc][q] : __float_as_uint(-INFINITY);
             }
@@ -461,9 +462,12 @@ __global__ void __launch_bounds__(kThreads, 1)
           ++nfin;
           tc_fence_after();
         }
+        tau0 += (uint32_t)nt;
+        // before the results: S of the next segment is then there after them
+        if (PAIR && more) publish_q(wn);
         float w0 = 1.f, w1 = 0.f;  // weights of O_0 and O_1 (or of the stream's own O)
         if (!PAIR) {
-          float* st = stats + s * 256;
+          float* st = stats + (w.seg & 1) * 512 + s * 256;
           st[r] = m_ref;
           st[128 + r] = l;
           tc_fence_before();
@@ -471,7 +475,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (bar_or(bar_id, bar_n, !ok)) break;
         if (!PAIR) {
           tc_fence_after();
-          const float ma = stats[r], mb = stats[256 + r], la = stats[128 + r], lb = stats[256 + 128 + r];
+          if (more) load_q(wn);  // (both streams are done with Q)
+          const float* st = stats + (w.seg & 1) * 512;
+          const float ma = st[r], mb = st[256 + r], la = st[128 + r], lb = st[256 + 128 + r];
           float top = fmaxf(ma, mb);
           if (top == -INFINITY) top = 0.f;
           w0 = la == 0.f ? 0.f : fast_exp2((ma == -INFINITY ? 0.f : ma) - top);
@@ -489,7 +495,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           const float inv = (whole && !zero) ? 1.f / l : 1.f;
           const int pi = w.part();
           const uint32_t* seg_nf = nf + (w.seg % kNfRing) * 4;
-          const uint32_t back[4] = {mrow[0] & seg_nf[0], mrow[1] & seg_nf[1], mrow[2] & seg_nf[2], mrow[3] & seg_nf[3]};
+          const uint32_t back[4] = {sees(0) & seg_nf[0], sees(1) & seg_nf[1], sees(2) & seg_nf[2], sees(3) & seg_nf[3]};
           const bool nonfin = (back[0] | back[1] | back[2] | back[3]) != 0u;
           // without PAIR each stream writes half of the columns
           constexpr int NCOL = PAIR ? D : D / 2;
@@ -565,7 +571,10 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         tc_fence_before();
         if (threadIdx.x == 128) write_rec(p, part, w);
-      } while (w.next(p));
+        if (!more) break;
+        if (!PAIR) publish_q(wn);
+        w = wn;
+      }
     }
   }
 

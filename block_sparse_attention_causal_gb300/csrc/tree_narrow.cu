@@ -29,13 +29,13 @@ constexpr uint32_t kSmemLimit = 232448u - 6144u;  // leaves room for a waiting b
 template <int D, int N>
 struct NarrowCfg {
   static constexpr int NP = (N == 64) ? 1 : 2;  // P buffers
-  static constexpr uint32_t Q_BYTES = (uint32_t)N * D * 2u;
+  static constexpr uint32_t Q_BYTES = tile_bytes<D>(N);
   static constexpr uint32_t P_BYTES = (uint32_t)N * kTile * 2u;
-  static constexpr uint32_t KV_BYTES = (uint32_t)kTile * D * 2u;
+  static constexpr uint32_t KV_BYTES = tile_bytes<D>(kTile);
   static constexpr int NS_MAX = 12;
   static constexpr int NBAR = 12 + 3 * NS_MAX;
   // thr[N], ref[N], fac[N], res[N], offs[N], wmax[4][N], wsum[4][N]; seen[2][64][2]; words[128]; nf; barriers; words
-  static constexpr uint32_t SMALL = 14u * N * 4u + 2u * 64u * 8u + 128u * 4u + kNfRing * 16u + NBAR * 8u + 2u * NS_MAX * 4u + 40u * 4u;
+  static constexpr uint32_t SMALL = 14u * N * 4u + 2u * 64u * 8u + 128u * 4u + kNfRing * 16u + NBAR * 8u + (NS_MAX + kTileFlags) * 4u + 40u * 4u;
   static constexpr uint32_t FIXED = 2u * Q_BYTES + NP * P_BYTES + SMALL;
   static constexpr int NS_FIT = (int)((kSmemLimit - FIXED) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
@@ -45,7 +45,7 @@ struct NarrowCfg {
   static constexpr uint32_t OFF_SMALL = OFF_P + NP * P_BYTES;
   // the MMA's 128 rows of V^T read on past a tile of fewer dimensions; what
   // they find only reaches rows of O^T that nobody reads
-  static constexpr uint32_t OVER = (D == 64) ? 16384u : (D == 96) ? 8192u : 0u;
+  static constexpr uint32_t OVER = (D == 64) ? KV_BYTES : 0u;
   static constexpr uint32_t USED = OFF_SMALL + SMALL;
   static constexpr uint32_t SMEM_BYTES = USED > OFF_Q + OVER ? USED : OFF_Q + OVER;
   static_assert(SMEM_BYTES <= kSmemLimit, "shared memory");
@@ -118,7 +118,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   using C = NarrowCfg<D, N>;
   using R = RingCfg<D, C::NS>;
   constexpr int NS = C::NS, NP = C::NP;
-  constexpr uint32_t ROWB = R::ROWB;
   extern __shared__ __align__(1024) uint8_t smem[];
   float* thr = reinterpret_cast<float*>(smem + C::OFF_SMALL);  // [N] scores above it move the row's reference
   float* ref = thr + N;                                        // [N] the row's reference (log2 domain)
@@ -142,9 +141,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   ring.full = bars + 12;
   ring.empty = ring.full + C::NS_MAX;
   ring.guarded = ring.empty + C::NS_MAX;
-  ring.bad_boxes = reinterpret_cast<uint32_t*>(bars + C::NBAR);
-  ring.uses = ring.bad_boxes + C::NS_MAX;
-  uint32_t* misc = ring.uses + C::NS_MAX;
+  ring.uses = reinterpret_cast<uint32_t*>(bars + C::NBAR);
+  ring.flags = ring.uses + C::NS_MAX;
+  uint32_t* misc = ring.flags + kTileFlags;
   uint32_t* tmem_base_slot = misc;
   volatile int* abort_flag = reinterpret_cast<volatile int*>(misc + 1);
   int* scratch = reinterpret_cast<int*>(misc + 4);  // [8 + 12]
@@ -171,6 +170,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(&ring.guarded[i], 1);
       ring.uses[i] = 0u;
     }
+    for (int i = 0; i < kTileFlags; ++i) ring.flags[i] = 0u;
     *abort_flag = 0;
     fence_mbar_init();
   }
@@ -206,10 +206,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (elect_one()) {
         constexpr uint32_t IDESC_S = idesc_bf16_f32(128, N, 0, 0);
         constexpr uint32_t IDESC_O = idesc_bf16_f32(128, N, 1, 0);
-        const uint64_t ring_k = smem_desc(smem_u32(smem), 16, 8 * ROWB, R::SWZ);
-        const uint64_t ring_v = smem_desc(smem_u32(smem), kTile * ROWB, 8 * ROWB, R::SWZ);
-        const uint64_t q_desc = smem_desc(smem_u32(smem + C::OFF_Q), 16, 8 * ROWB, R::SWZ);
-        const uint64_t p_desc = smem_desc(smem_u32(smem + C::OFF_P), 16, 8 * 128, 2u);
+        const uint64_t ring_k = smem_desc(smem_u32(smem), 16, 8 * kRowBytes, kSwizzle128);
+        const uint64_t ring_v = smem_desc(smem_u32(smem), kTile * kRowBytes, 8 * kRowBytes, kSwizzle128);
+        const uint64_t q_desc = smem_desc(smem_u32(smem + C::OFF_Q), 16, 8 * kRowBytes, kSwizzle128);
+        const uint64_t p_desc = smem_desc(smem_u32(smem + C::OFF_P), 16, 8 * kRowBytes, kSwizzle128);
         const uint32_t dO = tbase + 2 * N;
         uint32_t ts = 0, tp = 0;  // tiles whose S and PV are issued
         bool more = true;         // tiles whose S is not
@@ -232,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t qd = q_desc + (uint64_t)(((ws.seg & 1) * C::Q_BYTES) >> 4);
 #pragma unroll
               for (int kk = 0; kk < D / 16; ++kk) {
-                const int c = kk / (R::CH / 16), wd = kk % (R::CH / 16);
-                umma_ss(tbase + (ts & 1) * N, kd + (uint64_t)((c * kTile * ROWB + wd * 32) >> 4),
-                        qd + (uint64_t)((c * N * ROWB + wd * 32) >> 4), IDESC_S, kk > 0);
+                const int c = kk / 4, wd = kk % 4;
+                umma_ss(tbase + (ts & 1) * N, kd + (uint64_t)((c * kTile * kRowBytes + wd * 32) >> 4),
+                        qd + (uint64_t)((c * N * kRowBytes + wd * 32) >> 4), IDESC_S, kk > 0);
               }
               umma_commit(&s_full[ts & 1]);
               umma_commit(&ring.empty[slot]);
@@ -257,7 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               const uint64_t pd = p_desc + (uint64_t)(((tp % NP) * C::P_BYTES) >> 4);
 #pragma unroll
               for (int kk = 0; kk < kTile / 16; ++kk)
-                umma_ss(dO, vd + (uint64_t)((kk * 16 * ROWB) >> 4),
+                umma_ss(dO, vd + (uint64_t)((kk * 16 * kRowBytes) >> 4),
                         pd + (uint64_t)(((kk / 4) * N * 128 + (kk % 4) * 32) >> 4), IDESC_O,
                         (p_at == wp.t0 && kk == 0) ? 0u : 1u);
               umma_commit(&ring.empty[slot]);
@@ -306,12 +306,9 @@ __global__ void __launch_bounds__(kThreads, 1)
           const int tok = row_token(p, r), g = r - tok * p.group, u0 = lane / ROWS * UNITS;
           const uint16_t* src = p.t.q.data + (int64_t)w.b * p.t.q.sb + ((int64_t)w.hk * p.group + g) * p.t.q.sh +
                                 (int64_t)tok * p.t.q.sn + u0 * 8;
-          uint8_t* row = sq + r * ROWB;
 #pragma unroll
           for (int i = 0; i < UNITS; ++i) {
-            const int u = u0 + i, c = u / (R::CH / 8), uc = u % (R::CH / 8);
-            const int sw = (R::CH == 64) ? (uc ^ (r & 7)) : (uc ^ ((r >> 1) & 3));
-            uint8_t* dst = row + c * N * ROWB + sw * 16;
+            uint8_t* dst = sq + unit_offset(N, r, u0 + i);
             if (r < p.rows) copy16(dst, src + i * 8);
             else *reinterpret_cast<uint4*>(dst) = make_uint4(0u, 0u, 0u, 0u);
           }
@@ -337,22 +334,13 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t tau = 0;
       bool ok = true;
       do {
-        const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
         const bool tail = w.t1 * kTile > w.len;
         uint32_t* sees = seen + (w.seg & 1) * 128;
         // the mask's words, one per thread (at most 64 tokens of two words)
         if (tail && p.t.tree_mask && tid < w.nl * p.mask_words)
           words[tid] = (uint32_t)__ldg(p.t.tree_mask + (int64_t)w.b * p.t.n * p.mask_words + tid);
-        // pages outside the pool (their tokens are not seen): looked up here
-        // once, and tile by tile only where there are any
-        bool bad_page = false;
-        {
-          const int c0 = (w.t0 * kTile) >> page_shift;
-          const int c1 = min((w.t1 * kTile) >> page_shift, (w.keys + (1 << page_shift) - 1) >> page_shift);
-          for (int c = c0 + tid; c < c1; c += 128) bad_page |= !page_ok(p.t, __ldg(table + c));
-        }
-        bad_page = bar_or(1, 128, bad_page);
         if (tail) {
+          bar_or(1, 128, false);
           // turned round: the rows that see each drafted token
           if (tid < w.nl) {
             const int j = tid;
@@ -387,7 +375,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < N; ++i) s[i] = 0u;
           }
           const int kb = t * kTile;
-          if (kb + kTile > w.len || bad_page) {
+          const uint32_t bad = tile_bad<1>(ring, tau, abort_flag);
+          if (kb + kTile > w.len || bad != 0u) {
             const int pos = kb + key;
             uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;
             if (pos >= w.len) {
@@ -395,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1)
               m0 = (pos < w.keys) ? sees[2 * j] : 0u;
               m1 = (pos < w.keys) ? sees[2 * j + 1] : 0u;
             }
-            if (bad_page && pos < w.keys && !page_ok(p.t, __ldg(table + (pos >> page_shift)))) m0 = m1 = 0u;
+            if ((bad >> (key >> page_shift)) & 1u) m0 = m1 = 0u;  // a page outside the pool
 #pragma unroll
             for (int i = 0; i < N; ++i)
               s[i] = (((i < 32 ? m0 : m1) >> (i & 31)) & 1u) ? s[i] : __float_as_uint(-INFINITY);
@@ -404,7 +393,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           bool over = head || !ok;
           if (!head) {
 #pragma unroll
-            for (int i = 0; i < N; ++i) over |= __uint_as_float(s[i]) * sl2 > thr[i];
+            for (int c = 0; c < N; c += 4) {
+              const float4 t4 = *reinterpret_cast<const float4*>(thr + c);
+              over |= __uint_as_float(s[c]) * sl2 > t4.x || __uint_as_float(s[c + 1]) * sl2 > t4.y ||
+                      __uint_as_float(s[c + 2]) * sl2 > t4.z || __uint_as_float(s[c + 3]) * sl2 > t4.w;
+            }
           }
           // (also the barrier between the tiles' uses of the small arrays)
           if (bar_or(1, 128, over)) {
@@ -462,10 +455,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ok = __all_sync(0xffffffffu, mbar_wait<1>(&p_empty[tau % NP], (tau / NP - 1) & 1, abort_flag, err));
           uint8_t* pk = p_key + (tau % NP) * C::P_BYTES;
 #pragma unroll
-          for (int i = 0; i < N; ++i) {
-            const float e = fast_exp2(fmaf(__uint_as_float(s[i]), sl2, -ref[i]));
-            l[i] += e;
-            *reinterpret_cast<uint16_t*>(pk + i * 128 + (p_col ^ ((i & 7) << 4))) = (uint16_t)pack_bf16x2(e, 0.f);
+          for (int c = 0; c < N; c += 16) {
+            // the references of 16 rows first: a load between the stores of P
+            // would wait for the store before it
+            float r[16];
+#pragma unroll
+            for (int i = 0; i < 16; i += 4) {
+              const float4 r4 = *reinterpret_cast<const float4*>(ref + c + i);
+              r[i] = r4.x, r[i + 1] = r4.y, r[i + 2] = r4.z, r[i + 3] = r4.w;
+            }
+#pragma unroll
+            for (int i = 0; i < 16; ++i) r[i] = fast_exp2(fmaf(__uint_as_float(s[c + i]), sl2, -r[i]));
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+              l[c + i] += r[i];
+              *reinterpret_cast<uint16_t*>(pk + (c + i) * 128 + (p_col ^ ((i & 7) << 4))) = (uint16_t)pack_bf16x2(r[i], 0.f);
+            }
           }
           fence_proxy_async();
           tc_fence_before();

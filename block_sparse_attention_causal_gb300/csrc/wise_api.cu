@@ -290,19 +290,19 @@ RowsView rows_view(const wise_rows* r) {
 }
 
 // View [n_pages, kv_heads * page, head_dim] of a pool; boxes of one page of one
-// head and 64 (128B swizzle) or 32 (64B swizzle, head_dim 96) columns.
+// head and 64 columns (of 96, the second box lies half outside and is filled
+// with zeros there).
 int encode_pages(CUtensorMap* m, const void* ptr, const wise_paged_cache* c) {
   auto enc = encoder();
   if (!enc) return WISE_ERR_CUDA;
-  const int ch = (c->head_dim == 96) ? 32 : 64;
   const cuuint64_t rows = (cuuint64_t)c->kv_heads * c->page;
   cuuint64_t dims[3] = {(cuuint64_t)c->head_dim, rows, (cuuint64_t)c->n_pages};
   cuuint64_t strides[2] = {(cuuint64_t)c->head_dim * 2, rows * c->head_dim * 2};
-  cuuint32_t box[3] = {(cuuint32_t)ch, (cuuint32_t)c->page, 1};
+  cuuint32_t box[3] = {64, (cuuint32_t)c->page, 1};
   cuuint32_t es[3] = {1, 1, 1};
   CUresult r = enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(ptr), dims, strides, box, es,
-                   CU_TENSOR_MAP_INTERLEAVE_NONE, ch == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-                   CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                   CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                   CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? WISE_OK : WISE_ERR_UNSUPPORTED;
 }
 
