@@ -362,13 +362,14 @@ struct Ring {
 
 // Pages of the CTA's tile `tile` that are not in the pool (bit i: page i of the
 // tile), as the producer found them. Its word names the tile, so that a reader
-// knows the word for its own; the ring holds far fewer than kTileFlags tiles.
+// knows the word for its own (nothing else hangs on it, so it needs no acquire:
+// that took 100 cycles a tile); the ring holds far fewer than kTileFlags tiles.
 constexpr int kTileFlags = 16;
 __device__ __forceinline__ uint32_t tile_word(uint32_t tile, uint32_t bad) { return ((tile + 1u) << 8) | bad; }
 template <int TAG>
 static __device__ __noinline__ uint32_t tile_bad_slow(const uint32_t* flag, uint32_t tile, volatile int* abort_flag) {
   for (;;) {
-    const uint32_t v = ld_acquire_smem(flag);
+    const uint32_t v = *reinterpret_cast<const volatile uint32_t*>(flag);
     if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
     if (*abort_flag) return 0u;
   }
@@ -378,7 +379,7 @@ static __device__ __noinline__ uint32_t tile_bad_slow(const uint32_t* flag, uint
 template <int TAG>
 __device__ __forceinline__ uint32_t tile_bad(const Ring& ring, uint32_t tile, volatile int* abort_flag) {
   const uint32_t* flag = &ring.flags[tile % kTileFlags];
-  const uint32_t v = ld_acquire_smem(flag);
+  const uint32_t v = *reinterpret_cast<const volatile uint32_t*>(flag);
   if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
   return tile_bad_slow<TAG>(flag, tile, abort_flag);
 }
@@ -419,7 +420,7 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
         flagged = true;
         if (lane == 0) atomicOr(err, kErrBadCache);
       }
-      if (lane == 0) st_release_smem(&ring.flags[(pos >> 1) % kTileFlags], tile_word(pos >> 1, bad));
+      if (lane == 0) *reinterpret_cast<volatile uint32_t*>(&ring.flags[(pos >> 1) % kTileFlags]) = tile_word(pos >> 1, bad);
       for (int kv = 0; kv < 2 && ok; ++kv, ++pos) {
         const int slot = (int)(pos % NS);
         if (pos >= (uint32_t)NS)
