@@ -658,6 +658,8 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
     pos = None if positions is None else _check_array("positions", positions, torch.int32, (b, n), dev)
     steps, rotary, flags = None, 0, 0
     if rope is not None:
+        if not isinstance(rope, Rope) or not isinstance(rope.steps, torch.Tensor):
+            raise ValueError("rope must be a Rope (see rope_frequencies)")
         rotary = 2 * rope.steps.numel()
         steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
         flags = _lib.WISE_ROPE_PAIRS if rope.pairs else 0

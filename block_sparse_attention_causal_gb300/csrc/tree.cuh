@@ -264,6 +264,10 @@ struct Walk {
 __device__ __forceinline__ void clear_rec(const TreeParams& p) {
   if (!p.by_unit) p.rec[blockIdx.x].parts = 0;
 }
+// No unit is joined (a CTA that cannot work).
+__device__ __forceinline__ void clear_recs(const TreeParams& p) {
+  for (int i = threadIdx.x; i < p.recs; i += blockDim.x) p.rec[i].parts = 0;
+}
 __device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const Walk& w) {
   if (w.t0 != 0) return;
   const bool cut = w.t1 < w.nt;
@@ -367,21 +371,27 @@ struct Ring {
 constexpr int kTileFlags = 16;
 __device__ __forceinline__ uint32_t tile_word(uint32_t tile, uint32_t bad) { return ((tile + 1u) << 8) | bad; }
 template <int TAG>
-static __device__ __noinline__ uint32_t tile_bad_slow(const uint32_t* flag, uint32_t tile, volatile int* abort_flag) {
+static __device__ __noinline__ uint32_t tile_bad_slow(const uint32_t* flag, uint32_t tile, volatile int* abort_flag,
+                                                      uint32_t* err) {
+  const uint64_t t0 = global_timer_ns();
   for (;;) {
     const uint32_t v = *reinterpret_cast<const volatile uint32_t*>(flag);
     if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
     if (*abort_flag) return 0u;
+    if (global_timer_ns() - t0 > kWaitLimitNs) {
+      *abort_flag = 1;
+      atomicOr(err, kErrTimeout);
+    }
   }
 }
 // (called once the tile's copies or MMAs were seen done, so the word is there
 // or a few cycles away)
 template <int TAG>
-__device__ __forceinline__ uint32_t tile_bad(const Ring& ring, uint32_t tile, volatile int* abort_flag) {
+__device__ __forceinline__ uint32_t tile_bad(const Ring& ring, uint32_t tile, volatile int* abort_flag, uint32_t* err) {
   const uint32_t* flag = &ring.flags[tile % kTileFlags];
   const uint32_t v = *reinterpret_cast<const volatile uint32_t*>(flag);
   if ((v >> 8) == (tile_word(tile, 0u) >> 8)) return v & 0xffu;
-  return tile_bad_slow<TAG>(flag, tile, abort_flag);
+  return tile_bad_slow<TAG>(flag, tile, abort_flag, err);
 }
 
 // The warp that loads the ring, page by page (whole warp; lane i issues the
@@ -473,7 +483,7 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ri
       const int slot = (int)(pos % NS);
       ok = __all_sync(0xffffffffu, wait_loaded<TAG>(ring.full, ring.uses, NS, pos, abort_flag, p.t.err));
       if (!ok) break;
-      const uint32_t bad = tile_bad<TAG>(ring, pos >> 1, abort_flag);
+      const uint32_t bad = tile_bad<TAG>(ring, pos >> 1, abort_flag, p.t.err);
       const int kb = t * kTile;
       uint8_t* v = ring.tiles + slot * C::KV_BYTES;
       if (bad != 0u || kb + kTile > w.len || w.keys == 0) {

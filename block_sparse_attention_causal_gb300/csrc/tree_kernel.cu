@@ -125,6 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
     grid_wait();
+    clear_recs(p);
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
     return;
   }
@@ -385,7 +386,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           // the stream's last S MMA of the segment has read Q: the next
           // segment's comes in while this tile is worked on
           if (PAIR && more && i + 1 == nt) load_q(wn);
-          const uint32_t bad = tile_bad<4>(ring, tau0 + (uint32_t)i, abort_flag);
+          const uint32_t bad = tile_bad<4>(ring, tau0 + (uint32_t)i, abort_flag, err);
           uint32_t v[4][32];
 #pragma unroll
           for (int cc = 0; cc < 4; ++cc) tmem_ld_x32(tS + cc * 32, v[cc]);
@@ -586,6 +587,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
 }
 
+// Whether a record names parts that exist. After a wait that ran out a CTA
+// leaves its records unwritten; what lies there must not be followed.
+__device__ __forceinline__ bool rec_ok(const TreeParams& p, const int4& ra, const int4& rb) {
+  return ra.x >= 2 && ra.y >= 0 && ra.z >= 0 && ra.x <= kTreeCtas - ra.z && ra.y < 2 * kTreeCtas && ra.w >= 0 &&
+         ra.w < p.t.cache.batch && rb.x >= 0 && rb.x < p.t.cache.kv_heads && rb.y >= 0 && rb.y < p.pairs;
+}
+
 // Joins the partial results of a row whose unit was cut, in the line's order,
 // whatever the order in which they were written. grid.x: join records, grid.y:
 // rows (kJoinWarps of them per block, or one whose parts the warps share).
@@ -604,7 +612,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
   const int4 rb = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rb.x;
   const int row = rb.y * 256 + r;
-  if (parts < 2 || r >= p.row_slots || row >= p.rows) return;
+  if (!rec_ok(p, ra, rb) || r >= p.row_slots || row >= p.rows) return;
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -705,7 +713,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
   const int4 rc = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rc.x;
   const int r = rb * 32 + lane, row = rc.y * 256 + r;
-  if (parts < 2 || rc.y * 256 + rb * 32 >= p.rows) return;
+  if (!rec_ok(p, ra, rc) || rc.y * 256 + rb * 32 >= p.rows) return;
   auto part_at = [&](int k) -> int64_t { return k == 0 ? first_part : 2 * (first_cta + k); };
   const float* st = p.part_s + r;
   const float4* po = reinterpret_cast<const float4*>(p.part_o) + (rb * (D / 4) + c4) * 32 + lane;

@@ -152,6 +152,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
   if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
     grid_wait();
+    clear_recs(p);
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
     return;
   }
@@ -375,7 +376,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int i = 0; i < N; ++i) s[i] = 0u;
           }
           const int kb = t * kTile;
-          const uint32_t bad = tile_bad<1>(ring, tau, abort_flag);
+          const uint32_t bad = tile_bad<1>(ring, tau, abort_flag, err);
           if (kb + kTile > w.len || bad != 0u) {
             const int pos = kb + key;
             uint32_t m0 = 0xffffffffu, m1 = 0xffffffffu;

@@ -65,6 +65,10 @@
  *   launch; eager launches and recorded ones draw from separate halves of the
  *   slots, so replays and eager calls on other streams can run side by side.
  *   One graph must not be replayed on two streams at once.
+ * - The paged-cache calls launch their kernels as programmatic dependents:
+ *   blocks may start, and set themselves up, while the kernel before them in
+ *   the stream still runs, and wait for it before they touch its memory. Later
+ *   work on the stream sees nothing of this.
  * - Argument, shape and alignment errors are reported before any launch and
  *   nothing is written. A failed launch returns WISE_ERR_CUDA. Kernel-side
  *   problems (a malformed support list or page table, a wait that timed out) are recorded in
@@ -492,7 +496,8 @@ size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, in
  *   scale      : 0 => 1/sqrt(head_dim).
  *   out_dtype  : WISE_BF16 or WISE_F32.
  *   o, lse     : [batch, heads, n, head_dim] dense, 16-byte aligned; float32
- *                [batch, heads, n] or NULL. Every row is written.
+ *                [batch, heads, n] or NULL. Every row is written. They must
+ *                not overlap the inputs.
  *   workspace  : wise_attn_tree_workspace bytes (device, 16-byte aligned;
  *                scratch, needs no initialisation). Calls that may run at the
  *                same time need workspaces of their own.

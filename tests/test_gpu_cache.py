@@ -266,6 +266,95 @@ def test_unseen_drafted_tokens_have_no_influence(bad):
             assert torch.isnan(lse[:, :, [2, 3]]).all() and torch.isnan(o[:, :, [2, 3]]).all()
 
 
+@pytest.mark.parametrize("n,h,hk", [(40, 4, 2), (70, 8, 2), (128, 1, 1), (20, 3, 1)],
+                         ids=lambda x: str(x))
+@pytest.mark.parametrize("bad", [np.nan, np.inf])
+def test_unseen_drafted_tokens_have_no_influence_on_wide_units(n, h, hk, bad):
+    """The same for units of 60 to 280 rows, drafted tokens over two tiles."""
+    rng = np.random.default_rng(n)
+    lengths, page, d, spoilt = [70, 250], 32, 128, n // 2
+    totals = [x + n for x in lengths]
+    table, n_pages = _table(rng, totals, page)
+    k, v = _pools(rng, hk, d, page, table, n_pages, totals)
+    sees = _tree(rng, 2, n, "tree")
+    sees[:, :, spoilt] = False
+    seen_by = [spoilt, n - 1]
+    sees[:, seen_by, spoilt] = True
+    mask = wise.pack_tree_mask(torch.from_numpy(sees).cuda())
+    q = _bf16(rng.standard_normal((2, h, n, d))).cuda()
+    want, want_lse = _check_attention(q, _cache(k, v, table, lengths), sees, lengths, None, table, mask=mask)
+    rest = [x for x in range(n) if x not in seen_by]
+    for pool in ("v", "k"):
+        kk, vv = k.clone(), v.clone()
+        for b in range(2):
+            pg, row = C.slot(table, b, lengths[b] + spoilt, page)
+            (vv if pool == "v" else kk)[pg, :, row, 77] = bad
+        o, lse = wise.tree_attention(q, _cache(kk, vv, table, lengths), tree_mask=mask, out_dtype=torch.float32)
+        wise.check_device()
+        assert torch.equal(o[:, :, rest], want[:, :, rest]) and torch.equal(lse[:, :, rest], want_lse[:, :, rest])
+        if pool == "v":
+            hit = o[:, :, seen_by, 77]
+            assert torch.isnan(hit).all() if np.isnan(bad) else (hit == bad).all()
+            other = [x for x in range(d) if x != 77]
+            assert torch.equal(o[:, :, seen_by][..., other], want[:, :, seen_by][..., other])
+        elif np.isnan(bad):
+            assert torch.isnan(lse[:, :, seen_by]).all() and torch.isnan(o[:, :, seen_by]).all()
+
+
+@pytest.mark.parametrize("n", [1, 9, 20, 40])
+def test_nan_in_a_committed_token_reaches_every_row(n):
+    rng = np.random.default_rng(n)
+    lengths, page, d, h, hk = [300], 64, 64, 8, 2
+    table, n_pages = _table(rng, [300 + n], page)
+    k, v = _pools(rng, hk, d, page, table, n_pages, [300 + n])
+    q = _bf16(rng.standard_normal((1, h, n, d))).cuda()
+    clean = wise.tree_attention(q, _cache(k, v, table, lengths))
+    pg, row = C.slot(table, 0, 200, page)
+    kk, vv = k.clone(), v.clone()
+    kk[pg, 1, row, 3] = float("nan")
+    o, lse = wise.tree_attention(q, _cache(kk, v, table, lengths))
+    assert torch.isnan(o[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
+    assert torch.equal(o[:, :4], clean[0][:, :4]) and torch.equal(lse[:, :4], clean[1][:, :4])
+    vv[pg, 0, row, 5] = float("inf")
+    o, lse = wise.tree_attention(q, _cache(k, vv, table, lengths))
+    wise.check_device()
+    assert (o[:, :4, :, 5] == float("inf")).all() and torch.equal(lse, clean[1])
+    assert torch.equal(o[:, 4:], clean[0][:, 4:]) and torch.isfinite(o[:, :4, :, :5]).all()
+
+
+def test_pools_past_32_bits():
+    """Pages whose elements lie past 2^32 in their pool."""
+    rng = np.random.default_rng(3)
+    page, d, hk, n = 128, 128, 2, 5
+    n_pages = (1 << 32) // (page * d * hk) + 8  # 8.6 GB a pool
+    k, v = (torch.empty((n_pages, hk, page, d), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    table = np.array([[n_pages - 1, n_pages - 3], [n_pages - 5, n_pages - 2]], np.int32)
+    lengths = [0, 0]
+    cache = wise.PagedCache(k, v, _i32(table), _i32(lengths))
+    x = _bf16(rng.standard_normal((2, hk, 200, d))).cuda()
+    y = _bf16(rng.standard_normal((2, hk, 200, d))).cuda()
+    wise.cache_append(cache, x, y)
+    cache.lengths = _i32([195, 195])
+    q = _bf16(rng.standard_normal((2, 4, n, d))).cuda()
+    o, lse = wise.tree_attention(q, cache, out_dtype=torch.float32)
+    # the same tokens in a small pool
+    small = np.array([[0, 1], [2, 3]], np.int32)
+    pools = [torch.zeros((4, hk, page, d), dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    near = wise.PagedCache(*pools, _i32(small), _i32([0, 0]))
+    wise.cache_append(near, x, y)
+    near.lengths = _i32([195, 195])
+    want, want_lse = wise.tree_attention(q, near, out_dtype=torch.float32)
+    assert torch.equal(o, want) and torch.equal(lse, want_lse)
+    path = _i32([[1, 4, -1], [0, 2, 3]])
+    for c in (cache, near):
+        c.lengths = wise.cache_accept(c, _i32([2, 3]), path)
+    wise.check_device()
+    for b in range(2):
+        for i in range(2):
+            assert torch.equal(k[int(table[b, i])], pools[0][2 * b + i]) or i == 1
+            assert torch.equal(v[int(table[b, i]), :, :72], pools[1][2 * b + i, :, :72])
+
+
 def test_strided_queries_and_given_buffers():
     rng = np.random.default_rng(17)
     lengths, page, d, n, h, hk = [70, 9], 32, 96, 5, 6, 3
