@@ -613,12 +613,12 @@ def _check_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
     return stream.cuda_stream
 
 
-def _empty(shape, dtype: torch.dtype, dev: int, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
+def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[torch.cuda.Stream]) -> torch.Tensor:
     """A new buffer; one for a call on another stream belongs to that stream."""
     if stream is None:
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
     with torch.cuda.stream(stream):
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return torch.empty(shape, dtype=dtype, device=device)
 
 
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
@@ -648,7 +648,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
         if q.shape[2] != n:
             raise ValueError("q and k must hold the same number of tokens")
         if q_out is None:
-            q_out = _empty((b, heads, n, d), torch.bfloat16, dev, stream)
+            q_out = _empty((b, heads, n, d), torch.bfloat16, q.device, stream)
             qo = q_out.data_ptr()
         else:
             qo = _check_array("q_out", q_out, torch.bfloat16, (b, heads, n, d), dev)
@@ -695,24 +695,32 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
     mask = None if tree_mask is None else _check_array("tree_mask", tree_mask, torch.int32, (b, n, (n + 31) // 32), dev)
     nbytes = lib.wise_attn_tree_workspace(desc, heads, n)
     if out is None:
-        out = _empty((b, heads, n, d), out_dtype, dev, stream)
+        out = _empty((b, heads, n, d), out_dtype, q.device, stream)
         o_ptr = out.data_ptr()
     else:
         o_ptr = _check_array("out", out, out_dtype, (b, heads, n, d), dev)
     lse_ptr = None
     if want_lse:
         if lse is None:
-            lse = _empty((b, heads, n), torch.float32, dev, stream)
+            lse = _empty((b, heads, n), torch.float32, q.device, stream)
             lse_ptr = lse.data_ptr()
         else:
             lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev)
-    if workspace is None:
-        workspace = _empty(nbytes, torch.uint8, dev, stream)
-    else:
+    own = 0
+    if workspace is not None:
         _check_bytes("workspace", workspace, nbytes, q.device)
-        nbytes = workspace.numel()
-    st = lib.wise_attn_tree(desc, heads, n, qr, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr, workspace.data_ptr(),
-                            nbytes, handle)
+        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel()
+    else:
+        # straight from torch's allocator, on the call's stream (a tensor would
+        # cost the host 3 us more): free again once the call is queued, for
+        # later work of the same stream
+        ws_ptr = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(nbytes, 16), handle)
+    try:
+        st = lib.wise_attn_tree(desc, heads, n, qr, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr, ws_ptr, nbytes,
+                                handle)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     _lib.check(st, "wise_attn_tree")
     return out, (lse if want_lse else None)
 
@@ -737,7 +745,7 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
         tokens = path.shape[1]
         path_ptr = _check_array("path", path, torch.int32, (b, tokens), dev)
     if new_lengths is None:
-        new_lengths = _empty(b, torch.int32, dev, stream)
+        new_lengths = _empty((b,), torch.int32, n_accepted.device, stream)
         out = new_lengths.data_ptr()
     else:
         out = _check_array("new_lengths", new_lengths, torch.int32, (b,), dev)
