@@ -7,6 +7,11 @@
 // same rows and are joined through TMEM at the end of a segment; more rows,
 // each stream has rows of its own and both use every key tile.
 //
+// Measured (one GB300): 256 rows of each of 8 key heads over 32K tokens of 128
+// (a drafted tree of 64, 34.4 GFLOP, 135 MB): 43.5 us. A key tile takes 3050
+// cycles: a stream's chain of S MMA (8 of 128 x 128 x 16 from shared memory),
+// softmax (1250 cycles) and PV, the other stream's in between.
+//
 // Warp roles (384 threads): 0 TMA, 1 guard of V, 2 MMA issue for both streams,
 // 4-7 softmax and results of stream 0 (one row per thread), 8-11 of stream 1.
 // TMEM: S_0 | S_1 | O_0 | O_1, P (bf16) written over S.

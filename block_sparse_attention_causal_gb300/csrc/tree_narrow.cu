@@ -10,6 +10,10 @@
 // the time in which its bytes arrive; rows-as-lanes tiles of 128 took longer
 // than the bytes (one warp worked, 128 scores in each of its lanes).
 //
+// Measured (one GB300): next tokens of 32 sequences of up to 8K, 32/8 heads of
+// 128, 657 MB: 105 us = 6.25 TB/s, 92 % of a copy's rate; one of 128K, 537 MB:
+// 84 us, 94 %. A short prompt's next token takes 9.8 us, latency throughout.
+//
 // The row maximum goes over threads here. It need not be exact: a row's
 // reference only moves when a score passes it by 2^8, so per tile a vote over
 // the block of four warps is enough, and only a segment's first tile and the

@@ -634,6 +634,60 @@ def test_two_streams_at_once():
         assert torch.equal(o, want[j % 2][0]) and torch.equal(lse, want[j % 2][1])
 
 
+def test_calls_on_given_streams_and_captured_forks():
+    """Every call on a stream of its own, in order by events, and the same
+    recorded into one graph whose branches run side by side."""
+    rng = np.random.default_rng(47)
+    lengths, page, d, h, hk, n = [200, 33], 32, 128, 8, 2, 5
+    totals = [x + n for x in lengths]
+    table, n_pages = _table(rng, totals, page)
+    k, v = _pools(rng, hk, d, page, table, n_pages, totals, fill=0.0)
+    x = [_bf16(rng.standard_normal((2, y, n, d))).cuda() for y in (hk, hk, h)]
+    other = _cache(k, v, table, lengths)
+    oq = _bf16(rng.standard_normal((2, h, 1, d))).cuda()
+    rope = wise.rope_frequencies(d)
+    kept, path = _i32([2, 3]), _i32([[0, 3, 0], [1, 2, 4]])
+
+    def work(cache, a, b):
+        """Append on one stream, attend on another (beside attention over
+        another cache on the first), accept on the first again."""
+        q = wise.cache_append(cache, x[0], x[1], q=x[2], rope=rope, stream=a)
+        b.wait_stream(a)
+        o, lse = wise.tree_attention(q, cache, stream=b)
+        o2, lse2 = wise.tree_attention(oq, other, stream=a)
+        a.wait_stream(b)
+        return [q, o, lse, o2, lse2, wise.cache_accept(cache, kept, path, stream=a)]
+
+    main = torch.cuda.current_stream()
+    cache = _cache(k, v, table, lengths)
+    want = work(cache, main, main)
+    want += [cache.k_pages, cache.v_pages]
+    torch.cuda.synchronize()
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    eager = _cache(k, v, table, lengths)
+    a.wait_stream(main)
+    got = work(eager, a, b)
+    torch.cuda.synchronize()
+    for u, w in zip(got + [eager.k_pages, eager.v_pages], want):
+        assert torch.equal(u, w)
+    again = _cache(k, v, table, lengths)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=a):
+        got = work(again, a, b)
+    for _ in range(3):
+        again.k_pages.copy_(k)
+        again.v_pages.copy_(v)
+        for u in got:
+            u.zero_()
+        graph.replay()
+        # eager calls on another stream meanwhile
+        side, side_lse = wise.tree_attention(oq, other, stream=b)
+        torch.cuda.synchronize()
+        for u, w in zip(got + [again.k_pages, again.v_pages, side, side_lse], want + [want[3], want[4]]):
+            assert torch.equal(u, w)
+    wise.check_device()
+
+
 # -------------------------------------------------------- entries that are bad
 
 def test_bad_entries_are_flagged_and_skipped():
