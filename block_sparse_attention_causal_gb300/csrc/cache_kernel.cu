@@ -56,14 +56,15 @@ __device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const 
 }
 
 // Bound by memory: each value is read and written once (a prompt of 32K tokens,
-// 32/8 heads of 128, 805 MB: 128 us = 6.28 TB/s, 93 % of a copy's rate).
+// 32/8 heads of 128, 805 MB: 121 us = 6.65 TB/s, 98 % of a copy's rate).
 //
 // One thread per (token, pair of chunks), walking the heads of q, k and v of
 // its token: the sines and cosines of its eight frequencies are computed once
 // per token. With few tokens the heads are spread over gridDim.y.
 // AHEAD heads are loaded before the first is stored (four where a thread has
-// that many: a prompt of 32K took 134 us with one, 128 us with four; with few
-// tokens the longer code costs more than it gives, 3.4 us against 3.1 us).
+// that many: a prompt of 32K took 134 us with one, 128 us with four, 140 us with
+// eight; with few tokens the longer code costs more than it gives, 3.4 us
+// against 3.1 us).
 template <int D, bool PAIRS, int AHEAD>
 __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
   constexpr int NP = D / 16;  // chunk pairs of a head
@@ -121,8 +122,11 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
       for (int f = 0; f < 8; ++f) {
         // the angle in turns modulo one, exact: the low 64 bits of the product
         const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(p.rope + 8 * c + f);
-        const float t = (float)(int32_t)(turn >> 32) * 0x1p-31f;  // in units of pi, [-1, 1]
-        sincospif(t, &sn[f], &cs[f]);
+        // in [-pi, pi], where the hardware's sine and cosine are off by at most
+        // 2^-21: 2^12 below the rounding of the keys to bf16
+        const float t = (float)(int32_t)(turn >> 32) * (6.28318530717958648f * 0x1p-32f);
+        sn[f] = __sinf(t);
+        cs[f] = __cosf(t);
       }
     }
 #pragma unroll
@@ -202,9 +206,13 @@ cudaError_t launch_append_d(const AppendLaunch& a, cudaStream_t stream) {
   const int64_t items = (int64_t)a.cache.batch * a.n * (D / 16);
   const int units = a.heads + 2 * a.cache.kv_heads;
   const int64_t blocks = (items + 255) / 256;
-  // heads are spread until the grid holds about a full GPU of threads
-  constexpr int64_t kFull = 152 * 8;
-  int64_t ny = kFull / blocks;
+  // Heads are spread until the grid holds a full GPU of threads, and on, as long
+  // as a thread keeps four of them, to 24 blocks per SM: three run at a time, and
+  // the fewer rounds they make the more of the last one is empty (a prompt of 32K:
+  // 128 us with 7 blocks per SM, 121 us with 20).
+  constexpr int64_t kFull = 152 * 8, kMany = 152 * 24;
+  int64_t ny = kMany / blocks < units / 4 ? kMany / blocks : units / 4;
+  if (ny < kFull / blocks) ny = kFull / blocks;
   ny = ny < 1 ? 1 : (ny > units ? units : ny);
   const dim3 grid((unsigned)blocks, (unsigned)ny);
   auto kernel = ny * 4 <= units ? (a.pairs ? append_kernel<D, true, 4> : append_kernel<D, false, 4>)

@@ -3,9 +3,9 @@
 Tolerances. A rounding to bf16 is off by at most 2^-8 of the value, one in
 fp32 by 2^-24.
  * append: one rounding to bf16 of a rotation taken in fp32. The angle is
-   reduced in whole numbers; its top 32 bits as fp32, the sine and cosine
-   (2 ulp) and the two products and their sum are off by less than 2^-20 of
-   |x| + |y|.
+   reduced in whole numbers; its top 32 bits as fp32 (2^-23), the sine and
+   cosine (2^-21.1 on [-pi, pi]) and the two products and their sum (2^-23)
+   are off by less than 2^-20 of |x| + |y|.
  * attention: the scores are exact products summed in fp32, off by at most
    e_s = (d + 8) 2^-24 * scale * sum |q k|, plus 2^-22 for the exponential;
    a weight is rounded to bf16 (2^-8), in the numerator and in the sum that
