@@ -17,7 +17,7 @@ __device__ __forceinline__ int64_t slot_offset(const CacheView& c, int b, int64_
     atomicOr(err, kErrBadCache);
     return -1;
   }
-  const int32_t pg = __ldg(c.page_table + (int64_t)b * c.max_pages + col);
+  const int32_t pg = c.page_table[(int64_t)b * c.max_pages + col];
   if (pg < 0 || (int64_t)pg >= c.n_pages) {
     atomicOr(err, kErrBadCache);
     return -1;
@@ -83,8 +83,8 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
   const bool rot = c < nrot;
   const int ca = (rot && !PAIRS) ? c * 8 : 2 * c * 8;
   const int cb = (rot && !PAIRS) ? (c + nrot) * 8 : ca + 8;
-  const int32_t len = __ldg(p.cache.lengths + b);
-  const int32_t nl = p.new_len ? __ldg(p.new_len + b) : p.n;
+  const int32_t len = p.cache.lengths[b];
+  const int32_t nl = p.new_len ? p.new_len[b] : p.n;
   if (len < 0 || nl < 0 || nl > p.n) atomicOr(p.err, kErrBadCache);
   const bool store = len >= 0 && i < nl;
   const int64_t dst = store ? slot_offset(p.cache, b, (int64_t)len + i, D, p.err) : -1;
@@ -111,17 +111,18 @@ __global__ void __launch_bounds__(256) append_kernel(const AppendLaunch p) {
         out[k] = (key ? p.cache.k_pages : p.cache.v_pages) + dst + hv * head_step;
       }
       if (out[k]) {
-        x[k].a = __ldg(reinterpret_cast<const uint4*>(src + ca));
-        x[k].b = __ldg(reinterpret_cast<const uint4*>(src + cb));
+        // past the L1 cache: each value is read once (through it a prompt of 32K takes 127 us)
+        x[k].a = __ldcg(reinterpret_cast<const uint4*>(src + ca));
+        x[k].b = __ldcg(reinterpret_cast<const uint4*>(src + cb));
       }
     }
     if (u0 == (int)blockIdx.y && rot) {
       // after the first loads are on their way
-      const int64_t pos = p.positions ? (int64_t)__ldg(p.positions + tok) : (int64_t)len + i;
+      const int64_t pos = p.positions ? (int64_t)p.positions[tok] : (int64_t)len + i;
 #pragma unroll
       for (int f = 0; f < 8; ++f) {
         // the angle in turns modulo one, exact: the low 64 bits of the product
-        const uint64_t turn = (uint64_t)pos * (uint64_t)__ldg(p.rope + 8 * c + f);
+        const uint64_t turn = (uint64_t)pos * (uint64_t)p.rope[8 * c + f];
         // in [-pi, pi], where the hardware's sine and cosine are off by at most
         // 2^-21: 2^12 below the rounding of the keys to bf16
         const float t = (float)(int32_t)(turn >> 32) * (6.28318530717958648f * 0x1p-32f);
@@ -156,8 +157,8 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptLaun
   const int per_seq = 2 * p.cache.kv_heads * chunks;
   const int b = blockIdx.y;
   const int x = blockIdx.x * blockDim.x + threadIdx.x;
-  const int32_t len = __ldg(p.cache.lengths + b);
-  int32_t na = __ldg(p.n_accepted + b);
+  const int32_t len = p.cache.lengths[b];
+  int32_t na = p.n_accepted[b];
   const int64_t room = ((int64_t)p.cache.max_pages << p.cache.page_shift) - len;
   if (len < 0 || na < 0 || na > p.path_tokens || na > room) {
     if (x == 0) atomicOr(p.err, kErrBadCache);
@@ -174,7 +175,7 @@ __global__ void __launch_bounds__(kAcceptThreads) accept_kernel(const AcceptLaun
     const int mine = i0 + threadIdx.x;
     int64_t f = -1, t = -1;
     if (mine < na) {
-      const int32_t src = __ldg(path + mine), prev = mine > 0 ? __ldg(path + mine - 1) : -1;
+      const int32_t src = path[mine], prev = mine > 0 ? path[mine - 1] : -1;
       if (src <= prev || src < mine) {
         atomicOr(p.err, kErrBadCache);
       } else if (src != mine) {  // else already in its place

@@ -10,7 +10,10 @@ namespace wise {
 // precedes them in the stream: a kernel that has triggered (grid_trigger) lets
 // the next one's blocks start and set themselves up while it still runs. Every
 // block calls grid_wait before its first access to global memory, which waits
-// until the kernels before it are complete and their writes visible.
+// until the kernels before it are complete and their writes visible. What those
+// may have written is loaded plainly, never with __ldg: that names data which
+// nothing writes while the kernel runs, so the compiler may move it above the
+// wait.
 template <class... P, class... A>
 inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                   const A&... args) {

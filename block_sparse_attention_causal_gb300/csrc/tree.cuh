@@ -71,8 +71,8 @@ __device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;
 // holds; true if nothing had to be clamped.
 __device__ __forceinline__ bool seq_counts(const TreeLaunch& t, int b, int& len, int& nl) {
   const int64_t cap = (int64_t)t.cache.max_pages << t.cache.page_shift;
-  const int64_t l0 = __ldg(t.cache.lengths + b);
-  const int n0 = t.new_len ? __ldg(t.new_len + b) : t.n;
+  const int64_t l0 = t.cache.lengths[b];
+  const int n0 = t.new_len ? t.new_len[b] : t.n;
   const int64_t l = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
   int n = n0 < 0 ? 0 : (n0 > t.n ? t.n : n0);
   if (l + n > cap) n = (int)(cap - l);
@@ -138,12 +138,15 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
   const int per = (batch + THREADS - 1) / THREADS;
   const int b_lo = min(batch, (int)threadIdx.x * per), b_hi = min(batch, b_lo + per);
   int mine = 0;
+  int last_len = 0, last_nl = 0;  // of sequence b_hi - 1 (most batches: the thread's only one)
+  bool good = true;
   for (int b = b_lo; b < b_hi; ++b) {
-    int len, nl, fl, ac;
-    if (!seq_counts(p.t, b, len, nl) && blockIdx.x == 0) atomicOr(p.t.err, kErrBadCache);
-    seq_tiles(p, len, nl, fl, ac);
+    int fl, ac;
+    good &= seq_counts(p.t, b, last_len, last_nl);
+    seq_tiles(p, last_len, last_nl, fl, ac);
     mine += seq_line(p, fl, ac);
   }
+  if (!good && blockIdx.x == 0) atomicOr(p.t.err, kErrBadCache);
   int before = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -170,8 +173,8 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
   if (x0 >= before && x0 < before + mine) {  // (x0 is the line's end without a part)
     int at = before;
     for (int b = b_lo; b < b_hi; ++b) {
-      int len, nl, fl, ac;
-      seq_counts(p.t, b, len, nl);
+      int len = last_len, nl = last_nl, fl, ac;
+      if (b + 1 < b_hi) seq_counts(p.t, b, len, nl);
       seq_tiles(p, len, nl, fl, ac);
       const int line = seq_line(p, fl, ac);
       if (x0 >= at && x0 < at + line) {
@@ -412,7 +415,7 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
     // the lanes hold 32 columns of the page table from `have` on, and the 32
     // after them, which are under way while these are used
     int have = w.t0 * boxes;
-    auto columns = [&](int c) -> int32_t { return c + lane <= last_page ? __ldg(table + c + lane) : -1; };
+    auto columns = [&](int c) -> int32_t { return c + lane <= last_page ? table[c + lane] : -1; };
     int32_t held = columns(have), ahead = columns(have + 32);
     for (int t = w.t0; ok && t < w.t1; ++t) {
       const int col = t * boxes;
@@ -536,7 +539,7 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ri
 // Row pointer of drafted token j's values in the pool, or null.
 __device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {
   const int64_t tok = (int64_t)len + j;
-  const int32_t pg = __ldg(t.cache.page_table + (int64_t)b * t.cache.max_pages + (tok >> t.cache.page_shift));
+  const int32_t pg = t.cache.page_table[(int64_t)b * t.cache.max_pages + (tok >> t.cache.page_shift)];
   if (!page_ok(t, pg)) return nullptr;
   return t.cache.v_pages + ((((int64_t)pg * t.cache.kv_heads + hk) << t.cache.page_shift) +
                             (tok & ((1 << t.cache.page_shift) - 1))) * d;

@@ -368,7 +368,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           mrow[i] = tok >= 32 * i + 31 ? 0xffffffffu : tok < 32 * i ? 0u : (2u << (tok - 32 * i)) - 1u;
           if (p.t.tree_mask) mrow[i] = 0u;
           if (p.t.tree_mask && live && i < p.mask_words)
-            mrow[i] = (uint32_t)__ldg(p.t.tree_mask + ((int64_t)w.b * p.t.n + tok) * p.mask_words + i);
+            mrow[i] = (uint32_t)p.t.tree_mask[((int64_t)w.b * p.t.n + tok) * p.mask_words + i];
         }
         // word i of it without tokens past the sequence's new ones
         auto sees = [&](int i) -> uint32_t {

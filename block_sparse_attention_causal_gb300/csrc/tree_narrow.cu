@@ -343,7 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t* sees = seen + (w.seg & 1) * 128;
         // the mask's words, one per thread (at most 64 tokens of two words)
         if (tail && p.t.tree_mask && tid < w.nl * p.mask_words)
-          words[tid] = (uint32_t)__ldg(p.t.tree_mask + (int64_t)w.b * p.t.n * p.mask_words + tid);
+          words[tid] = (uint32_t)p.t.tree_mask[(int64_t)w.b * p.t.n * p.mask_words + tid];
         if (tail) {
           bar_or(1, 128, false);
           // turned round: the rows that see each drafted token

@@ -614,6 +614,38 @@ def test_drafting_loop_replayed_from_a_graph():
     assert torch.equal(a[0].view(torch.int16), r[0].view(torch.int16)) and torch.equal(a[2], r[2])
 
 
+def test_lengths_handed_from_call_to_call():
+    """Each acceptance's lengths are the next call's, with no other kernel
+    between them, and share their lines with the lengths that were read before."""
+    rng = np.random.default_rng(53)
+    b, h, hk, d, page, steps = 5, 8, 2, 64, 16, 24
+    table, n_pages = _table(rng, [3 * steps] * b, page)
+    kept = _i32(rng.integers(0, 4, (steps, b)))
+    path = _i32([[0, 1, 2]] * b)
+    x = [[_bf16(rng.standard_normal((b, y, 3, d))).cuda() for y in (h, hk, hk)] for _ in range(steps)]
+    zero = torch.zeros((n_pages, hk, page, d), dtype=torch.bfloat16)
+    rope = wise.rope_frequencies(d)
+    results = []
+    for wait in (True, False):
+        lengths = _i32([[0] * b] + [[-1] * b] * steps)
+        cache = _cache(zero, zero, table, [0] * b)
+        outs = []
+        torch.cuda.synchronize()
+        for i, (q, k, v) in enumerate(x):
+            cache.lengths = lengths[i]
+            qr = wise.cache_append(cache, k, v, q=q, rope=rope)
+            outs.append(wise.tree_attention(qr, cache, new_len=kept[i]))
+            wise.cache_accept(cache, kept[i], path, new_lengths=lengths[i + 1])
+            if wait:
+                torch.cuda.synchronize()
+        wise.check_device()
+        assert torch.equal(lengths[1:], torch.cumsum(kept, 0).to(torch.int32))
+        results.append((outs, cache.k_pages, cache.v_pages))
+    for (o, lse), (o2, lse2) in zip(results[0][0], results[1][0]):
+        assert torch.equal(o, o2) and torch.equal(lse, lse2)
+    assert torch.equal(results[0][1], results[1][1]) and torch.equal(results[0][2], results[1][2])
+
+
 def test_two_streams_at_once():
     rng = np.random.default_rng(31)
     want, got, made = [], [], []
