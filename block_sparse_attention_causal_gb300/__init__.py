@@ -627,7 +627,8 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
                  stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
     """Write new tokens' keys and values [batch, kv_heads, n, head_dim] behind
     the committed tokens, the keys rotated by `rope`; with q [batch, heads, n,
-    head_dim], return the rotated queries too (dense, or in q_out). Tokens
+    head_dim], return the rotated queries too (dense, or in q_out, which may
+    not share memory with the inputs). Tokens
     i < new_len[b] (default: all n) go to slots lengths[b] + i; their
     positions are positions[b, i] (int32; default lengths[b] + i -- a drafted
     token's is lengths[b] + its depth). k, v and q may have any strides that
@@ -680,7 +681,8 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
     :func:`pack_tree_mask`; default: tokens 0 .. i, so n = 1 is a next token).
     The cache may have fewer heads than q (grouped-query attention). Returns
     (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None); rows that
-    see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf."""
+    see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf. out, lse
+    and workspace, if given, may not share memory with the inputs."""
     desc, dev = _check_cache(cache)
     handle = _check_stream(stream, dev)
     lib = _lib.load()
@@ -730,9 +732,10 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
     """Keep drafted tokens: the keys and values of new tokens path[b, i],
     i < n_accepted[b] (int32; strictly ascending; the rest of a row is not
-    read), move to slots lengths[b] + i. Without a path the first n_accepted[b] new tokens are
-    kept where they are. Returns the new lengths (int32 [batch], not
-    cache.lengths itself: assign them, or copy them in place)."""
+    read), move to slots lengths[b] + i. Without a path the first n_accepted[b]
+    new tokens are kept where they are. Returns the new lengths (int32 [batch];
+    new_lengths may not be cache.lengths or another input: assign them, or copy
+    them in place)."""
     desc, dev = _check_cache(cache)
     handle = _check_stream(stream, dev)
     lib = _lib.load()

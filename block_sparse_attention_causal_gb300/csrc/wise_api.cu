@@ -269,6 +269,12 @@ int check_rows(const wise_rows* r) {
   return aligned16(r->data) ? WISE_OK : WISE_ERR_ALIGNMENT;
 }
 
+// Whether two arrays of 32-bit words share memory (a null one: no).
+bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a && b && x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
+}
+
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
 
 CacheView cache_view(const wise_paged_cache* c) {
@@ -817,10 +823,12 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   if (st != WISE_OK) return st;
   if (!n_accepted || !new_lengths || path_tokens < 1 || path_tokens > kMaxCacheTokens) return WISE_ERR_INVALID_ARGUMENT;
   if (misaligned4(path) || misaligned4(n_accepted) || misaligned4(new_lengths)) return WISE_ERR_ALIGNMENT;
-  // a block may read lengths[b] after another has written new_lengths[b]
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(cache->lengths), a1 = reinterpret_cast<uintptr_t>(new_lengths);
-  const uintptr_t span = (uintptr_t)cache->batch * 4;
-  if (a0 < a1 + span && a1 < a0 + span) return WISE_ERR_INVALID_ARGUMENT;
+  // a block may read its inputs after another has written new_lengths[b]
+  const int64_t batch = cache->batch;
+  if (overlap(new_lengths, batch, cache->lengths, batch) || overlap(new_lengths, batch, n_accepted, batch) ||
+      overlap(new_lengths, batch, path, batch * path_tokens) ||
+      overlap(new_lengths, batch, cache->page_table, batch * cache->max_pages))
+    return WISE_ERR_INVALID_ARGUMENT;
   AcceptLaunch a;
   memset(&a, 0, sizeof(a));
   a.err = error_word();

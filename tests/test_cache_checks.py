@@ -110,6 +110,16 @@ def test_accept_arguments(lib):
         assert call(out=at) == E.WISE_ERR_INVALID_ARGUMENT
 
 
+def test_accept_refuses_results_over_its_inputs(lib):
+    # 2 sequences; a path of 4 tokens: 32 bytes
+    def call(out, na=1 << 16, path=1 << 17):
+        return lib.wise_cache_accept(_cache(), 4, path, na, out, None)
+    for out in (1 << 16, (1 << 16) + 4, (1 << 16) - 4, 1 << 17, (1 << 17) + 28, (1 << 17) - 4):
+        assert call(out) == E.WISE_ERR_INVALID_ARGUMENT
+    table = _cache().page_table
+    assert call(table) == E.WISE_ERR_INVALID_ARGUMENT and call(table + 4) == E.WISE_ERR_INVALID_ARGUMENT
+
+
 def test_status_text(lib):
     assert "cache" in lib.wise_status_str(E.WISE_ERR_BAD_CACHE).decode()
 
