@@ -33,8 +33,9 @@ struct TreeCfg {
   static constexpr int NS_MAX = 12;
   static constexpr int NBAR = 9 + 3 * NS_MAX;
   static constexpr uint32_t OFF_RING = (PAIR ? 2u : 1u) * Q_BYTES;
-  // stats[2][2][2][128]; nf; barriers; words
-  static constexpr uint32_t SMALL = 2u * 2u * 2u * 128u * 4u + kNfRing * 16u + NBAR * 8u + (NS_MAX + kTileFlags) * 4u + 40u * 4u;
+  static constexpr uint32_t STATS = PAIR ? 0u : 2u * 2u * 2u * 128u;
+  // stats; nf; barriers; words
+  static constexpr uint32_t SMALL = STATS * 4u + kNfRing * 16u + NBAR * 8u + (NS_MAX + kTileFlags) * 4u + 40u * 4u;
   static constexpr int NS_FIT = (int)((LIMIT - OFF_RING - SMALL) / KV_BYTES);
   static constexpr int NS = NS_FIT < NS_MAX ? NS_FIT : NS_MAX;
   static_assert(NS >= 4, "ring");
@@ -105,9 +106,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr bool PAIR = C::PAIR;
   constexpr int NS = C::NS;
   extern __shared__ __align__(1024) uint8_t smem[];
-  // [2][2][2][128] of even and odd segments, each stream: references and sums of its rows
+  // without PAIR: [2][2][2][128] of even and odd segments, each stream: references and sums of its rows
   float* stats = reinterpret_cast<float*>(smem + C::OFF_SMALL);
-  uint32_t* nf = reinterpret_cast<uint32_t*>(stats + 1024);  // [kNfRing][4]
+  uint32_t* nf = reinterpret_cast<uint32_t*>(stats + C::STATS);  // [kNfRing][4]
   uint64_t* bars = reinterpret_cast<uint64_t*>(nf + kNfRing * 4);
   uint64_t* q_full = bars;           // [2] Q of a segment in which stream s has tiles is in shared memory
   uint64_t* s_full = q_full + 2;     // [2] S_s computed
