@@ -8,9 +8,12 @@
 // each stream has rows of its own and both use every key tile.
 //
 // Measured (one GB300): 256 rows of each of 8 key heads over 32K tokens of 128
-// (a drafted tree of 64, 34.4 GFLOP, 135 MB): 43.5 us. A key tile takes 3050
-// cycles: a stream's chain of S MMA (8 of 128 x 128 x 16 from shared memory),
-// softmax (1250 cycles) and PV, the other stream's in between.
+// (a drafted tree of 64, 34.4 GFLOP, 135 MB): 43.2 us. A key tile takes 1.63 us
+// (1.33 at the rate of a large library product), bound by a stream's chain of S
+// MMA (8 of 128 x 128 x 16 from shared memory), softmax and PV, the other
+// stream's in between; the first one comes 6 us after the start, and the partial
+// results take 12 us out and through the join. Sixteen softmax warps, half a row
+// per thread, took 45.5 us (96 registers a thread are too few).
 //
 // Warp roles (384 threads): 0 TMA, 1 guard of V, 2 MMA issue for both streams,
 // 4-7 softmax and results of stream 0 (one row per thread), 8-11 of stream 1.
