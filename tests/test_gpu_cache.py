@@ -14,6 +14,10 @@ fp32 by 2^-24.
  * LSE: e_s, plus 2^-20 for the exponentials and the logarithm, plus 2^-24
    for every addition of the longest chain of the sum and of its value.
 """
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -612,6 +616,37 @@ def test_drafting_loop_replayed_from_a_graph():
     for (o, lse), (o2, lse2) in zip(eager, replayed):
         assert torch.equal(o, o2) and torch.equal(lse, lse2)
     assert torch.equal(a[0].view(torch.int16), r[0].view(torch.int16)) and torch.equal(a[2], r[2])
+
+
+FIRST_CALLS = """
+import torch
+import block_sparse_attention_causal_gb300 as wise
+heads, n, d = %d, 3, 128
+pool = torch.randn((8, 2, 16, d), device="cuda").bfloat16()
+cache = wise.PagedCache(pool, pool.clone(), torch.arange(8, dtype=torch.int32, device="cuda").reshape(1, 8),
+                        torch.tensor([40], dtype=torch.int32, device="cuda"))
+q = torch.randn((1, heads, n, d), device="cuda").bfloat16()
+k = torch.randn((1, 2, n, d), device="cuda").bfloat16()
+kept, rope = torch.tensor([2], dtype=torch.int32, device="cuda"), wise.rope_frequencies(d)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    rotated = wise.cache_append(cache, k, k, q=q, rope=rope)
+    o, lse = wise.tree_attention(rotated, cache)
+    lengths = wise.cache_accept(cache, kept)
+graph.replay()
+torch.cuda.synchronize()
+want = wise.tree_attention(rotated, cache)
+assert torch.equal(o, want[0]) and torch.equal(lse, want[1]) and lengths.tolist() == [42]
+wise.check_device()
+"""
+
+
+@pytest.mark.parametrize("heads", [8, 100])
+def test_a_process_s_first_calls_are_captured(heads):
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    done = subprocess.run([sys.executable, "-c", FIRST_CALLS % heads], cwd=root, capture_output=True, text=True, timeout=300)
+    assert done.returncode == 0, done.stderr
 
 
 def test_lengths_handed_from_call_to_call():
