@@ -444,8 +444,10 @@ typedef struct wise_rows {
  * for each pair (x, y) i < rotary_dim / 2 of a head's first rotary_dim values
  *     (x, y) -> (x cos a - y sin a, y cos a + x sin a),
  *     a = 2 pi frac(position * rope[i] / 2^64).
- * The angle is reduced in whole numbers, so it is exact to fp32 rounding at
- * any position. The products are taken in fp32 and rounded once to bf16.
+ * The angle is reduced in whole numbers, and its sine and cosine are each good
+ * to 2^-22 of their own value at any position. The products are taken in fp32
+ * and rounded once to bf16: a result is off by at most 2^-8 of itself and 2^-21
+ * of its two products' sizes, |x cos a| + |y sin a| (|y cos a| + |x sin a|).
  *   new_tokens : n, rows per sequence. n >= 1.
  *   k, v       : [batch, kv_heads, n, head_dim].
  *   heads, q, q_out : query heads and rows [batch, heads, n, head_dim]; q_out
