@@ -627,8 +627,8 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
                  stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
     """Write new tokens' keys and values [batch, kv_heads, n, head_dim] behind
     the committed tokens, the keys rotated by `rope`; with q [batch, heads, n,
-    head_dim], return the rotated queries too (dense, or in q_out, which may
-    not share memory with the inputs). Tokens
+    head_dim], return the rotated queries too (dense, or in q_out, which is
+    refused if it shares memory with the inputs or the cache). Tokens
     i < new_len[b] (default: all n) go to slots lengths[b] + i; their
     positions are positions[b, i] (int32; default lengths[b] + i -- a drafted
     token's is lengths[b] + its depth). k, v and q may have any strides that

@@ -269,10 +269,40 @@ int check_rows(const wise_rows* r) {
   return aligned16(r->data) ? WISE_OK : WISE_ERR_ALIGNMENT;
 }
 
-// Whether two arrays of 32-bit words share memory (a null one: no).
-bool overlap(const void* a, int64_t na, const void* b, int64_t nb) {
+// Whether [a, a + bytes_a) and [b, b + bytes_b) share memory (a null one: no).
+bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + (uintptr_t)nb * 4 && y < x + (uintptr_t)na * 4;
+  return a && b && x < y + (uintptr_t)bytes_b && y < x + (uintptr_t)bytes_a;
+}
+
+// Whether a dense array shares memory with any of the rows [batch, heads, n, d].
+// Rows may lie around it (a slice of a larger buffer), so only where it falls
+// between their first and last byte is each run of tokens looked at.
+bool overlap_rows(const wise_rows* r, int64_t batch, int64_t heads, int64_t n, int64_t d, const void* out, int64_t bytes) {
+  if (!r || !out) return false;
+  const uintptr_t first = reinterpret_cast<uintptr_t>(r->data), row = (uintptr_t)d * 2;
+  const uintptr_t sb = (uintptr_t)r->stride[0] * 2, sh = (uintptr_t)r->stride[1] * 2, sn = (uintptr_t)r->stride[2] * 2;
+  const uintptr_t lo = reinterpret_cast<uintptr_t>(out), hi = lo + (uintptr_t)bytes;
+  auto meets = [&](uintptr_t from, uintptr_t last) { return from < hi && lo < last + row; };
+  if (!meets(first, first + (batch - 1) * sb + (heads - 1) * sh + (n - 1) * sn)) return false;
+  for (int64_t b = 0; b < batch; ++b)
+    for (int64_t h = 0; h < heads; ++h) {
+      const uintptr_t from = first + b * sb + h * sh;
+      if (!meets(from, from + (n - 1) * sn)) continue;
+      // the first row that ends past the array's beginning
+      const uintptr_t at = sn == 0 || from + row > lo ? from : from + (lo - from - row) / sn * sn + sn;
+      if (at < hi) return true;
+    }
+  return false;
+}
+
+int64_t pool_bytes(const wise_paged_cache* c) { return c->n_pages * c->kv_heads * c->page * c->head_dim * 2; }
+
+// Whether an array lies over any part of a cache.
+bool overlap_cache(const wise_paged_cache* c, const void* out, int64_t bytes) {
+  return overlap(out, bytes, c->k_pages, pool_bytes(c)) || overlap(out, bytes, c->v_pages, pool_bytes(c)) ||
+         overlap(out, bytes, c->page_table, (int64_t)c->batch * c->max_pages * 4) ||
+         overlap(out, bytes, c->lengths, (int64_t)c->batch * 4);
 }
 
 bool misaligned4(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 3u) != 0; }
@@ -755,6 +785,16 @@ int wise_cache_append(const wise_paged_cache* cache, int32_t new_tokens, const w
   if ((q && !aligned16(q_out)) || misaligned4(new_len) || misaligned4(positions) ||
       (reinterpret_cast<uintptr_t>(rope) & 7u))
     return WISE_ERR_ALIGNMENT;
+  if (q) {
+    // threads write rows of q_out while others still read
+    const int64_t batch = cache->batch, d = cache->head_dim, bytes = batch * heads * new_tokens * d * 2;
+    if (overlap_cache(cache, q_out, bytes) || overlap_rows(q, batch, heads, new_tokens, d, q_out, bytes) ||
+        overlap_rows(k, batch, cache->kv_heads, new_tokens, d, q_out, bytes) ||
+        overlap_rows(v, batch, cache->kv_heads, new_tokens, d, q_out, bytes) ||
+        overlap(q_out, bytes, new_len, batch * 4) || overlap(q_out, bytes, positions, batch * new_tokens * 4) ||
+        overlap(q_out, bytes, rope, (int64_t)rotary_dim / 2 * 8))
+      return WISE_ERR_INVALID_ARGUMENT;
+  }
   AppendLaunch a;
   memset(&a, 0, sizeof(a));
   a.err = error_word();
@@ -825,9 +865,9 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   if (misaligned4(path) || misaligned4(n_accepted) || misaligned4(new_lengths)) return WISE_ERR_ALIGNMENT;
   // a block may read its inputs after another has written new_lengths[b]
   const int64_t batch = cache->batch;
-  if (overlap(new_lengths, batch, cache->lengths, batch) || overlap(new_lengths, batch, n_accepted, batch) ||
-      overlap(new_lengths, batch, path, batch * path_tokens) ||
-      overlap(new_lengths, batch, cache->page_table, batch * cache->max_pages))
+  if (overlap(new_lengths, batch * 4, cache->lengths, batch * 4) || overlap(new_lengths, batch * 4, n_accepted, batch * 4) ||
+      overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) ||
+      overlap(new_lengths, batch * 4, cache->page_table, batch * cache->max_pages * 4))
     return WISE_ERR_INVALID_ARGUMENT;
   AcceptLaunch a;
   memset(&a, 0, sizeof(a));

@@ -451,8 +451,9 @@ typedef struct wise_rows {
  *   new_tokens : n, rows per sequence. n >= 1.
  *   k, v       : [batch, kv_heads, n, head_dim].
  *   heads, q, q_out : query heads and rows [batch, heads, n, head_dim]; q_out
- *                dense, 16-byte aligned, not overlapping q. Every row of q is
- *                rotated. q NULL: heads and q_out are ignored.
+ *                dense, 16-byte aligned, not overlapping any other buffer of
+ *                the call (refused). Every row of q is rotated. q NULL: heads
+ *                and q_out are ignored.
  *   new_len    : [batch] int32 or NULL (n each): tokens i < new_len[b] are
  *                written; no other slot of the cache changes.
  *   positions  : [batch, n] int32 or NULL: lengths[b] + i.

@@ -120,6 +120,33 @@ def test_accept_refuses_results_over_its_inputs(lib):
     assert call(table) == E.WISE_ERR_INVALID_ARGUMENT and call(table + 4) == E.WISE_ERR_INVALID_ARGUMENT
 
 
+def test_append_refuses_rotated_queries_over_its_inputs(lib):
+    # 2 sequences, 3 tokens, 2 heads of 64 (128 bytes a row); queries, keys and
+    # values of a token side by side: 6 rows a token, 18 a sequence
+    at = 1 << 24
+
+    def call(out, heads=2, q=at, strides=(18 * 64, 64, 6 * 64), **more):
+        c = _cache(kp=1 << 20, vp=1 << 21, table=1 << 22, lengths=1 << 23)
+        r = [_rows(q + x * 128, strides) for x in (0, 2, 4)]
+        args = dict(dict(new_len=1 << 25, positions=1 << 26, rope=1 << 27), **more)
+        return lib.wise_cache_append(c, 3, r[1], r[2], heads, r[0], out, args["new_len"], args["positions"], args["rope"], 64,
+                                     0, None)
+    size = 2 * 2 * 3 * 128
+    pool = 8 * 2 * 16 * 64 * 2
+    for base, length in ((at, 36 * 128), (1 << 20, pool), (1 << 21, pool), (1 << 22, 32), (1 << 23, 16), (1 << 25, 16),
+                         (1 << 26, 32), (1 << 27, 256)):
+        for out in (base, base + length - 16, base - size + 16):
+            assert call(out) == E.WISE_ERR_INVALID_ARGUMENT, hex(out)
+    # every row of the three is found, and nothing between them: the second
+    # sequence's rows lie far behind, and each token's are 64 rows apart
+    for token in range(3):
+        for row in range(6):
+            for seq in range(2):
+                where = at + seq * (1 << 20) + token * 64 * 128 + row * 128
+                assert call(where + 112, strides=(1 << 19, 64, 64 * 64)) == E.WISE_ERR_INVALID_ARGUMENT
+                assert call(where - size + 16, strides=(1 << 19, 64, 64 * 64)) == E.WISE_ERR_INVALID_ARGUMENT
+
+
 def test_status_text(lib):
     assert "cache" in lib.wise_status_str(E.WISE_ERR_BAD_CACHE).decode()
 

@@ -77,3 +77,37 @@ def test_small_sines_and_cosines_keep_their_bits(base, pairs):
         for part, u, v in ((a, x * c, -y * s), (b, y * c, x * s)):
             want, size = u + v, np.abs(u) + np.abs(v)
             assert np.all(np.abs(got[..., part] - want) <= BF16 * np.abs(want) + (1 + BF16) * 2.0 ** -21 * size)
+
+
+# ---------------------------------------------------------- buffers that meet
+
+def test_append_refuses_results_over_its_buffers_and_takes_those_between():
+    b, h, hk, n, d, page = 2, 2, 1, 3, 64, 16
+    g = torch.Generator(device="cuda").manual_seed(5)
+    # one arena: the first sequence's rows, room for the rotated queries, the second's
+    rows, room = n * (h + 2 * hk) * d, b * h * n * d
+    arena = torch.randn((2 * (rows + room),), generator=g, device="cuda").bfloat16()
+    qkv = arena.as_strided((b, n, h + 2 * hk, d), (rows + room, (h + 2 * hk) * d, d, 1)).transpose(1, 2)
+    q, k, v = qkv[:, :h], qkv[:, h:h + hk], qkv[:, h + hk:]
+    rope = wise.rope_frequencies(d)
+
+    def cache():
+        pool = torch.zeros((2, hk, page, d), dtype=torch.bfloat16, device="cuda")
+        return wise.PagedCache(pool, pool.clone(), _i32([[0], [1]]), _i32([3, 0]))
+    plain, given = cache(), cache()
+    before = qkv.clone()
+    want = wise.cache_append(plain, k, v, q=q, rope=rope)
+    between = arena[rows:rows + room].view(b, h, n, d)
+    got = wise.cache_append(given, k, v, q=q, q_out=between, rope=rope)
+    assert got is between and torch.equal(got, want) and torch.equal(qkv, before)
+    assert torch.equal(plain.k_pages, given.k_pages) and torch.equal(plain.v_pages, given.v_pages)
+    for off in (0, rows - 8, rows + 8):
+        with pytest.raises(wise.WiseError):
+            wise.cache_append(given, k, v, q=q, q_out=arena[off:off + room].view(b, h, n, d), rope=rope)
+    dense = q.contiguous()
+    with pytest.raises(wise.WiseError):
+        wise.cache_append(given, k, v, q=dense, q_out=dense, rope=rope)
+    with pytest.raises(wise.WiseError):
+        wise.cache_append(given, k, v, q=q, q_out=given.k_pages.view(-1)[:room].view(b, h, n, d), rope=rope)
+    wise.check_device()
+    assert torch.equal(qkv, before) and torch.equal(plain.k_pages, given.k_pages)
