@@ -82,7 +82,7 @@ def test_small_sines_and_cosines_keep_their_bits(base, pairs):
 # ---------------------------------------------------------- buffers that meet
 
 def test_append_refuses_results_over_its_buffers_and_takes_those_between():
-    b, h, hk, n, d, page = 2, 2, 1, 3, 64, 16
+    b, h, hk, n, d, page = 2, 2, 1, 5, 64, 16
     g = torch.Generator(device="cuda").manual_seed(5)
     # one arena: the first sequence's rows, room for the rotated queries, the second's
     rows, room = n * (h + 2 * hk) * d, b * h * n * d
