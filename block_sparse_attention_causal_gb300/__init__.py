@@ -682,7 +682,8 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
     The cache may have fewer heads than q (grouped-query attention). Returns
     (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None); rows that
     see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf. out, lse
-    and workspace, if given, may not share memory with the inputs."""
+    and workspace, if given, are refused if they share memory with each other,
+    the inputs or the cache."""
     desc, dev = _check_cache(cache)
     handle = _check_stream(stream, dev)
     lib = _lib.load()

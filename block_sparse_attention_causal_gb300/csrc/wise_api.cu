@@ -834,6 +834,24 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
   if (!aligned16(o) || misaligned4(lse) || misaligned4(new_len) || misaligned4(tree_mask)) return WISE_ERR_ALIGNMENT;
   if (!workspace || workspace_bytes < wise_attn_tree_workspace(cache, heads, new_tokens)) return WISE_ERR_WORKSPACE;
   if (!aligned16(workspace)) return WISE_ERR_ALIGNMENT;
+  {
+    // results and partial results are written while other blocks still read
+    const int64_t batch = cache->batch, d = cache->head_dim, n = new_tokens, rows = batch * heads * n;
+    const struct {
+      const void* at;
+      int64_t bytes;
+    } outs[3] = {{o, rows * d * (out_dtype == WISE_F32 ? 4 : 2)},
+                 {lse, rows * 4},
+                 {workspace, (int64_t)wise_attn_tree_workspace(cache, heads, new_tokens)}};
+    for (int i = 0; i < 3; ++i) {
+      const void* at = outs[i].at;
+      const int64_t bytes = outs[i].bytes;
+      if (overlap_cache(cache, at, bytes) || overlap_rows(q, batch, heads, n, d, at, bytes) ||
+          overlap(at, bytes, new_len, batch * 4) || overlap(at, bytes, tree_mask, batch * n * ((n + 31) / 32) * 4) ||
+          overlap(at, bytes, outs[(i + 1) % 3].at, outs[(i + 1) % 3].bytes))
+        return WISE_ERR_INVALID_ARGUMENT;
+    }
+  }
   TreeLaunch t;
   memset(&t, 0, sizeof(t));
   t.err = error_word();

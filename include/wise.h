@@ -499,11 +499,11 @@ size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, in
  *   scale      : 0 => 1/sqrt(head_dim).
  *   out_dtype  : WISE_BF16 or WISE_F32.
  *   o, lse     : [batch, heads, n, head_dim] dense, 16-byte aligned; float32
- *                [batch, heads, n] or NULL. Every row is written. They must
- *                not overlap the inputs.
+ *                [batch, heads, n] or NULL. Every row is written.
  *   workspace  : wise_attn_tree_workspace bytes (device, 16-byte aligned;
  *                scratch, needs no initialisation). Calls that may run at the
  *                same time need workspaces of their own.
+ * o, lse and the workspace must not overlap each other or the inputs (refused).
  * Pages not in [0, n_pages) are not read (their tokens are not seen) and
  * flagged (WISE_ERR_BAD_CACHE), as are negative lengths, new_len outside
  * 0 .. n, and tokens past the page table. The sums of a long row are joined

@@ -147,6 +147,30 @@ def test_append_refuses_rotated_queries_over_its_inputs(lib):
                 assert call(where - size + 16, strides=(1 << 19, 64, 64 * 64)) == E.WISE_ERR_INVALID_ARGUMENT
 
 
+def test_tree_attention_refuses_results_over_its_buffers(lib):
+    # 2 sequences, 2 heads over 2, 3 tokens of 64 values (128 bytes a row): 1536 bytes of O, 48 of LSE
+    kp, vp, table, lengths, q, new_len, mask, o, lse, w = ((1 << 20) * x for x in range(1, 11))
+    ws = lib.wise_attn_tree_workspace(_cache(), 2, 3)
+    assert 16 < ws < 1 << 20
+
+    def call(**other):
+        a = dict(dict(o=o, lse=lse, w=w, dtype=0), **other)
+        return lib.wise_attn_tree(_cache(kp=kp, vp=vp, table=table, lengths=lengths), 2, 3, _rows(q, (6 * 64, 64, 128)),
+                                  new_len, mask, 0.0, a["dtype"], a["o"], a["lse"], a["w"], ws, None)
+    pool = 8 * 2 * 16 * 64 * 2
+    for base, length in ((kp, pool), (vp, pool), (table, 32), (lengths, 16), (q, 12 * 128), (new_len, 16), (mask, 32)):
+        for name, size, step in (("o", 12 * 128, 16), ("lse", 48, 4), ("w", ws, 16)):
+            for at in (base, base + length - 16, base - size + step):
+                assert call(**{name: at}) == E.WISE_ERR_INVALID_ARGUMENT, (name, hex(at))
+    for at in (o, o + 12 * 128 - 4, o - 44):
+        assert call(lse=at) == E.WISE_ERR_INVALID_ARGUMENT
+    assert call(dtype=1, lse=o + 24 * 128 - 4) == E.WISE_ERR_INVALID_ARGUMENT  # O of 32 bits: twice as long
+    for at in (w, w + ws - 16, w - 12 * 128 + 16):
+        assert call(o=at) == E.WISE_ERR_INVALID_ARGUMENT
+    for at in (w, w + ws - 4, w - 44):
+        assert call(lse=at) == E.WISE_ERR_INVALID_ARGUMENT
+
+
 def test_status_text(lib):
     assert "cache" in lib.wise_status_str(E.WISE_ERR_BAD_CACHE).decode()
 
