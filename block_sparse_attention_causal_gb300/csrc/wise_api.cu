@@ -298,6 +298,10 @@ bool overlap_rows(const wise_rows* r, int64_t batch, int64_t heads, int64_t n, i
 
 int64_t pool_bytes(const wise_paged_cache* c) { return c->n_pages * c->kv_heads * c->page * c->head_dim * 2; }
 
+// Whether a cache's keys and values share memory: calls that write them hand both
+// to different threads.
+bool pools_meet(const wise_paged_cache* c) { return overlap(c->k_pages, pool_bytes(c), c->v_pages, pool_bytes(c)); }
+
 // Whether an array lies over any part of a cache.
 bool overlap_cache(const wise_paged_cache* c, const void* out, int64_t bytes) {
   return overlap(out, bytes, c->k_pages, pool_bytes(c)) || overlap(out, bytes, c->v_pages, pool_bytes(c)) ||
@@ -785,6 +789,7 @@ int wise_cache_append(const wise_paged_cache* cache, int32_t new_tokens, const w
   if ((q && !aligned16(q_out)) || misaligned4(new_len) || misaligned4(positions) ||
       (reinterpret_cast<uintptr_t>(rope) & 7u))
     return WISE_ERR_ALIGNMENT;
+  if (pools_meet(cache)) return WISE_ERR_INVALID_ARGUMENT;
   if (q) {
     // threads write rows of q_out while others still read
     const int64_t batch = cache->batch, d = cache->head_dim, bytes = batch * heads * new_tokens * d * 2;
@@ -884,8 +889,8 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   // a block may read its inputs after another has written new_lengths[b]
   const int64_t batch = cache->batch;
   if (overlap(new_lengths, batch * 4, cache->lengths, batch * 4) || overlap(new_lengths, batch * 4, n_accepted, batch * 4) ||
-      overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) ||
-      overlap(new_lengths, batch * 4, cache->page_table, batch * cache->max_pages * 4))
+      overlap(new_lengths, batch * 4, cache->page_table, batch * cache->max_pages * 4) ||
+      overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) || pools_meet(cache))
     return WISE_ERR_INVALID_ARGUMENT;
   AcceptLaunch a;
   memset(&a, 0, sizeof(a));

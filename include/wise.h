@@ -401,7 +401,8 @@ int wise_support_jaccard(const wise_attn_desc* desc, const int32_t* row_ptr_a, c
  * A paged key/value cache (all pointers in device memory, owned by the
  * caller; no counterpart in the paper). Pools of pages hold `page` consecutive
  * tokens of one sequence for every key/value head:
- *   k_pages, v_pages : [n_pages, kv_heads, page, head_dim] bf16, dense;
+ *   k_pages, v_pages : [n_pages, kv_heads, page, head_dim] bf16, dense; calls
+ *                      that write them refuse pools that overlap;
  *   page_table       : [batch, max_pages] int32: token t of sequence b lies in
  *                      row t % page of page page_table[b][t / page]. Entries
  *                      past a sequence's last token are never read. Sequences
@@ -463,7 +464,8 @@ typedef struct wise_rows {
  *                are copied.
  *   flags      : WISE_ROPE_PAIRS or 0.
  * Two tokens of one call must not fall on one slot (sequences that are
- * appended to own their last page). Tokens that do not fit the page table, or
+ * appended to own their last page). k, v and q may lie in the pools (tokens
+ * copied from one page to another), in slots that the call does not write. Tokens that do not fit the page table, or
  * whose page is not in [0, n_pages), are skipped and flagged
  * (WISE_ERR_BAD_CACHE in the device word), as are negative lengths and
  * new_len outside 0 .. n. One launch.

@@ -171,6 +171,15 @@ def test_tree_attention_refuses_results_over_its_buffers(lib):
         assert call(lse=at) == E.WISE_ERR_INVALID_ARGUMENT
 
 
+def test_pools_that_share_memory_are_refused_where_they_are_written(lib):
+    pool = 8 * 2 * 16 * 64 * 2
+    for vp in (1 << 20, (1 << 20) + pool - 16, (1 << 20) - pool + 16):
+        c = _cache(kp=1 << 20, vp=vp, table=1 << 22, lengths=1 << 23)
+        assert lib.wise_cache_append(c, 3, _rows(1 << 24), _rows(1 << 25), 0, None, None, None, None, None, 0, 0, None) == \
+            E.WISE_ERR_INVALID_ARGUMENT
+        assert lib.wise_cache_accept(c, 4, 1 << 24, 1 << 25, 1 << 26, None) == E.WISE_ERR_INVALID_ARGUMENT
+
+
 def test_status_text(lib):
     assert "cache" in lib.wise_status_str(E.WISE_ERR_BAD_CACHE).decode()
 
