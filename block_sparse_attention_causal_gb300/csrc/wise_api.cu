@@ -888,8 +888,7 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   if (misaligned4(path) || misaligned4(n_accepted) || misaligned4(new_lengths)) return WISE_ERR_ALIGNMENT;
   // a block may read its inputs after another has written new_lengths[b]
   const int64_t batch = cache->batch;
-  if (overlap(new_lengths, batch * 4, cache->lengths, batch * 4) || overlap(new_lengths, batch * 4, n_accepted, batch * 4) ||
-      overlap(new_lengths, batch * 4, cache->page_table, batch * cache->max_pages * 4) ||
+  if (overlap_cache(cache, new_lengths, batch * 4) || overlap(new_lengths, batch * 4, n_accepted, batch * 4) ||
       overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) || pools_meet(cache))
     return WISE_ERR_INVALID_ARGUMENT;
   AcceptLaunch a;

@@ -525,7 +525,7 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
  *                lists parents first), or NULL: tokens stay where they are
  *                (new token i is kept as token i).
  *   n_accepted : [batch] int32, 0 .. path_tokens.
- *   new_lengths: [batch] int32; must not overlap the inputs.
+ *   new_lengths: [batch] int32; must not overlap the inputs or the pools (refused).
  * Entries not above the one before them or below their own place, or whose
  * slot does not fit the page table or lies in a page outside [0, n_pages), are
  * not moved and flagged (WISE_ERR_BAD_CACHE); counts outside their range are

@@ -180,6 +180,14 @@ def test_pools_that_share_memory_are_refused_where_they_are_written(lib):
         assert lib.wise_cache_accept(c, 4, 1 << 24, 1 << 25, 1 << 26, None) == E.WISE_ERR_INVALID_ARGUMENT
 
 
+def test_accept_refuses_new_lengths_in_the_pools(lib):
+    pool = 8 * 2 * 16 * 64 * 2
+    c = _cache(kp=1 << 20, vp=1 << 21, table=1 << 22, lengths=1 << 23)
+    for base in (1 << 20, 1 << 21):
+        for out in (base, base + pool - 4, base - 4):
+            assert lib.wise_cache_accept(c, 4, 1 << 24, 1 << 25, out, None) == E.WISE_ERR_INVALID_ARGUMENT
+
+
 def test_status_text(lib):
     assert "cache" in lib.wise_status_str(E.WISE_ERR_BAD_CACHE).decode()
 
