@@ -41,6 +41,7 @@ __all__ = ["discover", "select_support", "sparse", "Support", "device_status", "
 
 _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
 _BF16, _I32 = torch.bfloat16, torch.int32
+_MAX_I32 = (1 << 31) - 1  # the C ABI's counts are 32 bits wide, and ctypes cuts longer ones off
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream]) -> int:
@@ -570,6 +571,8 @@ def _check_cache(cache: PagedCache) -> Tuple[_lib.PagedCacheDesc, int]:
     shape = kp.shape
     n_pages, hk, page, d = shape
     b, max_pages = table.shape
+    if max_pages > _MAX_I32 or b > _MAX_I32 or max(shape) > _MAX_I32:
+        raise ValueError("the cache's axes must be shorter than 2^31")
     dev = kp.get_device()
     # everything at once (a call of a few microseconds notices each check); what
     # fails is named below
@@ -591,6 +594,8 @@ def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d:
     """The C view of rows [batch, heads, n, d] (any strides of the first three axes)."""
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
         raise ValueError(f"{name} must be a bfloat16 [batch, heads, tokens, head_dim] tensor")
+    if max(t.shape) > _MAX_I32:
+        raise ValueError(f"{name}'s axes must be shorter than 2^31")
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
     b, h, n, last = t.shape
@@ -659,7 +664,7 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
     pos = None if positions is None else _check_array("positions", positions, torch.int32, (b, n), dev)
     steps, rotary, flags = None, 0, 0
     if rope is not None:
-        if not isinstance(rope, Rope) or not isinstance(rope.steps, torch.Tensor):
+        if not isinstance(rope, Rope) or not isinstance(rope.steps, torch.Tensor) or rope.steps.numel() > _MAX_I32 // 2:
             raise ValueError("rope must be a Rope (see rope_frequencies)")
         rotary = 2 * rope.steps.numel()
         steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
@@ -747,6 +752,8 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
         if not isinstance(path, torch.Tensor) or path.dim() != 2 or path.shape[1] < 1:
             raise ValueError("path must be an int32 [batch, path_tokens] tensor")
         tokens = path.shape[1]
+        if tokens > _MAX_I32:
+            raise ValueError("path must be shorter than 2^31")
         path_ptr = _check_array("path", path, torch.int32, (b, tokens), dev)
     if new_lengths is None:
         new_lengths = _empty((b,), torch.int32, n_accepted.device, stream)

@@ -259,3 +259,17 @@ def test_row_checks():
         wise._check_array("new_len", torch.zeros(2, dtype=torch.int64), torch.int32, (2,), dev)
     with pytest.raises(ValueError, match="device"):
         wise._check_array("new_len", torch.zeros(2, dtype=torch.int32), torch.int32, (2,), dev)
+
+
+def test_axes_past_32_bits_are_refused():
+    """Not cut off to their low bits: 2^32 + 1 tokens are not one."""
+    long = (1 << 32) + 1
+    row = torch.zeros((1, 1, 1, 64), dtype=torch.bfloat16)
+    for shape in ((1, 1, long, 64), (1, long, 1, 64)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            wise._check_rows("k", row.expand(shape), 1, None, 64, -1)
+    pool = torch.zeros((1, 1, 16, 64), dtype=torch.bfloat16)
+    for table in ((1, long), (long, 1)):
+        c = wise.PagedCache(pool, pool.clone(), torch.empty(table, dtype=torch.int32, device="meta"), torch.zeros(1, dtype=torch.int32))
+        with pytest.raises(ValueError, match="2\\^31"):
+            wise._check_cache(c)
