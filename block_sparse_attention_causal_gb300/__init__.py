@@ -638,7 +638,8 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
     positions are positions[b, i] (int32; default lengths[b] + i -- a drafted
     token's is lengths[b] + its depth). k, v and q may have any strides that
     are multiples of 8 with a contiguous last axis. `lengths` does not
-    change: see :func:`cache_accept`."""
+    change: see :func:`cache_accept`. The new tensors of a call with `stream`
+    belong to that stream, as in the two calls below."""
     desc, dev = _check_cache(cache)
     handle = _check_stream(stream, dev)
     lib = _lib.load()
@@ -685,7 +686,9 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
     row i of tree_mask lists (int32 [batch, n, ceil(n / 32)], see
     :func:`pack_tree_mask`; default: tokens 0 .. i, so n = 1 is a next token).
     The cache may have fewer heads than q (grouped-query attention). Returns
-    (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None); rows that
+    (O [batch, heads, n, head_dim], LSE [batch, heads, n] or None), in
+    out_dtype (bfloat16 or float32; the softmax weights are rounded to bfloat16
+    in both) and float32; rows that
     see nothing, and rows i >= new_len[b], get O = 0 and LSE = -inf. out, lse
     and workspace, if given, are refused if they share memory with each other,
     the inputs or the cache."""

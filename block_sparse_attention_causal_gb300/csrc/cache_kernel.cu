@@ -85,7 +85,7 @@ __device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const 
 }
 
 // Bound by memory: each value is read and written once (a prompt of 32K tokens,
-// 32/8 heads of 128, 805 MB: 121 us = 6.65 TB/s, 98 % of a copy's rate).
+// 32/8 heads of 128, 805 MB: 121 us = 6.63 TB/s, 98 % of a copy's rate).
 //
 // One thread per (token, pair of chunks), walking the heads of q, k and v of
 // its token: the sines and cosines of its eight frequencies are computed once
@@ -95,7 +95,7 @@ __device__ __forceinline__ void rotate(ChunkPair& p, const float (&c)[8], const 
 // eight; with few tokens the longer code costs more than it gives, 3.4 us
 // against 3.1 us). The form with four is held to three blocks per SM: heads of 96
 // would otherwise take 92 registers and run two (2 x 4K tokens of 40 heads: 72.5 us
-// instead of 64.5).
+// instead of 64.5). The other form fits four.
 template <int D, bool PAIRS, int AHEAD>
 __global__ void __launch_bounds__(256, AHEAD == 4 ? 3 : 4) append_kernel(const AppendLaunch p) {
   constexpr int NP = D / 16;  // chunk pairs of a head

@@ -8,12 +8,14 @@
 // each stream has rows of its own and both use every key tile.
 //
 // Measured (one GB300): 256 rows of each of 8 key heads over 32K tokens of 128
-// (a drafted tree of 64, 34.4 GFLOP, 135 MB): 43.2 us. A key tile takes 1.63 us
+// (a drafted tree of 64, 34.4 GFLOP, 135 MB): 43.4 us. A key tile takes 1.63 us
 // (1.33 at the rate of a large library product), bound by a stream's chain of S
 // MMA (8 of 128 x 128 x 16 from shared memory), softmax and PV, the other
 // stream's in between; the first one comes 6 us after the start, and the partial
-// results take 12 us out and through the join. Sixteen softmax warps, half a row
-// per thread, took 45.5 us (96 registers a thread are too few).
+// results take 12 us out and through the join. The compiler spills 250 to 370
+// bytes a thread (a launch of 168 registers, 128 of them a softmax row's scores);
+// sixteen softmax warps, half a row per thread, took 45.5 us (96 registers a
+// thread are too few).
 //
 // Warp roles (384 threads): 0 TMA, 1 guard of V, 2 MMA issue for both streams,
 // 4-7 softmax and results of stream 0 (one row per thread), 8-11 of stream 1.
@@ -436,8 +438,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             resc = true;
           }
           const float m_use = (m_ref == -INFINITY) ? 0.f : m_ref;
-          // P = 2^(s scale log2e - m), rounded to bf16 for the tensor core;
-          // the sum is of the fp32 values
+          // P = 2^(s scale log2e - m), rounded to bf16 (2^-8) for the tensor core,
+          // whose operands are both of V's type; the sum is of the fp32 values.
+          // Against fp64, O is off by 0.0023 of its norm, 0.0017 of it from
+          // O's own rounding; twice the MMAs would be needed for weights of 16 bits.
           const uint64_t sc2 = f2_pack(sl2, sl2), nm2 = f2_pack(-m_use, -m_use);
           uint64_t rs2[2] = {0ull, 0ull};
 #pragma unroll
@@ -846,9 +850,10 @@ cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream
   p.pairs = (p.rows + 255) / 256;
   p.mask_words = (t.n + 31) / 32;
   p.scale_log2 = t.scale * 1.4426950408889634f;
-  // a change of units costs a wide unit about as much as six key tiles
-  // (128 KB of partial results out, Q in behind the loads of K and V), a narrow
-  // one about as much as one
+  // A change of units (results out, Q in, the pipeline filled again; 128 KB of
+  // partial results for a wide unit) counts as so many key tiles in the line.
+  // Measured: of 4, 6 and 8 places for wide units, and 0 to 3 for narrow ones, 8
+  // and 2 gave the shortest times.
   p.overhead = p.rows > 64 ? kWideOverhead : kNarrowOverhead;
   const WorkspaceLayout w = workspace_layout(t.cache.batch, t.cache.kv_heads, p.rows, t.head_dim);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(t.workspace) + 31) / 32 * 32);

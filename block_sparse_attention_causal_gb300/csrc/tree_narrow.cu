@@ -28,7 +28,9 @@ namespace wise {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr uint32_t kSmemLimit = 232448u - 6144u;  // leaves room for a waiting block of the join kernel
+// Leaves room for a waiting block of the join kernel (N of 16 and 32; with 64 the
+// registers leave none).
+constexpr uint32_t kSmemLimit = 232448u - 6144u;
 
 template <int D, int N>
 struct NarrowCfg {
@@ -455,7 +457,8 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_wait_st();
             }
           }
-          // P = 2^(s scale log2e - ref), rounded to bf16 for the tensor core
+          // P = 2^(s scale log2e - ref), rounded to bf16 (2^-8) for the tensor core,
+          // whose operands are both of V's type; the sum is of the fp32 values
           if (tau >= (uint32_t)NP)
             ok = __all_sync(0xffffffffu, mbar_wait<1>(&p_empty[tau % NP], (tau / NP - 1) & 1, abort_flag, err));
           uint8_t* pk = p_key + (tau % NP) * C::P_BYTES;

@@ -489,6 +489,8 @@ size_t wise_attn_tree_workspace(const wise_paged_cache* cache, int32_t heads, in
  * A row that sees nothing (an empty mask row behind an empty cache, or
  * i >= new_len[b]) gets O = 0 and LSE = -inf. Values of tokens that a row does
  * not see have no influence on it, whatever they are (infinities, NaN).
+ * Scores, maxima, sums and O are fp32, whatever out_dtype is; a softmax weight is
+ * rounded once to bf16 (2^-8 of itself) before it meets its value.
  *   heads      : query heads, a multiple of kv_heads (at most 4096 times);
  *                query head h reads key/value head h / (heads / kv_heads).
  *   new_tokens : n, 1 <= n <= 128 rows per sequence.
