@@ -269,10 +269,10 @@ int check_rows(const wise_rows* r) {
   return aligned16(r->data) ? WISE_OK : WISE_ERR_ALIGNMENT;
 }
 
-// Whether [a, a + bytes_a) and [b, b + bytes_b) share memory (a null one: no).
+// Whether [a, a + bytes_a) and [b, b + bytes_b) share memory (a null or empty one: no).
 bool overlap(const void* a, int64_t bytes_a, const void* b, int64_t bytes_b) {
   const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
-  return a && b && x < y + (uintptr_t)bytes_b && y < x + (uintptr_t)bytes_a;
+  return a && b && bytes_a > 0 && bytes_b > 0 && x < y + (uintptr_t)bytes_b && y < x + (uintptr_t)bytes_a;
 }
 
 // Whether a dense array shares memory with any of the rows [batch, heads, n, d].
@@ -889,7 +889,7 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   // a block may read its inputs after another has written new_lengths[b]
   const int64_t batch = cache->batch;
   if (overlap_cache(cache, new_lengths, batch * 4) || overlap(new_lengths, batch * 4, n_accepted, batch * 4) ||
-      overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) || pools_meet(cache))
+      overlap(new_lengths, batch * 4, path, batch * path_tokens * 4) || (path && pools_meet(cache)))
     return WISE_ERR_INVALID_ARGUMENT;
   AcceptLaunch a;
   memset(&a, 0, sizeof(a));

@@ -126,6 +126,24 @@ def test_append_refuses_results_over_its_buffers_and_takes_those_between():
     assert torch.equal(qkv, before) and torch.equal(plain.k_pages, given.k_pages)
 
 
+def test_one_pool_for_keys_and_values_is_read_but_not_written():
+    g = torch.Generator(device="cuda").manual_seed(6)
+    pool = torch.randn((4, 2, 16, 64), generator=g, device="cuda").bfloat16()
+    tied = wise.PagedCache(pool, pool, _i32([[2, 0], [1, 3]]), _i32([20, 5]))
+    apart = wise.PagedCache(pool, pool.clone(), tied.page_table, tied.lengths)
+    before = pool.clone()
+    q = torch.randn((2, 4, 2, 64), generator=g, device="cuda").bfloat16()
+    for got, want in zip(wise.tree_attention(q, tied), wise.tree_attention(q, apart)):
+        assert torch.equal(got, want)
+    assert wise.cache_accept(tied, _i32([2, 0])).tolist() == [22, 5]  # moves nothing
+    with pytest.raises(wise.WiseError):
+        wise.cache_accept(tied, _i32([2, 0]), _i32([[0, 1], [0, 0]]))
+    with pytest.raises(wise.WiseError):
+        wise.cache_append(tied, q[:, :2], q[:, 2:])
+    wise.check_device()
+    assert torch.equal(pool, before)
+
+
 # ---------------------------------------------------------------- attention
 
 def _paged(g, totals, hk, d, page, spare_cols=1, spare_pages=2):
