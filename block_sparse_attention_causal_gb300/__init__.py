@@ -16,7 +16,11 @@ Language Models" (WISE):
 * :func:`cache_append`, :func:`tree_attention`, :func:`cache_accept` -- what
   follows the prompt: a paged cache of keys and values, attention of a next
   token or of a tree of drafted tokens over it, and the drafted tokens that
-  are kept.
+  are kept;
+* :func:`norm_rotate`, and the norms and axes of :func:`cache_append` --
+  queries and keys normed per head and rotated in one pass;
+* :func:`cache_weights`, :func:`cache_evict` -- the attention weight that a
+  cache's tokens gather, and the cache cut down to the heaviest.
 
 Torch tensors supply device memory and the stream; every computation runs in
 the library's CUDA kernels. There is no CPU path: without the compiled
@@ -37,7 +41,8 @@ __all__ = ["discover", "select_support", "sparse", "Support", "device_status", "
            "select_finalize", "new_select_state",
            "WISE_SUPPORT_SINK", "WISE_SUPPORT_DIAG", "useful_flops", "dense_flops", "retained_mass",
            "support_jaccard", "select_control", "gather_plan", "PagedCache", "Rope", "rope_frequencies",
-           "pack_tree_mask", "cache_append", "tree_attention", "cache_accept"]
+           "pack_tree_mask", "cache_append", "tree_attention", "cache_accept", "norm_rotate", "cache_weights",
+           "cache_evict"]
 
 _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
 _BF16, _I32 = torch.bfloat16, torch.int32
@@ -519,15 +524,19 @@ class Rope:
     the rotation of pair i per position in units of 2^-64 turn (int64, modulo
     2^64), so that the angle of any position is reduced exactly; build it with
     :func:`rope_frequencies`. pairs: rotate neighbouring values instead of the
-    two halves."""
+    two halves. axes (int32, one entry per pair): positions have several axes
+    (time, row and column of an image), and pair i turns with axis axes[i]."""
     steps: torch.Tensor
     pairs: bool = False
+    axes: Optional[torch.Tensor] = None
 
 
 def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, inv_freq: Optional[Sequence[float]] = None,
-                     pairs: bool = False, device="cuda") -> Rope:
+                     pairs: bool = False, sections: Optional[Sequence[int]] = None, device="cuda") -> Rope:
     """The Rope of `rotary_dim` values with frequencies base^(-2i / rotary_dim),
-    or with the rotary_dim / 2 frequencies `inv_freq` (radians per position)."""
+    or with the rotary_dim / 2 frequencies `inv_freq` (radians per position).
+    sections: positions of several axes; the first sections[0] pairs turn with
+    axis 0, the next sections[1] with axis 1, and so on."""
     if rotary_dim < 0 or rotary_dim % 16 != 0:
         raise ValueError("rotary_dim must be a non-negative multiple of 16")
     if inv_freq is None:
@@ -537,7 +546,12 @@ def rope_frequencies(rotary_dim: int, base: float = 10000.0, *, inv_freq: Option
         raise ValueError("inv_freq must hold rotary_dim / 2 finite frequencies")
     steps = [int(round(f / (2.0 * math.pi) * 2.0 ** 64)) % (1 << 64) for f in freq]
     steps = [x - (1 << 64) if x >> 63 else x for x in steps]
-    return Rope(torch.tensor(steps, dtype=torch.int64, device=device), pairs)
+    axes = None
+    if sections is not None:
+        if not sections or any(x < 0 for x in sections) or sum(sections) != rotary_dim // 2:
+            raise ValueError("sections must be non-negative and sum to rotary_dim / 2")
+        axes = torch.tensor([a for a, x in enumerate(sections) for _ in range(x)], dtype=torch.int32, device=device)
+    return Rope(torch.tensor(steps, dtype=torch.int64, device=device), pairs, axes)
 
 
 def pack_tree_mask(mask: torch.Tensor) -> torch.Tensor:
@@ -626,9 +640,57 @@ def _empty(shape, dtype: torch.dtype, device: torch.device, stream: Optional[tor
         return torch.empty(shape, dtype=dtype, device=device)
 
 
+def _check_rope(rope: Rope, dev: int) -> Tuple[int, int, int]:
+    """Address of a rotation's steps, its rotary_dim and flags."""
+    if not isinstance(rope, Rope) or not isinstance(rope.steps, torch.Tensor) or rope.steps.numel() > _MAX_I32 // 2:
+        raise ValueError("rope must be a Rope (see rope_frequencies)")
+    rotary = 2 * rope.steps.numel()
+    steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
+    return steps, rotary, _lib.WISE_ROPE_PAIRS if rope.pairs else 0
+
+
+def _check_positions(rope: Optional[Rope], positions: Optional[torch.Tensor], batch: int, n: int, dev: int):
+    """The C descriptor of a rotation (or None) and the address of its positions (or None)."""
+    axes, n_axes, shape = None, 1, (batch, n)
+    if rope is None:
+        if positions is not None:
+            _check_array("positions", positions, torch.int32, shape, dev)
+        return None, None
+    steps, rotary, flags = _check_rope(rope, dev)
+    if rope.axes is not None:
+        axes = _check_array("rope.axes", rope.axes, torch.int32, (rotary // 2,), dev)
+        if not isinstance(positions, torch.Tensor) or positions.dim() != 3 or not 1 <= positions.shape[0] <= _MAX_I32:
+            raise ValueError("a rope with axes needs positions [axes, batch, n]")
+        n_axes = positions.shape[0]
+        shape = (n_axes, batch, n)
+    pos = None if positions is None else _check_array("positions", positions, torch.int32, shape, dev)
+    return _lib.RopeDesc(steps, axes, rotary, n_axes, flags, 0), pos
+
+
+def _check_norms(q_norm: Optional[torch.Tensor], heads: int, k_norm: Optional[torch.Tensor], kv_heads: int, d: int, eps: float,
+                 dev: int):
+    """The C descriptor of the norms, or None."""
+    if q_norm is None and k_norm is None:
+        return None
+    at, step, kind = [None, None], [0, 0], None
+    for i, (name, w, h) in enumerate((("q_norm", q_norm, heads), ("k_norm", k_norm, kv_heads))):
+        if w is None:
+            continue
+        if not isinstance(w, torch.Tensor) or w.dtype not in _OUT or kind not in (None, w.dtype):
+            raise ValueError("q_norm and k_norm must be bfloat16 or float32, both of one type")
+        kind = w.dtype
+        per_head = w.dim() == 2
+        at[i] = _check_array(name, w, kind, (h, d) if per_head else (d,), dev)
+        step[i] = d if per_head else 0
+    if not (isinstance(eps, (int, float)) and 0.0 < eps < math.inf):
+        raise ValueError("norm_eps must be positive and finite")
+    return _lib.HeadNorm(at[0], at[1], step[0], step[1], _OUT[kind], eps)
+
+
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Optional[torch.Tensor] = None,
                  q_out: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
                  positions: Optional[torch.Tensor] = None, rope: Optional[Rope] = None,
+                 q_norm: Optional[torch.Tensor] = None, k_norm: Optional[torch.Tensor] = None, norm_eps: float = 1e-6,
                  stream: Optional[torch.cuda.Stream] = None) -> Optional[torch.Tensor]:
     """Write new tokens' keys and values [batch, kv_heads, n, head_dim] behind
     the committed tokens, the keys rotated by `rope`; with q [batch, heads, n,
@@ -662,15 +724,18 @@ def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Opti
     elif q_out is not None:
         raise ValueError("q_out without q")
     nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
-    pos = None if positions is None else _check_array("positions", positions, torch.int32, (b, n), dev)
-    steps, rotary, flags = None, 0, 0
-    if rope is not None:
-        if not isinstance(rope, Rope) or not isinstance(rope.steps, torch.Tensor) or rope.steps.numel() > _MAX_I32 // 2:
-            raise ValueError("rope must be a Rope (see rope_frequencies)")
-        rotary = 2 * rope.steps.numel()
-        steps = _check_array("rope.steps", rope.steps, torch.int64, (rotary // 2,), dev)
-        flags = _lib.WISE_ROPE_PAIRS if rope.pairs else 0
-    st = lib.wise_cache_append(desc, n, kr, vr, heads, qr, qo, nl, pos, steps, rotary, flags, handle)
+    if q_norm is None and k_norm is None and (rope is None or getattr(rope, "axes", None) is None):
+        pos = None if positions is None else _check_array("positions", positions, torch.int32, (b, n), dev)
+        steps, rotary, flags = None, 0, 0
+        if rope is not None:
+            steps, rotary, flags = _check_rope(rope, dev)
+        st = lib.wise_cache_append(desc, n, kr, vr, heads, qr, qo, nl, pos, steps, rotary, flags, handle)
+    else:
+        if q_norm is not None and q is None:
+            raise ValueError("q_norm without q")
+        rd, pos = _check_positions(rope, positions, b, n, dev)
+        norm = _check_norms(q_norm, heads, k_norm, hk, d, norm_eps, dev)
+        st = lib.wise_cache_append_norm(desc, n, kr, vr, heads, qr, qo, nl, pos, rd, norm, handle)
     _lib.check(st, "wise_cache_append")
     return q_out
 
@@ -766,6 +831,139 @@ def cache_accept(cache: PagedCache, n_accepted: torch.Tensor, path: Optional[tor
     st = lib.wise_cache_accept(desc, tokens, path_ptr, na, out, handle)
     _lib.check(st, "wise_cache_accept")
     return new_lengths
+
+
+def norm_rotate(q: torch.Tensor, k: Optional[torch.Tensor] = None, *, q_norm: Optional[torch.Tensor] = None,
+                k_norm: Optional[torch.Tensor] = None, norm_eps: float = 1e-6, positions: Optional[torch.Tensor] = None,
+                rope: Optional[Rope] = None, q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Tuple[torch.Tensor, Optional[torch.Tensor]]:
+    """Queries [batch, heads, n, head_dim] and keys [batch, kv_heads, n,
+    head_dim] as :func:`discover` and :func:`sparse` take them, normed per head
+    and rotated as in :func:`cache_append`; positions are positions[b, i]
+    (int32; default i), or positions[a, b, i] with rope.axes. q and k may have
+    any strides that are multiples of 8 with a contiguous last axis. Returns
+    (q, k), dense, in q_out and k_out if given, which are refused if they share
+    memory with each other or the inputs."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 4:
+        raise ValueError("q must be a bfloat16 [batch, heads, tokens, head_dim] tensor")
+    _check_device("q", q)
+    dev = q.get_device()
+    handle = _check_stream(stream, dev)
+    lib = _lib.load()
+    b, heads, n, d = q.shape
+    if b < 1 or heads < 1:
+        raise ValueError("q must not be empty")
+    qr = _check_rows("q", q, b, None, d, dev)
+    if q_out is None:
+        q_out = _empty((b, heads, n, d), torch.bfloat16, q.device, stream)
+        qo = q_out.data_ptr()
+    else:
+        qo = _check_array("q_out", q_out, torch.bfloat16, (b, heads, n, d), dev)
+    kr, ko, hk = None, None, 0
+    if k is not None:
+        kr = _check_rows("k", k, b, None, d, dev)
+        hk = k.shape[1]
+        if k.shape[2] != n or hk < 1:
+            raise ValueError("k must hold as many tokens as q, and a head")
+        if k_out is None:
+            k_out = _empty((b, hk, n, d), torch.bfloat16, q.device, stream)
+            ko = k_out.data_ptr()
+        else:
+            ko = _check_array("k_out", k_out, torch.bfloat16, (b, hk, n, d), dev)
+    elif k_norm is not None or k_out is not None:
+        raise ValueError("k_norm or k_out without k")
+    rd, pos = _check_positions(rope, positions, b, n, dev)
+    norm = _check_norms(q_norm, heads, k_norm, hk, d, norm_eps, dev)
+    st = lib.wise_norm_rotate(b, n, d, heads, qr, qo, hk, kr, ko, pos, rd, norm, handle)
+    _lib.check(st, "wise_norm_rotate")
+    return q_out, k_out
+
+
+def cache_weights(q: torch.Tensor, cache: PagedCache, lse: torch.Tensor, weights: torch.Tensor, *,
+                  new_len: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None, scale: float = 0.0,
+                  stream: Optional[torch.cuda.Stream] = None) -> torch.Tensor:
+    """Add the attention weight of new tokens' queries to what the cache's
+    tokens have gathered: weights[b, x, t] (float32 [batch, kv_heads, width], in
+    place) gains the sum over key head x's group of heads and the rows that see
+    token t of exp(score - lse). q, new_len, tree_mask and scale are those of
+    :func:`tree_attention`, lse is what it returned (rows whose lse is -inf add
+    nothing). Entries of new tokens (t >= lengths[b]) are written, whatever
+    stood there; others behind them do not change. Returns weights, which are
+    refused if they share memory with the inputs. For a drafted tree, call it
+    once the path is known, with the kept rows' q and lse as a run (the cache
+    with the lengths of before, new_len the tokens that were kept)."""
+    desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
+    lib = _lib.load()
+    b, hk, d = desc.batch, desc.kv_heads, desc.head_dim
+    qr = _check_rows("q", q, b, None, d, dev)
+    heads, n = q.shape[1], q.shape[2]
+    if heads % hk != 0:
+        raise ValueError("the cache's heads must divide q's heads")
+    nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
+    mask = None if tree_mask is None else _check_array("tree_mask", tree_mask, torch.int32, (b, n, (n + 31) // 32), dev)
+    lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev)
+    width = weights.shape[2] if isinstance(weights, torch.Tensor) and weights.dim() == 3 else 0
+    w = _check_array("weights", weights, torch.float32, (b, hk, width), dev)
+    st = lib.wise_cache_weights(desc, heads, n, qr, lse_ptr, nl, mask, scale, w, width, handle)
+    _lib.check(st, "wise_cache_weights")
+    return weights
+
+
+def cache_evict(cache: PagedCache, weights: torch.Tensor, budget: int, page_table: torch.Tensor, *, recent: int = 0,
+                sink: int = 0, new_lengths: Optional[torch.Tensor] = None, weights_out: Optional[torch.Tensor] = None,
+                workspace: Optional[torch.Tensor] = None,
+                stream: Optional[torch.cuda.Stream] = None) -> Tuple[PagedCache, torch.Tensor]:
+    """Keep at most `budget` committed tokens of each sequence: of a longer one
+    each key head keeps its first `sink` tokens, its last `recent` ones and, of
+    those between, the heaviest (weights: float32 [batch, kv_heads, width], see
+    :func:`cache_weights`; of equal ones those in lower slots). The kept tokens
+    go, in the order of their slots, to slots 0, 1, ... of the pages of
+    `page_table` (int32 [batch, pages], of the same pools), which must not be
+    pages that the call reads; a sequence of at most `budget` tokens may name
+    its own pages again (nothing of it moves then). Returns the cache behind the
+    new table, with its new lengths, and the kept tokens' weights (float32
+    [batch, kv_heads, width_out], by default as wide as the new table's pages;
+    zero behind the kept tokens). Slots no longer tell positions: give
+    :func:`cache_append` those of later tokens. new_lengths, weights_out and
+    workspace are refused if they share memory with each other or the inputs."""
+    desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
+    lib = _lib.load()
+    b, hk = desc.batch, desc.kv_heads
+    width = weights.shape[2] if isinstance(weights, torch.Tensor) and weights.dim() == 3 else 0
+    w = _check_array("weights", weights, torch.float32, (b, hk, width), dev)
+    pages = page_table.shape[1] if isinstance(page_table, torch.Tensor) and page_table.dim() == 2 else 0
+    to = _check_array("page_table", page_table, torch.int32, (b, pages), dev)
+    for name, x in (("budget", budget), ("recent", recent), ("sink", sink), ("page_table's rows", pages)):
+        if not isinstance(x, int) or not 0 <= x <= _MAX_I32:
+            raise ValueError(f"{name} must be a non-negative whole number below 2^31")
+    if new_lengths is None:
+        new_lengths = _empty((b,), torch.int32, weights.device, stream)
+        out = new_lengths.data_ptr()
+    else:
+        out = _check_array("new_lengths", new_lengths, torch.int32, (b,), dev)
+    if weights_out is None:
+        weights_out = _empty((b, hk, pages * desc.page), torch.float32, weights.device, stream)
+        wo = weights_out.data_ptr()
+    else:
+        wo = _check_array("weights_out", weights_out, torch.float32,
+                          (b, hk, weights_out.shape[2] if isinstance(weights_out, torch.Tensor) and weights_out.dim() == 3 else 0), dev)
+    nbytes = lib.wise_cache_evict_workspace(desc, budget)
+    own = 0
+    if workspace is not None:
+        _check_bytes("workspace", workspace, nbytes, weights.device)
+        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel()
+    else:
+        ws_ptr = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(nbytes, 16), handle)
+    try:
+        st = lib.wise_cache_evict(desc, w, width, budget, recent, sink, to, pages, out, wo, weights_out.shape[2], ws_ptr, nbytes,
+                                  handle)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    _lib.check(st, "wise_cache_evict")
+    return PagedCache(cache.k_pages, cache.v_pages, page_table, new_lengths), weights_out
 
 
 def device_status(stream: Optional[torch.cuda.Stream] = None) -> int:

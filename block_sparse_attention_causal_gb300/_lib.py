@@ -38,7 +38,8 @@ EXPORTS = (
     "wise_support_retained_mass", "wise_support_jaccard", "wise_select_control", "wise_attn_discover_select",
     "wise_select_finalize", "wise_validate_schedule", "wise_wait_expiry_check", "wise_gather_plan_bytes",
     "wise_gather_plan", "wise_attn_sparse_planned", "wise_cache_append", "wise_attn_tree_workspace",
-    "wise_attn_tree", "wise_cache_accept",
+    "wise_attn_tree", "wise_cache_accept", "wise_cache_append_norm", "wise_norm_rotate", "wise_cache_weights",
+    "wise_cache_evict_workspace", "wise_cache_evict",
 )
 
 
@@ -83,6 +84,18 @@ class Rows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64 * 3)]
 
 
+class HeadNorm(ctypes.Structure):
+    """wise_head_norm"""
+    _fields_ = [("q_weight", ctypes.c_void_p), ("k_weight", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+                ("k_stride", ctypes.c_int64), ("weight_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class RopeDesc(ctypes.Structure):
+    """wise_rope"""
+    _fields_ = [("steps", ctypes.c_void_p), ("axes", ctypes.c_void_p), ("rotary_dim", ctypes.c_int32),
+                ("n_axes", ctypes.c_int32), ("flags", ctypes.c_uint32), ("reserved", ctypes.c_uint32)]
+
+
 _lock = threading.Lock()
 _handle = None
 
@@ -94,6 +107,8 @@ _u32 = ctypes.c_uint32
 _dp = ctypes.POINTER(AttnDesc)
 _cp = ctypes.POINTER(PagedCacheDesc)
 _rp = ctypes.POINTER(Rows)
+_op = ctypes.POINTER(RopeDesc)
+_np = ctypes.POINTER(HeadNorm)
 
 _SIGNATURES = {
     "wise_abi_version": (ctypes.c_int, []),
@@ -124,6 +139,11 @@ _SIGNATURES = {
     "wise_attn_tree_workspace": (_sz, [_cp, _i32, _i32]),
     "wise_attn_tree": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _sz, _vp]),
     "wise_cache_accept": (ctypes.c_int, [_cp, _i32, _vp, _vp, _vp, _vp]),
+    "wise_cache_append_norm": (ctypes.c_int, [_cp, _i32, _rp, _rp, _i32, _rp, _vp, _vp, _vp, _op, _np, _vp]),
+    "wise_norm_rotate": (ctypes.c_int, [_i32, _i32, _i32, _i32, _rp, _vp, _i32, _rp, _vp, _vp, _op, _np, _vp]),
+    "wise_cache_weights": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, _vp, ctypes.c_float, _vp, _i64, _vp]),
+    "wise_cache_evict_workspace": (_sz, [_cp, _i32]),
+    "wise_cache_evict": (ctypes.c_int, [_cp, _vp, _i64, _i32, _i32, _i32, _vp, _i32, _vp, _vp, _i64, _vp, _sz, _vp]),
     "wise_wait_expiry_check": (ctypes.c_int, [_vp]),
     "wise_device_status": (ctypes.c_int, [_vp]),
 }

@@ -219,4 +219,64 @@ int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int
 // page of one head.
 cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream);
 
+// Rows normed per head and rotated (norm_kernel.cu): into a paged cache, or
+// dense ones.
+struct NormLaunch {
+  CacheView cache;  // paged
+  int32_t paged;
+  int32_t batch, n, head_dim, heads, kv_heads;  // heads: 0 without q
+  RowsView q, k, v;                             // k, v: data null without them
+  uint16_t* q_out;
+  uint16_t* k_out;  // pool, or dense rows
+  uint16_t* v_out;  // pool
+  const int32_t* new_len;
+  const int32_t* positions;  // [n_axes, batch, n]
+  const int64_t* rope;
+  const int32_t* axes;  // [rotary_dim / 2] or null: axis 0
+  int32_t n_axes, rotary_dim, pairs;
+  const void* q_weight;  // null: not normed
+  const void* k_weight;
+  int64_t q_weight_stride, k_weight_stride;  // elements from head to head (0: shared)
+  int32_t weight_f32;
+  float eps;
+  uint32_t* err;
+};
+cudaError_t launch_norm(const NormLaunch& a, cudaStream_t stream);
+
+// Eviction by weight (evict_kernel.cu).
+struct EvictLaunch {
+  CacheView cache;
+  int32_t head_dim;
+  int32_t budget, recent, sink;
+  const float* weights;  // [batch, kv_heads, width]
+  int64_t width;
+  const int32_t* to_table;  // [batch, to_pages]
+  int32_t to_pages;
+  int32_t chunks;  // blocks of the move per key head
+  int32_t* new_lengths;
+  float* weights_out;  // [batch, kv_heads, width_out]
+  int64_t width_out;
+  int32_t* list;  // [batch, kv_heads, list_width]: kept places
+  int64_t list_width;
+  uint32_t* err;
+};
+int64_t evict_move_chunks(int64_t budget, int64_t width_out);
+cudaError_t launch_evict(const EvictLaunch& e, cudaStream_t stream);
+
+// Attention weight of new tokens, summed per cached token (weights_kernel.cu).
+struct WeightsLaunch {
+  CacheView cache;
+  int32_t head_dim, heads, n;
+  RowsView q;
+  const float* lse;  // [batch, heads, n]
+  const int32_t* new_len;
+  const int32_t* tree_mask;
+  float scale;
+  float* weights;  // [batch, kv_heads, width]
+  int64_t width;
+  uint32_t* err;
+};
+// map = K's tensor map, as for launch_tree
+cudaError_t launch_weights(const WeightsLaunch& w, const CUtensorMap* map, cudaStream_t stream);
+
 }  // namespace wise

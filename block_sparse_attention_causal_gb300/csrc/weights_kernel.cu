@@ -1,0 +1,387 @@
+// Attention weight gathered by the tokens of a paged cache: for each key head
+//   w[t] += sum over the rows i of its group of heads that see t of exp(s_it - LSE_i),
+// s_it = scale q_i k_t, with the LSE that the rows' attention returned.
+//
+// Tiles are turned round as in tree_narrow.cu: 128 keys are the MMA's rows and
+// up to 256 query rows its columns,
+//   S^T[key, row] = K Q^T,
+// so that a thread holds one key's scores of all rows and sums their weights in
+// its registers, always in the same order; no value meets another key's, so what
+// lies behind the last token, or in a key that a row does not see, has no way
+// into a sum. More than 256 rows are further launches, one after the other.
+//
+// Warp roles (384 threads): 0 TMA (a ring of K tiles), 1 MMA issue, 2 and 3 Q
+// and what belongs to it, 4-7 and 8-11 sums of alternate tiles, one key per thread.
+// The key tiles of all (sequence, key head) units form the line of tree.cuh.
+#include "tree.cuh"
+
+namespace wise {
+namespace {
+
+constexpr int kThreads = 384;
+constexpr int kMaxRows = 256;
+constexpr int kMaxSlots = 6;
+constexpr uint32_t kSmem = 232448u;
+
+struct WeightsParams {
+  TreeParams p;        // the line: units of one (sequence, key head)
+  const float* lse;
+  float* weights;
+  int64_t width;
+  int32_t row0, nrows;  // this launch's rows of a unit
+  int32_t cols;         // nrows in whole blocks of 16
+  int32_t slots;        // ring
+  uint32_t tmem_cols;
+};
+
+// Behind the ring and two Q buffers of `cols` rows:
+struct Small {
+  float lse2[2][kMaxRows];                // of even and odd segments: LSE in powers of two, +inf: the row adds nothing
+  uint32_t words[2][kTreeMaxTokens * 4];  // [token][new token / 32]: who sees whom
+  int plain[2][2];                        // rows from 0 on that all count, as either of its warps found
+  uint64_t q_full[2];   // Q, lse2 and words of a segment are there (2 warps)
+  uint64_t seg_done[2];  // and no longer needed (8 warps)
+  uint64_t s_full[2];    // scores computed
+  uint64_t s_empty[2];   // and read (4 warps)
+  uint64_t full[kMaxSlots], empty[kMaxSlots];
+  uint64_t drain;
+  uint32_t flags[kTileFlags];
+  uint32_t tmem_base;
+  volatile int abort_flag;
+  int scratch[kThreads / 32 + 12];
+};
+constexpr uint32_t kRoom = kSmem - (uint32_t)sizeof(Small);
+
+__device__ __forceinline__ void add8(const float* lse2, const uint32_t* s, float sl2, uint64_t (&sum)[2]) {
+  const uint64_t sc = f2_pack(sl2, sl2);
+#pragma unroll
+  for (int c = 0; c < 8; c += 4) {
+    const float4 l = *reinterpret_cast<const float4*>(lse2 + c);
+    float e0, e1, e2, e3;
+    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, f2_pack(-l.x, -l.y)), e0, e1);
+    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, f2_pack(-l.z, -l.w)), e2, e3);
+    sum[0] = fadd2(sum[0], f2_pack(fast_exp2(e0), fast_exp2(e1)));
+    sum[1] = fadd2(sum[1], f2_pack(fast_exp2(e2), fast_exp2(e3)));
+  }
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1)
+    weights_kernel(const __grid_constant__ CUtensorMap tm_k, const WeightsParams a) {
+  extern __shared__ __align__(1024) uint8_t smem[];
+  const TreeParams& p = a.p;
+  constexpr uint32_t KV_BYTES = tile_bytes<D>(kTile);
+  const uint32_t q_bytes = tile_bytes<D>(a.cols);
+  uint8_t* sq = smem + a.slots * KV_BYTES;
+  Small& m = *reinterpret_cast<Small*>(sq + 2 * q_bytes);
+  uint32_t* err = p.t.err;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
+    grid_wait();
+    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+    return;
+  }
+  if (threadIdx.x == 32) {
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&m.q_full[i], 2);
+      mbar_init(&m.seg_done[i], 8);
+      mbar_init(&m.s_full[i], 1);
+      mbar_init(&m.s_empty[i], 4);
+    }
+    for (int i = 0; i < a.slots; ++i) {
+      mbar_init(&m.full[i], 1);
+      mbar_init(&m.empty[i], 1);
+    }
+    mbar_init(&m.drain, 1);
+    for (int i = 0; i < kTileFlags; ++i) m.flags[i] = 0u;
+    m.abort_flag = 0;
+    fence_mbar_init();
+  }
+  if (threadIdx.x == 0) tma_prefetch_desc(&tm_k);
+  prefetch_tables(p);
+  grid_wait();
+  // tensor memory only now: a kernel before this one that still runs could wait
+  // for what this one holds
+  if (warp == 1) {
+    tmem_alloc(&m.tmem_base, a.tmem_cols);
+    tmem_relinquish();
+  }
+  grid_trigger();
+  LinePart part;
+  find_part<kThreads>(p, m.scratch, part);
+  const uint32_t tbase = m.tmem_base;
+  volatile int* abort_flag = &m.abort_flag;
+  const int slots = a.slots;
+  Ring ring;
+  ring.flags = m.flags;
+  if (part.left > 0) {
+    Walk w;
+    w.start(p, part);
+    if (warp == 0) {
+      // ----------------------------------------------------------------- TMA
+      const int page = 1 << p.t.cache.page_shift;
+      const int boxes = kTile >> p.t.cache.page_shift;  // pages per tile
+      const uint32_t box_bytes = tile_bytes<D>(page);
+      uint32_t tau = 0;
+      int slot = 0;
+      uint32_t turn = 0;  // uses of the present slot before
+      bool ok = true, flagged = false;
+      do {
+        const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
+        const int last_page = (w.keys - 1) >> p.t.cache.page_shift;  // -1: none
+        // the lanes hold 32 columns of the page table, and the 32 after them,
+        // which are under way while these are used
+        int have = w.t0 * boxes;
+        auto columns = [&](int c) -> int32_t { return c + lane <= last_page ? table[c + lane] : -1; };
+        int32_t held = columns(have), ahead = columns(have + 32);
+        for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
+          const int col = t * boxes;
+          if (col >= have + 32) {  // (32 columns are whole tiles)
+            have += 32;
+            held = ahead;
+            ahead = columns(have + 32);
+          }
+          const int32_t pg = __shfl_sync(0xffffffffu, held, (col - have + lane) & 31);
+          const bool in = lane < boxes && col + lane <= last_page;
+          const bool good = in && page_ok(p.t, pg);
+          const uint32_t bad = __ballot_sync(0xffffffffu, in && !good);
+          const uint32_t loads = __ballot_sync(0xffffffffu, good);
+          if (bad != 0u && !flagged) {
+            flagged = true;
+            if (lane == 0) atomicOr(err, kErrBadCache);
+          }
+          if (turn > 0) ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.empty[slot], (turn - 1) & 1, abort_flag, err));
+          if (!ok) break;
+          if (lane == 0) {
+            *reinterpret_cast<volatile uint32_t*>(&m.flags[tau % kTileFlags]) = tile_word(tau, bad);
+            mbar_arrive_expect_tx(&m.full[slot], (uint32_t)__popc(loads) * box_bytes);
+          }
+          __syncwarp();
+          if (good) {
+            uint8_t* dst = smem + slot * KV_BYTES + (uint32_t)(lane * page) * kRowBytes;
+#pragma unroll
+            for (int c = 0; c < row_chunks<D>(); ++c)
+              tma_load_3d(dst + c * kTile * kRowBytes, &tm_k, &m.full[slot], c * 64, w.hk * page, pg);
+          }
+          __syncwarp();
+          if (++slot == slots) slot = 0, ++turn;
+        }
+      } while (ok && w.next(p));
+      // no copy into this CTA's shared memory may outlive the CTA
+      if (lane == 0) {
+        int none = 0;
+        for (uint32_t i = (tau > (uint32_t)slots ? tau - slots : 0u); i < tau; ++i)
+          mbar_wait<1>(&m.full[i % slots], (i / slots) & 1, &none, err);
+      }
+      __syncwarp();
+    } else if (warp == 1) {
+      // ----------------------------------------------------------- MMA issue
+      if (elect_one()) {
+        const uint32_t idesc = idesc_bf16_f32(128, a.cols, 0, 0);
+        const uint64_t k_desc = smem_desc(smem_u32(smem), 16, 8 * kRowBytes, kSwizzle128);
+        const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 8 * kRowBytes, kSwizzle128);
+        uint32_t tau = 0, turn = 0;
+        int slot = 0;
+        bool ok = true;
+        do {
+          ok = mbar_wait<1>(&m.q_full[w.seg & 1], (w.seg >> 1) & 1, abort_flag, err);
+          const uint64_t qd = q_desc + (uint64_t)(((w.seg & 1) * q_bytes) >> 4);
+          for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
+            const int buf = tau & 1;
+            ok = mbar_wait<1>(&m.full[slot], turn & 1, abort_flag, err) &&
+                 (tau < 2u || mbar_wait<1>(&m.s_empty[buf], ((tau >> 1) - 1) & 1, abort_flag, err));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t kd = k_desc + (uint64_t)((slot * KV_BYTES) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < D / 16; ++kk) {
+              const int c = kk / 4, wd = kk % 4;
+              umma_ss(tbase + buf * a.cols, kd + (uint64_t)((c * kTile * kRowBytes + wd * 32) >> 4),
+                      qd + (uint64_t)((c * a.cols * kRowBytes + wd * 32) >> 4), idesc, kk > 0);
+            }
+            umma_commit(&m.s_full[buf]);
+            umma_commit(&m.empty[slot]);
+            if (++slot == slots) slot = 0, ++turn;
+          }
+        } while (ok && w.next(p));
+        // every MMA of this thread done before TMEM and shared memory go
+        int none = 0;
+        umma_commit(&m.drain);
+        mbar_wait<1>(&m.drain, 0, &none, err);
+      }
+      __syncwarp();
+    } else if (warp < 4) {
+      // ------------------------------------------------------------------- Q
+      const int th = threadIdx.x - 64;  // 0 .. 63
+      bool ok = true;
+      do {
+        const int buf = w.seg & 1;
+        if (w.seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.seg_done[buf], ((w.seg >> 1) - 1) & 1, abort_flag, err));
+        if (!ok) break;
+        const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));  // rows of valid tokens come first
+        uint8_t* dst = sq + buf * q_bytes;
+        constexpr int UNITS = D / 8;
+        const uint16_t* q = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
+        for (int x = th; x < a.cols * UNITS; x += 64) {
+          const int r = x / UNITS, u = x % UNITS, tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
+          uint8_t* at = dst + unit_offset(a.cols, r, u);
+          if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn + u * 8);
+          else *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+        }
+        int first = live;  // first row that adds nothing
+        for (int r = th; r < a.cols; r += 64) {
+          const int tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
+          float l = -INFINITY;
+          if (r < live) l = a.lse[((int64_t)w.b * p.t.heads + w.hk * p.group + g) * p.t.n + tok];
+          if (l == -INFINITY) first = min(first, r);
+          m.lse2[buf][r] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+        }
+        first = __reduce_min_sync(0xffffffffu, first);
+        if (lane == 0) m.plain[buf][warp & 1] = first;
+        // which new tokens each token sees
+        if (w.t1 * kTile > w.len)
+          for (int x = th; x < w.nl * 4; x += 64) {
+            const int i = x >> 2, j0 = (x & 3) * 32;
+            uint32_t v = 0u;
+            if (p.t.tree_mask) v = (x & 3) < p.mask_words ? (uint32_t)p.t.tree_mask[((int64_t)w.b * p.t.n + i) * p.mask_words + (x & 3)] : 0u;
+            else v = i >= j0 + 31 ? 0xffffffffu : i < j0 ? 0u : (2u << (i - j0)) - 1u;
+            m.words[buf][x] = v;
+          }
+        copy16_wait();
+        fence_proxy_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.q_full[buf]);
+      } while (w.next(p));
+      __syncwarp();
+    } else {
+      // ---------------------------------------------------------------- sums
+      const int s = (warp - 4) >> 2;  // tiles with this parity
+      const int quarter = warp & 3, key = quarter * 32 + lane;
+      const uint32_t tS = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + s * a.cols;
+      const float sl2 = p.scale_log2;
+      uint32_t tau = 0;
+      bool ok = true;
+      do {
+        const int buf = w.seg & 1;
+        ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.q_full[buf], (w.seg >> 1) & 1, abort_flag, err));
+        const float* lse2 = m.lse2[buf];
+        const int plain = ok ? min(m.plain[buf][0], m.plain[buf][1]) : 0;
+        const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));
+        float* row = a.weights + ((int64_t)w.b * p.t.cache.kv_heads + w.hk) * a.width;
+        for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
+          if ((int)(tau & 1u) != s) continue;
+          const int pos = t * kTile + key;
+          const bool in = pos < w.keys && pos < a.width;
+          const bool fresh = pos >= w.len && a.row0 == 0;  // a new token's sum begins with the first launch
+          float old = 0.f;
+          if (in && !fresh) old = row[pos];
+          ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.s_full[s], (tau >> 1) & 1, abort_flag, err));
+          if (!ok) break;
+          const uint32_t bad = tile_bad<1>(ring, tau, abort_flag, err);
+          tc_fence_after();
+          const bool tail = (t + 1) * kTile > w.len;
+          uint64_t sum[2] = {0ull, 0ull};
+          for (int c0 = 0; c0 < live; c0 += 16) {
+            uint32_t v[16];
+            __syncwarp();
+            tmem_ld_x16(tS + c0, v);
+            tmem_wait_ld16(v);
+            if (!tail && c0 + 16 <= plain) {
+              add8(lse2 + c0, v, sl2, sum);
+              add8(lse2 + c0 + 8, v + 8, sl2, sum);
+            } else {
+              // column by column: rows that do not see the key, or add nothing
+              const int j = pos - w.len;
+              float e = 0.f;
+#pragma unroll 1
+              for (int c = c0; c < min(c0 + 16, live); ++c) {
+                const int tok = row_token(p, a.row0 + c);
+                const bool sees = j < 0 || (j < w.nl && ((m.words[buf][tok * 4 + (j >> 5)] >> (j & 31)) & 1u));
+                float x = 0.f;
+#pragma unroll
+                for (int k = 0; k < 16; ++k)
+                  if (c - c0 == k) x = __uint_as_float(v[k]);
+                if (sees && lse2[c] != INFINITY) e += fast_exp2(fmaf(x, sl2, -lse2[c]));
+              }
+              sum[0] = fadd2(sum[0], f2_pack(e, 0.f));
+            }
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&m.s_empty[s]);
+          if (pos < w.keys && pos >= a.width) atomicOr(err, kErrBadCache);
+          float x0, x1;
+          f2_unpack(fadd2(sum[0], sum[1]), x0, x1);
+          // (a page outside the pool: its tokens are not seen)
+          if (in) row[pos] = ((bad >> (key >> p.t.cache.page_shift)) & 1u) ? old : old + (x0 + x1);
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&m.seg_done[buf]);
+      } while (ok && w.next(p));
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tbase, a.tmem_cols);
+  }
+}
+
+template <int D>
+cudaError_t launch_d(const WeightsParams& a, const CUtensorMap* map, uint32_t bytes, cudaStream_t stream) {
+  static bool configured[64] = {};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!configured[dev]) {
+    e = cudaFuncSetAttribute(weights_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem);
+    if (e != cudaSuccess) return e;
+    configured[dev] = true;
+  }
+  return launch_chained(weights_kernel<D>, dim3(kTreeCtas), dim3(kThreads), bytes, stream, *map, a);
+}
+
+}  // namespace
+
+cudaError_t launch_weights(const WeightsLaunch& w, const CUtensorMap* map, cudaStream_t stream) {
+  WeightsParams a;
+  TreeParams& p = a.p;
+  p = TreeParams{};
+  p.t.cache = w.cache;
+  p.t.head_dim = w.head_dim;
+  p.t.heads = w.heads;
+  p.t.n = w.n;
+  p.t.q = w.q;
+  p.t.new_len = w.new_len;
+  p.t.tree_mask = w.tree_mask;
+  p.t.err = w.err;
+  p.group = w.heads / w.cache.kv_heads;
+  p.group_mul = (uint32_t)((0x100000000ull + p.group - 1) / p.group);
+  p.rows = p.group * w.n;
+  p.pairs = 1;
+  p.mask_words = (w.n + 31) / 32;
+  p.overhead = 1;
+  p.scale_log2 = w.scale * 1.4426950408889634f;
+  a.lse = w.lse;
+  a.weights = w.weights;
+  a.width = w.width;
+  for (a.row0 = 0; a.row0 < p.rows; a.row0 += kMaxRows) {
+    a.nrows = p.rows - a.row0 < kMaxRows ? p.rows - a.row0 : kMaxRows;
+    a.cols = (a.nrows + 15) / 16 * 16;
+    a.tmem_cols = 32;
+    while (a.tmem_cols < 2u * (uint32_t)a.cols) a.tmem_cols *= 2;
+    const uint32_t chunks = w.head_dim > 64 ? 2 : 1, tile = kTile * chunks * kRowBytes, q = 2 * a.cols * chunks * kRowBytes;
+    a.slots = (int32_t)((kRoom - q) / tile);
+    if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+    const uint32_t bytes = a.slots * tile + q + (uint32_t)sizeof(Small);
+    const cudaError_t e = w.head_dim == 64   ? launch_d<64>(a, map, bytes, stream)
+                          : w.head_dim == 96 ? launch_d<96>(a, map, bytes, stream)
+                                             : launch_d<128>(a, map, bytes, stream);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
+}
+
+}  // namespace wise

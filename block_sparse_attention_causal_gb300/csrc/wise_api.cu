@@ -358,6 +358,56 @@ int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
   return WISE_OK;
 }
 
+// The weights and rotation of wise_cache_append_norm and wise_norm_rotate.
+int check_norm(const wise_rope* r, const wise_head_norm* n, int64_t heads, int64_t kv_heads, int32_t d,
+               const int32_t* positions) {
+  if (r) {
+    if (r->rotary_dim < 0 || r->rotary_dim > d || r->rotary_dim % 16 != 0 || (r->rotary_dim > 0 && !r->steps) ||
+        r->n_axes < 1 || (!r->axes && r->n_axes != 1) || (r->axes && !positions) || (r->flags & ~WISE_ROPE_PAIRS))
+      return WISE_ERR_INVALID_ARGUMENT;
+    if ((reinterpret_cast<uintptr_t>(r->steps) & 7u) || misaligned4(r->axes)) return WISE_ERR_ALIGNMENT;
+  }
+  if (n) {
+    if ((n->weight_dtype != WISE_BF16 && n->weight_dtype != WISE_F32) || !(n->eps > 0.f) || isinf(n->eps) ||
+        n->q_stride < 0 || n->k_stride < 0)
+      return WISE_ERR_INVALID_ARGUMENT;
+    if (n->q_stride > INT64_MAX / 4 / (heads > 0 ? heads : 1) || n->k_stride > INT64_MAX / 4 / (kv_heads > 0 ? kv_heads : 1))
+      return WISE_ERR_UNSUPPORTED;
+    if (!aligned16(n->q_weight) || !aligned16(n->k_weight) || n->q_stride % 8 != 0 || n->k_stride % 8 != 0)
+      return WISE_ERR_ALIGNMENT;
+  }
+  return misaligned4(positions) ? WISE_ERR_ALIGNMENT : WISE_OK;
+}
+// Whether an output lies over the positions, rotation or weights.
+bool overlap_norm(const wise_rope* r, const wise_head_norm* n, int64_t heads, int64_t kv_heads, int64_t d,
+                  const int32_t* positions, int64_t tokens, const void* out, int64_t bytes) {
+  const int64_t axes = r ? r->n_axes : 1, pairs = r ? r->rotary_dim / 2 : 0;
+  if (overlap(out, bytes, positions, axes * tokens * 4)) return true;
+  if (r && (overlap(out, bytes, r->steps, pairs * 8) || overlap(out, bytes, r->axes, pairs * 4))) return true;
+  const int64_t size = n && n->weight_dtype == WISE_F32 ? 4 : 2;
+  return n && (overlap(out, bytes, n->q_weight, ((heads - 1) * n->q_stride + d) * size) ||
+               overlap(out, bytes, n->k_weight, ((kv_heads - 1) * n->k_stride + d) * size));
+}
+void set_norm(NormLaunch& a, const wise_rope* r, const wise_head_norm* n, const int32_t* positions) {
+  a.positions = positions;
+  a.n_axes = 1;
+  if (r) {
+    a.rope = r->steps;
+    a.axes = r->axes;
+    a.n_axes = r->n_axes;
+    a.rotary_dim = r->rotary_dim;
+    a.pairs = (r->flags & WISE_ROPE_PAIRS) != 0;
+  }
+  if (n) {
+    a.q_weight = n->q_weight;
+    a.k_weight = n->k_weight;
+    a.q_weight_stride = n->q_stride;
+    a.k_weight_stride = n->k_stride;
+    a.weight_f32 = n->weight_dtype == WISE_F32;
+    a.eps = n->eps;
+  }
+}
+
 // Self-check of the bounded wait: one thread waits on an mbarrier that
 // nothing arrives on, through the same wait routine as the attention kernels
 // but with a 20 ms limit. The wait expires, kErrTimeout is recorded, and the
@@ -902,6 +952,198 @@ int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const 
   a.n_accepted = n_accepted;
   a.new_lengths = new_lengths;
   return launch_cache_accept(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+int wise_cache_append_norm(const wise_paged_cache* cache, int32_t new_tokens, const wise_rows* k, const wise_rows* v,
+                           int32_t heads, const wise_rows* q, void* q_out, const int32_t* new_len,
+                           const int32_t* positions, const wise_rope* rope, const wise_head_norm* norm,
+                           wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if (new_tokens < 1 || (q && (heads < 1 || !q_out))) return WISE_ERR_INVALID_ARGUMENT;
+  if (new_tokens > kMaxCacheTokens || (int64_t)cache->batch * new_tokens > INT32_MAX ||
+      2 * (int64_t)cache->kv_heads + (q ? heads : 0) > INT32_MAX)
+    return WISE_ERR_UNSUPPORTED;
+  const int64_t batch = cache->batch, d = cache->head_dim, n = new_tokens;
+  if ((st = check_norm(rope, norm, q ? heads : 0, cache->kv_heads, cache->head_dim, positions)) != WISE_OK) return st;
+  if ((st = check_rows(k)) != WISE_OK || (st = check_rows(v)) != WISE_OK) return st;
+  if (q && (st = check_rows(q)) != WISE_OK) return st;
+  if ((q && !aligned16(q_out)) || misaligned4(new_len)) return WISE_ERR_ALIGNMENT;
+  if (pools_meet(cache)) return WISE_ERR_INVALID_ARGUMENT;
+  if (q) {
+    // threads write rows of q_out while others still read
+    const int64_t bytes = batch * heads * n * d * 2;
+    if (overlap_cache(cache, q_out, bytes) || overlap_rows(q, batch, heads, n, d, q_out, bytes) ||
+        overlap_rows(k, batch, cache->kv_heads, n, d, q_out, bytes) ||
+        overlap_rows(v, batch, cache->kv_heads, n, d, q_out, bytes) || overlap(q_out, bytes, new_len, batch * 4) ||
+        overlap_norm(rope, norm, heads, cache->kv_heads, d, positions, batch * n, q_out, bytes))
+      return WISE_ERR_INVALID_ARGUMENT;
+  }
+  NormLaunch a;
+  memset(&a, 0, sizeof(a));
+  a.err = error_word();
+  if (!a.err) return WISE_ERR_CUDA;
+  a.cache = cache_view(cache);
+  a.paged = 1;
+  a.batch = cache->batch;
+  a.n = new_tokens;
+  a.head_dim = cache->head_dim;
+  a.kv_heads = cache->kv_heads;
+  a.k = rows_view(k);
+  a.v = rows_view(v);
+  if (q) {
+    a.q = rows_view(q);
+    a.heads = heads;
+    a.q_out = static_cast<uint16_t*>(q_out);
+  }
+  a.k_out = a.cache.k_pages;
+  a.v_out = a.cache.v_pages;
+  a.new_len = new_len;
+  set_norm(a, rope, norm, positions);
+  return launch_norm(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+int wise_norm_rotate(int32_t batch, int32_t new_tokens, int32_t head_dim, int32_t heads, const wise_rows* q, void* q_out,
+                     int32_t kv_heads, const wise_rows* k, void* k_out, const int32_t* positions, const wise_rope* rope,
+                     const wise_head_norm* norm, wise_stream_t stream) {
+  if (batch < 1 || new_tokens < 1 || heads < 1 || !q_out || (k && (kv_heads < 1 || !k_out))) return WISE_ERR_INVALID_ARGUMENT;
+  if (head_dim != 64 && head_dim != 96 && head_dim != 128) return WISE_ERR_UNSUPPORTED;
+  if (!k) kv_heads = 0;
+  const int64_t b = batch, n = new_tokens, d = head_dim;
+  if (b * n > INT32_MAX || (int64_t)heads + kv_heads > INT32_MAX || b * n > INT64_MAX / 2 / d / ((int64_t)heads + kv_heads))
+    return WISE_ERR_UNSUPPORTED;
+  int st;
+  if ((st = check_norm(rope, norm, heads, kv_heads, head_dim, positions)) != WISE_OK) return st;
+  if ((st = check_rows(q)) != WISE_OK || (k && (st = check_rows(k)) != WISE_OK)) return st;
+  if (!aligned16(q_out) || (k && !aligned16(k_out))) return WISE_ERR_ALIGNMENT;
+  const int64_t q_bytes = b * heads * n * d * 2, k_bytes = b * kv_heads * n * d * 2;
+  for (int i = 0; i < (k ? 2 : 1); ++i) {
+    const void* out = i ? k_out : q_out;
+    const int64_t bytes = i ? k_bytes : q_bytes;
+    if (overlap_rows(q, b, heads, n, d, out, bytes) || (k && overlap_rows(k, b, kv_heads, n, d, out, bytes)) ||
+        overlap_norm(rope, norm, heads, kv_heads, d, positions, b * n, out, bytes) ||
+        (k && overlap(q_out, q_bytes, k_out, k_bytes)))
+      return WISE_ERR_INVALID_ARGUMENT;
+  }
+  NormLaunch a;
+  memset(&a, 0, sizeof(a));
+  a.err = error_word();
+  if (!a.err) return WISE_ERR_CUDA;
+  a.batch = batch;
+  a.n = new_tokens;
+  a.head_dim = head_dim;
+  a.heads = heads;
+  a.kv_heads = kv_heads;
+  a.q = rows_view(q);
+  a.q_out = static_cast<uint16_t*>(q_out);
+  if (k) {
+    a.k = rows_view(k);
+    a.k_out = static_cast<uint16_t*>(k_out);
+  }
+  set_norm(a, rope, norm, positions);
+  return launch_norm(a, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+int wise_cache_weights(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q,
+                       const float* lse, const int32_t* new_len, const int32_t* tree_mask, float scale, float* weights,
+                       int64_t width, wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if ((st = check_tree(cache, heads, new_tokens)) != WISE_OK) return st;
+  if (!lse || !weights || width < 1 || !(scale >= 0.f) || isinf(scale)) return WISE_ERR_INVALID_ARGUMENT;
+  if (width > INT64_MAX / 4 / cache->batch / cache->kv_heads) return WISE_ERR_UNSUPPORTED;
+  if ((st = check_rows(q)) != WISE_OK) return st;
+  if (misaligned4(lse) || misaligned4(weights) || misaligned4(new_len) || misaligned4(tree_mask)) return WISE_ERR_ALIGNMENT;
+  {
+    // sums are written while other blocks still read
+    const int64_t batch = cache->batch, n = new_tokens, bytes = batch * cache->kv_heads * width * 4;
+    if (overlap_cache(cache, weights, bytes) || overlap_rows(q, batch, heads, n, cache->head_dim, weights, bytes) ||
+        overlap(weights, bytes, lse, batch * heads * n * 4) || overlap(weights, bytes, new_len, batch * 4) ||
+        overlap(weights, bytes, tree_mask, batch * n * ((n + 31) / 32) * 4))
+      return WISE_ERR_INVALID_ARGUMENT;
+  }
+  WeightsLaunch w;
+  memset(&w, 0, sizeof(w));
+  w.err = error_word();
+  if (!w.err) return WISE_ERR_CUDA;
+  w.cache = cache_view(cache);
+  w.head_dim = cache->head_dim;
+  w.heads = heads;
+  w.n = new_tokens;
+  w.q = rows_view(q);
+  w.lse = lse;
+  w.new_len = new_len;
+  w.tree_mask = tree_mask;
+  w.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)cache->head_dim);
+  w.weights = weights;
+  w.width = width;
+  CUtensorMap map;
+  st = encode_pages(&map, cache->k_pages, cache);
+  if (st != WISE_OK) return st;
+  return launch_weights(w, &map, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+size_t wise_cache_evict_workspace(const wise_paged_cache* cache, int32_t budget) {
+  if (check_cache(cache, false) != WISE_OK || budget < 1) return 0;
+  return (size_t)cache->batch * cache->kv_heads * budget * 4;
+}
+
+int wise_cache_evict(const wise_paged_cache* cache, const float* weights, int64_t width, int32_t budget, int32_t recent,
+                     int32_t sink, const int32_t* to_table, int32_t to_pages, int32_t* new_lengths, float* weights_out,
+                     int64_t width_out, void* workspace, size_t workspace_bytes, wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if (!weights || !to_table || !new_lengths || !weights_out || width < 1 || to_pages < 1) return WISE_ERR_INVALID_ARGUMENT;
+  if (budget < 1 || recent < 0 || sink < 0 || (int64_t)recent + sink > budget || width_out < budget ||
+      (int64_t)to_pages * cache->page < budget)
+    return WISE_ERR_INVALID_ARGUMENT;
+  const int64_t batch = cache->batch, units = batch * cache->kv_heads;
+  if ((int64_t)to_pages * cache->page > kMaxCacheTokens || units > INT32_MAX / 8 ||
+      units > INT32_MAX / evict_move_chunks(budget, width_out) || width > INT64_MAX / 4 / units ||
+      width_out > INT64_MAX / 4 / units)
+    return WISE_ERR_UNSUPPORTED;
+  if (misaligned4(weights) || misaligned4(to_table) || misaligned4(new_lengths) || misaligned4(weights_out))
+    return WISE_ERR_ALIGNMENT;
+  const size_t need = wise_cache_evict_workspace(cache, budget);
+  if (!workspace || workspace_bytes < need) return WISE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WISE_ERR_ALIGNMENT;
+  if (pools_meet(cache)) return WISE_ERR_INVALID_ARGUMENT;
+  const struct {
+    const void* at;
+    int64_t bytes;
+  } outs[3] = {{new_lengths, batch * 4}, {weights_out, units * width_out * 4}, {workspace, (int64_t)need}};
+  for (int i = 0; i < 3; ++i) {
+    const void* at = outs[i].at;
+    const int64_t bytes = outs[i].bytes;
+    if (overlap_cache(cache, at, bytes) || overlap(at, bytes, weights, units * width * 4) ||
+        overlap(at, bytes, to_table, batch * to_pages * 4) ||
+        overlap(at, bytes, outs[(i + 1) % 3].at, outs[(i + 1) % 3].bytes))
+      return WISE_ERR_INVALID_ARGUMENT;
+  }
+  // the pools are written while the weights and the new table are read
+  for (const void* pool : {cache->k_pages, cache->v_pages})
+    if (overlap(pool, pool_bytes(cache), weights, units * width * 4) ||
+        overlap(pool, pool_bytes(cache), to_table, batch * to_pages * 4))
+      return WISE_ERR_INVALID_ARGUMENT;
+  EvictLaunch e;
+  memset(&e, 0, sizeof(e));
+  e.err = error_word();
+  if (!e.err) return WISE_ERR_CUDA;
+  e.cache = cache_view(cache);
+  e.head_dim = cache->head_dim;
+  e.budget = budget;
+  e.recent = recent;
+  e.sink = sink;
+  e.weights = weights;
+  e.width = width;
+  e.to_table = to_table;
+  e.to_pages = to_pages;
+  e.new_lengths = new_lengths;
+  e.weights_out = weights_out;
+  e.width_out = width_out;
+  e.list = static_cast<int32_t*>(workspace);
+  e.list_width = budget;
+  return launch_evict(e, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
 }
 
 int wise_validate_support(const wise_attn_desc* desc, const int32_t* row_ptr, const int32_t* col_idx,

@@ -33,7 +33,14 @@
  *                        tokens each of which sees the cache and its own
  *                        ancestors;
  *   wise_cache_accept    the drafted tokens that are kept become the cache's
- *                        own.
+ *                        own;
+ *   wise_cache_append_norm, wise_norm_rotate
+ *                        queries and keys normed per head and rotated by
+ *                        positions of one or several axes, in one pass: into
+ *                        a cache, or dense before a prompt's attention;
+ *   wise_cache_weights   the attention weight that a cache's tokens gather;
+ *   wise_cache_evict     the heaviest tokens of each key head are kept, in
+ *                        other pages.
  *
  * Conventions shared by every call
  * --------------------------------
@@ -84,7 +91,7 @@
 extern "C" {
 #endif
 
-#define WISE_ABI_VERSION 6
+#define WISE_ABI_VERSION 7
 
 typedef struct CUstream_st* wise_stream_t; /* same type as cudaStream_t */
 
@@ -536,6 +543,116 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
  */
 int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,
                       const int32_t* n_accepted, int32_t* new_lengths, wise_stream_t stream);
+
+/* Norm of each head's values before the rotation:
+ *     y = x / sqrt(mean(x^2) + eps) * w     (mean over head_dim values)
+ * for queries and for keys, in fp32. weight_dtype is the type of both weights;
+ * a row of weights is head_dim values, 16-byte aligned, and head h's is
+ * `stride` elements behind head h - 1's (a multiple of 8; 0: one row for all). */
+typedef struct wise_head_norm {
+  const void* q_weight; /* NULL: queries are not normed */
+  const void* k_weight; /* NULL: keys are not normed */
+  int64_t q_stride;
+  int64_t k_stride;
+  int32_t weight_dtype; /* wise_dtype */
+  float eps;            /* > 0 */
+} wise_head_norm;
+
+/* Position rotation (see wise_cache_append for `steps`). With `axes`, positions
+ * have n_axes axes, and pair i turns with axis axes[i] (pairs whose entry is not
+ * in [0, n_axes) do not turn and are flagged, WISE_ERR_BAD_CACHE). */
+typedef struct wise_rope {
+  const int64_t* steps; /* [rotary_dim / 2]; may be NULL when rotary_dim is 0 */
+  const int32_t* axes;  /* [rotary_dim / 2], or NULL: one axis */
+  int32_t rotary_dim;   /* multiple of 16, 0 <= rotary_dim <= head_dim */
+  int32_t n_axes;       /* >= 1; 1 without axes */
+  uint32_t flags;       /* WISE_ROPE_PAIRS or 0 */
+  uint32_t reserved;    /* 0 */
+} wise_rope;
+
+/*
+ * wise_cache_append_norm -- wise_cache_append with queries and keys normed on
+ * the way, and positions of several axes. Sums, norm and rotation are fp32, and a
+ * result is rounded once, to bf16: it is off by at most 2^-8 of itself and 2^-19
+ * of its two products' sizes. (The squares are summed in fp32: of a head with
+ * values above 2^60 the sum may overflow.)
+ *   positions  : [n_axes, batch, n] int32; NULL (without axes only):
+ *                lengths[b] + i.
+ *   rope       : NULL: no rotation.
+ *   norm       : NULL: no norm.
+ * The rest is as in wise_cache_append; q_out must not overlap the weights or the
+ * axes either. One launch.
+ */
+int wise_cache_append_norm(const wise_paged_cache* cache, int32_t new_tokens, const wise_rows* k, const wise_rows* v,
+                           int32_t heads, const wise_rows* q, void* q_out, const int32_t* new_len,
+                           const int32_t* positions, const wise_rope* rope, const wise_head_norm* norm,
+                           wise_stream_t stream);
+
+/*
+ * wise_norm_rotate -- the same for dense rows: queries and keys as a prompt's
+ * attention (wise_attn_discover, wise_attn_sparse) takes them.
+ *   batch, new_tokens (n), head_dim in {64, 96, 128}; batch * n < 2^31.
+ *   q, q_out   : [batch, heads, n, head_dim]; q_out dense, 16-byte aligned.
+ *   k, k_out   : [batch, kv_heads, n, head_dim]; k NULL: kv_heads and k_out
+ *                are ignored.
+ *   positions  : [n_axes, batch, n] int32; NULL (without axes only): i.
+ * The outputs must not overlap each other or the inputs (refused). One launch.
+ */
+int wise_norm_rotate(int32_t batch, int32_t new_tokens, int32_t head_dim, int32_t heads, const wise_rows* q, void* q_out,
+                     int32_t kv_heads, const wise_rows* k, void* k_out, const int32_t* positions, const wise_rope* rope,
+                     const wise_head_norm* norm, wise_stream_t stream);
+
+/*
+ * wise_cache_weights -- adds the attention weight of new tokens' queries to what
+ * the cache's tokens have gathered. For each sequence b, key head x and token t
+ * that row i < new_len[b] of head h of x's group sees (as in wise_attn_tree)
+ *     weights[b][x][t] += sum over h, i of exp(scale q_hi k_t - lse[b][h][i]).
+ * A committed token's sum is added to; a new token's (t >= lengths[b]) is
+ * written, whatever stood there. Other entries do not change. Rows with an LSE
+ * of -inf add nothing (rows that see nothing; or a caller's choice).
+ *   heads, new_tokens, q, new_len, tree_mask, scale : as in wise_attn_tree.
+ *   lse        : float32 [batch, heads, n], as wise_attn_tree returned it.
+ *   weights    : float32 [batch, kv_heads, width].
+ * weights must not overlap the inputs (refused). Tokens past width, the page
+ * table or the pool (pages outside [0, n_pages)) gather nothing and are flagged
+ * (WISE_ERR_BAD_CACHE). Sums are fp32, in a fixed order: repeated calls give the
+ * same bits. One launch for each 256 rows of a key head.
+ */
+int wise_cache_weights(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q,
+                       const float* lse, const int32_t* new_len, const int32_t* tree_mask, float scale, float* weights,
+                       int64_t width, wise_stream_t stream);
+
+/* Bytes of workspace wise_cache_evict needs; 0 when the arguments are invalid. */
+size_t wise_cache_evict_workspace(const wise_paged_cache* cache, int32_t budget);
+
+/*
+ * wise_cache_evict -- keeps at most `budget` committed tokens of each sequence.
+ * Of a longer one, each key head keeps the first `sink` tokens, the last `recent`
+ * ones, and of those between the budget - sink - recent with the greatest weight
+ * (of equal ones those in lower slots; NaN counts as the least). Heads keep
+ * different tokens. Kept token number i of a head, in the order of the slots,
+ * goes to slot i of the pages that to_table names, in the same pools: key and
+ * value as they are (keys were rotated when they were appended), its weight to
+ * weights_out. A shorter sequence's tokens keep their slots.
+ *   weights    : float32 [batch, kv_heads, width].
+ *   budget >= 1, recent >= 0, sink >= 0, recent + sink <= budget,
+ *   budget <= to_pages * page.
+ *   to_table   : [batch, to_pages] int32. Pages that the call reads must not be
+ *                written, except that a sequence that keeps all its tokens may
+ *                name its own pages, in order (nothing of it moves then).
+ *   new_lengths: [batch] int32: min(lengths[b], budget).
+ *   weights_out: float32 [batch, kv_heads, width_out], width_out >= budget;
+ *                entries behind the kept tokens are zero.
+ *   workspace  : wise_cache_evict_workspace bytes (device, 16-byte aligned).
+ * The outputs and the workspace must not overlap each other or the inputs
+ * (refused), nor the pools one another. Drafted tokens behind the committed ones
+ * stay behind. Lengths that are negative, or past the page table or width, are
+ * clamped and flagged (WISE_ERR_BAD_CACHE); tokens whose page, or whose new one,
+ * lies outside [0, n_pages) do not move and are flagged. Two launches.
+ */
+int wise_cache_evict(const wise_paged_cache* cache, const float* weights, int64_t width, int32_t budget, int32_t recent,
+                     int32_t sink, const int32_t* to_table, int32_t to_pages, int32_t* new_lengths, float* weights_out,
+                     int64_t width_out, void* workspace, size_t workspace_bytes, wise_stream_t stream);
 
 /* Host-side check of a support CSR (host pointers): row_ptr monotone from 0,
  * every row strictly ascending with 0 <= b <= q, and, if the flags ask for
