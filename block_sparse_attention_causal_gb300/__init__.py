@@ -17,6 +17,8 @@ Language Models" (WISE):
   follows the prompt: a paged cache of keys and values, attention of a next
   token or of a tree of drafted tokens over it, and the drafted tokens that
   are kept;
+* :func:`prefix_attention` -- the same attention for a batch whose sequences
+  share long prefixes, each read once for all;
 * :func:`norm_rotate`, and the norms and axes of :func:`cache_append` --
   queries and keys normed per head and rotated in one pass;
 * :func:`cache_weights`, :func:`cache_evict` -- the attention weight that a
@@ -41,8 +43,8 @@ __all__ = ["discover", "select_support", "sparse", "Support", "device_status", "
            "select_finalize", "new_select_state",
            "WISE_SUPPORT_SINK", "WISE_SUPPORT_DIAG", "useful_flops", "dense_flops", "retained_mass",
            "support_jaccard", "select_control", "gather_plan", "PagedCache", "Rope", "rope_frequencies",
-           "pack_tree_mask", "cache_append", "tree_attention", "cache_accept", "norm_rotate", "cache_weights",
-           "cache_evict"]
+           "pack_tree_mask", "cache_append", "tree_attention", "prefix_attention", "cache_accept", "norm_rotate",
+           "cache_weights", "cache_evict"]
 
 _OUT = {torch.bfloat16: WISE_BF16, torch.float32: WISE_F32}
 _BF16, _I32 = torch.bfloat16, torch.int32
@@ -798,6 +800,66 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
         if own:
             torch._C._cuda_cudaCachingAllocator_raw_delete(own)
     _lib.check(st, "wise_attn_tree")
+    return out, (lse if want_lse else None)
+
+
+def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.Tensor, *,
+                     group_starts: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
+                     tree_mask: Optional[torch.Tensor] = None, want_lse: bool = True,
+                     out_dtype: torch.dtype = torch.bfloat16, scale: float = 0.0, out: Optional[torch.Tensor] = None,
+                     lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
+                     stream: Optional[torch.cuda.Stream] = None):
+    """:func:`tree_attention` for a batch whose sequences share prefixes: the
+    sequences of group g, group_starts[g] up to (not including) group_starts[g +
+    1] (int32 [groups + 1], ascending; default: one group of all), begin with
+    the same prefix_lengths[g] tokens (int32 [groups]), whose keys and values are
+    read once for all of them. The page table names the shared pages for each
+    sequence; whole tiles of 128 tokens are shared, the rest is read by each
+    sequence. Sequences outside the groups, or shorter than their group's
+    prefix, share nothing. Everything else is as in :func:`tree_attention`."""
+    desc, dev = _check_cache(cache)
+    handle = _check_stream(stream, dev)
+    lib = _lib.load()
+    b, d = desc.batch, desc.head_dim
+    qr = _check_rows("q", q, b, None, d, dev)
+    heads, n = q.shape[1], q.shape[2]
+    if heads % desc.kv_heads != 0:
+        raise ValueError("the cache's heads must divide q's heads")
+    if out_dtype not in _OUT:
+        raise ValueError("out_dtype must be torch.bfloat16 or torch.float32")
+    groups = prefix_lengths.shape[0] if isinstance(prefix_lengths, torch.Tensor) and prefix_lengths.dim() == 1 else 0
+    if not 1 <= groups <= b or (group_starts is None and groups != 1):
+        raise ValueError("prefix_lengths must be an int32 [groups] tensor of 1 to batch groups (one without group_starts)")
+    pre = _check_array("prefix_lengths", prefix_lengths, torch.int32, (groups,), dev)
+    starts = None if group_starts is None else _check_array("group_starts", group_starts, torch.int32, (groups + 1,), dev)
+    nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
+    mask = None if tree_mask is None else _check_array("tree_mask", tree_mask, torch.int32, (b, n, (n + 31) // 32), dev)
+    nbytes = lib.wise_attn_prefix_workspace(desc, heads, n, groups)
+    if out is None:
+        out = _empty((b, heads, n, d), out_dtype, q.device, stream)
+        o_ptr = out.data_ptr()
+    else:
+        o_ptr = _check_array("out", out, out_dtype, (b, heads, n, d), dev)
+    lse_ptr = None
+    if want_lse:
+        if lse is None:
+            lse = _empty((b, heads, n), torch.float32, q.device, stream)
+            lse_ptr = lse.data_ptr()
+        else:
+            lse_ptr = _check_array("lse", lse, torch.float32, (b, heads, n), dev)
+    own = 0
+    if workspace is not None:
+        _check_bytes("workspace", workspace, nbytes, q.device)
+        ws_ptr, nbytes = workspace.data_ptr(), workspace.numel()
+    else:
+        ws_ptr = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(nbytes, 16), handle)
+    try:
+        st = lib.wise_attn_prefix(desc, heads, n, qr, groups, starts, pre, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr,
+                                  ws_ptr, nbytes, handle)
+    finally:
+        if own:
+            torch._C._cuda_cudaCachingAllocator_raw_delete(own)
+    _lib.check(st, "wise_attn_prefix")
     return out, (lse if want_lse else None)
 
 

@@ -39,7 +39,7 @@ EXPORTS = (
     "wise_select_finalize", "wise_validate_schedule", "wise_wait_expiry_check", "wise_gather_plan_bytes",
     "wise_gather_plan", "wise_attn_sparse_planned", "wise_cache_append", "wise_attn_tree_workspace",
     "wise_attn_tree", "wise_cache_accept", "wise_cache_append_norm", "wise_norm_rotate", "wise_cache_weights",
-    "wise_cache_evict_workspace", "wise_cache_evict",
+    "wise_cache_evict_workspace", "wise_cache_evict", "wise_attn_prefix_workspace", "wise_attn_prefix",
 )
 
 
@@ -139,6 +139,9 @@ _SIGNATURES = {
     "wise_attn_tree_workspace": (_sz, [_cp, _i32, _i32]),
     "wise_attn_tree": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _sz, _vp]),
     "wise_cache_accept": (ctypes.c_int, [_cp, _i32, _vp, _vp, _vp, _vp]),
+    "wise_attn_prefix_workspace": (_sz, [_cp, _i32, _i32, _i32]),
+    "wise_attn_prefix": (ctypes.c_int, [_cp, _i32, _i32, _rp, _i32, _vp, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp,
+                                        _sz, _vp]),
     "wise_cache_append_norm": (ctypes.c_int, [_cp, _i32, _rp, _rp, _i32, _rp, _vp, _vp, _vp, _op, _np, _vp]),
     "wise_norm_rotate": (ctypes.c_int, [_i32, _i32, _i32, _i32, _rp, _vp, _i32, _rp, _vp, _vp, _op, _np, _vp]),
     "wise_cache_weights": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, _vp, ctypes.c_float, _vp, _i64, _vp]),

@@ -21,9 +21,9 @@ LIB_DIR = os.path.join(PKG_DIR, "lib")
 LIB_PATH = os.path.join(LIB_DIR, "libwise.so")
 
 SOURCES = ["wise_api.cu", "select_kernel.cu", "diag_kernel.cu", "gather_plan.cu", "cache_kernel.cu", "tree_kernel.cu",
-           "tree_narrow.cu", "norm_kernel.cu", "weights_kernel.cu", "evict_kernel.cu", "attn_d64.cu", "attn_d96.cu", "attn_d128.cu"]
+           "tree_narrow.cu", "prefix_kernel.cu", "prefix_narrow.cu", "norm_kernel.cu", "weights_kernel.cu", "evict_kernel.cu", "attn_d64.cu", "attn_d96.cu", "attn_d128.cu"]
 HEADERS = ["ptx.cuh", "attn_kernel.cuh", "internal.h", "select_step.cuh", "select_keys.cuh", "gather.cuh", "rotate.cuh",
-           "tree.cuh"]
+           "tree.cuh", "tree_wide.cuh", "tree_narrow.cuh"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ARCH + ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 

@@ -197,7 +197,7 @@ struct AcceptLaunch {
 };
 cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream);
 
-// Attention of new tokens over a paged cache (tree_kernel.cu). The key
+// Attention of new tokens over a paged cache (tree_wide.cuh, tree_narrow.cuh). The key
 // tiles and kTreeOverhead places of each unit must number at most 2^31 - 1.
 constexpr int kTreeMaxTokens = 128;
 constexpr int kTreeOverhead = 8;  // at most this many places of the line of work per unit, besides its key tiles
@@ -213,6 +213,12 @@ struct TreeLaunch {
   float* lse;
   void* workspace;
   uint32_t* err;
+  const int32_t* skip;    // null, or [batch]: tokens at the front of each sequence that are left out
+  // for groups of sequences over what they share: cache.batch counts groups, cache.lengths
+  // are their shared tokens, cache.page_table and the rest are the sequences'
+  const int32_t* starts;  // [groups + 1]: each group's first sequence
+  const int32_t* leader;  // [groups]: the sequence whose page table is read
+  int32_t sequences;      // of all groups, at most
 };
 int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim);
 // maps = {K, V}: 3-D tensor maps [n_pages, kv_heads * page, d] with boxes of one
@@ -262,6 +268,17 @@ struct EvictLaunch {
 };
 int64_t evict_move_chunks(int64_t budget, int64_t width_out);
 cudaError_t launch_evict(const EvictLaunch& e, cudaStream_t stream);
+
+// Attention of a batch whose sequences share prefixes (prefix_kernel.cu): t as for
+// launch_tree, with the whole call's workspace.
+struct PrefixLaunch {
+  TreeLaunch t;
+  int32_t groups;
+  const int32_t* group_starts;  // [groups + 1] or null: one group of all sequences
+  const int32_t* prefix_lengths;  // [groups]
+};
+int64_t prefix_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim, int32_t groups);
+cudaError_t launch_prefix(const PrefixLaunch& p, const CUtensorMap* maps, cudaStream_t stream);
 
 // Attention weight of new tokens, summed per cached token (weights_kernel.cu).
 struct WeightsLaunch {

@@ -67,29 +67,51 @@ __device__ __forceinline__ void copy16(void* dst, const void* src) {
 }
 __device__ __forceinline__ void copy16_wait() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
+// Tokens at the front of sequence b that are left out (whole tiles).
+__device__ __forceinline__ int seq_skip(const TreeLaunch& t, int b) { return t.skip ? t.skip[b] : 0; }
+
 // Committed and new tokens of sequence b, clamped to what the page table
-// holds; true if nothing had to be clamped.
+// holds; true if nothing had to be clamped. PREFIX: shared tokens and rows
+// (tokens of all its sequences) of group b.
+template <bool PREFIX>
 __device__ __forceinline__ bool seq_counts(const TreeLaunch& t, int b, int& len, int& nl) {
-  const int64_t cap = (int64_t)t.cache.max_pages << t.cache.page_shift;
-  const int64_t l0 = t.cache.lengths[b];
-  const int n0 = t.new_len ? t.new_len[b] : t.n;
-  const int64_t l = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
-  int n = n0 < 0 ? 0 : (n0 > t.n ? t.n : n0);
-  if (l + n > cap) n = (int)(cap - l);
-  len = (int)l;
-  nl = n;
-  return l == l0 && n == n0;
+  if constexpr (PREFIX) {
+    len = t.cache.lengths[b];
+    nl = len > 0 ? (t.starts[b + 1] - t.starts[b]) * t.n : 0;
+    return true;
+  } else {
+    const int64_t cap = (int64_t)t.cache.max_pages << t.cache.page_shift;
+    const int64_t l0 = t.cache.lengths[b];
+    const int n0 = t.new_len ? t.new_len[b] : t.n;
+    const int64_t l = l0 < 0 ? 0 : (l0 > cap ? cap : l0);
+    int n = n0 < 0 ? 0 : (n0 > t.n ? t.n : n0);
+    if (l + n > cap) n = (int)(cap - l);
+    len = (int)l - seq_skip(t, b);
+    nl = n;
+    return l == l0 && n == n0;
+  }
+}
+// The page table's entries of sequence b (of group b: of the sequence that stands for it) from
+// the first token on that is not left out.
+template <bool PREFIX>
+__device__ __forceinline__ const int32_t* seq_table(const TreeLaunch& t, int b) {
+  if constexpr (PREFIX) return t.cache.page_table + (int64_t)t.leader[b] * t.cache.max_pages;
+  else return t.cache.page_table + (int64_t)b * t.cache.max_pages + (seq_skip(t, b) >> t.cache.page_shift);
 }
 // Key tiles (`full`) of a unit that holds a valid token's row, and how many
-// units of a key head do (`active`); each other unit counts one empty tile.
+// units of a key head do (`active`); each other unit counts one empty tile
+// (PREFIX: there are no others).
+template <bool PREFIX>
 __device__ __forceinline__ void seq_tiles(const TreeParams& p, int len, int nl, int& full, int& active) {
-  const int keys = len + nl;
+  const int keys = PREFIX ? len : len + nl;
   full = keys > 0 ? (keys + kTile - 1) / kTile : 1;
   active = (nl * p.group + 255) / 256;
   if (active > p.pairs) active = p.pairs;
 }
+template <bool PREFIX>
 __device__ __forceinline__ int seq_line(const TreeParams& p, int full, int active) {
-  return p.t.cache.kv_heads * (active * full + (p.pairs - active) + p.pairs * p.overhead);
+  if constexpr (PREFIX) return p.t.cache.kv_heads * active * (full + p.overhead);
+  else return p.t.cache.kv_heads * (active * full + (p.pairs - active) + p.pairs * p.overhead);
 }
 
 // The line as one CTA sees it: CTA c's part begins at place c * per + c * more
@@ -128,7 +150,7 @@ __device__ __forceinline__ void prefetch_tables(const TreeParams& p) {
 // Every thread sums the tiles of consecutive sequences, the block scans the
 // sums, and the thread whose sequences hold the part's first tile finds it
 // there. Two block barriers; `scratch` holds warps + 12 words.
-template <int THREADS>
+template <int THREADS, bool PREFIX = false>
 __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, LinePart& part) {
   constexpr int WARPS = THREADS / 32;
   int* sums = scratch;
@@ -142,9 +164,9 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
   bool good = true;
   for (int b = b_lo; b < b_hi; ++b) {
     int fl, ac;
-    good &= seq_counts(p.t, b, last_len, last_nl);
-    seq_tiles(p, last_len, last_nl, fl, ac);
-    mine += seq_line(p, fl, ac);
+    good &= seq_counts<PREFIX>(p.t, b, last_len, last_nl);
+    seq_tiles<PREFIX>(p, last_len, last_nl, fl, ac);
+    mine += seq_line<PREFIX>(p, fl, ac);
   }
   if (!good && blockIdx.x == 0) atomicOr(p.t.err, kErrBadCache);
   int before = mine;
@@ -165,7 +187,7 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
     total += sums[w];
   }
   const int cta = blockIdx.x;
-  part.ctas = min((int)gridDim.x, total);
+  part.ctas = PREFIX ? max(min((int)gridDim.x, total), 1) : min((int)gridDim.x, total);
   part.per = total / part.ctas;
   part.more = total - part.per * part.ctas;
   const int x0 = cta < part.ctas ? part.begin(cta) : total;
@@ -174,9 +196,9 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
     int at = before;
     for (int b = b_lo; b < b_hi; ++b) {
       int len = last_len, nl = last_nl, fl, ac;
-      if (b + 1 < b_hi) seq_counts(p.t, b, len, nl);
-      seq_tiles(p, len, nl, fl, ac);
-      const int line = seq_line(p, fl, ac);
+      if (b + 1 < b_hi) seq_counts<PREFIX>(p.t, b, len, nl);
+      seq_tiles<PREFIX>(p, len, nl, fl, ac);
+      const int line = seq_line<PREFIX>(p, fl, ac);
       if (x0 >= at && x0 < at + line) {
         const int ov = p.overhead, per_head = line / p.t.cache.kv_heads;
         const int hk = (x0 - at) / per_head;
@@ -213,8 +235,9 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
 
 // A CTA's walk over its part, a segment (consecutive key tiles of one unit) at
 // a time. Every role keeps its own.
-struct Walk {
-  int b, hk, pair;
+template <bool PREFIX>
+struct WalkOf {
+  int b, hk, pair;  // PREFIX: b is a group
   int len, nl, full, active;
   int t0, t1, nt;  // tiles [t0, t1) of the unit's nt
   int keys;        // tokens that the unit's rows may see
@@ -224,7 +247,7 @@ struct Walk {
   __device__ __forceinline__ void unit() {
     const bool on = pair < active;
     nt = on ? full : 1;
-    keys = on ? len + nl : 0;
+    keys = on ? (PREFIX ? len : len + nl) : 0;
     t1 = min(nt, t0 + left);
   }
   __device__ __forceinline__ void start(const TreeParams& p, const LinePart& f) {
@@ -236,7 +259,7 @@ struct Walk {
     t0 = f.t0;
     left = f.left;
     seg = 0;
-    seq_tiles(p, len, nl, full, active);
+    seq_tiles<PREFIX>(p, len, nl, full, active);
     unit();
   }
   __device__ __forceinline__ bool next(const TreeParams& p) {
@@ -244,13 +267,15 @@ struct Walk {
     if (left <= 0) return false;
     ++seg;
     t0 = 0;
-    if (++pair == p.pairs) {
+    if (++pair == (PREFIX ? active : p.pairs)) {
       pair = 0;
       if (++hk == p.t.cache.kv_heads) {
         hk = 0;
-        ++b;
-        seq_counts(p.t, b, len, nl);
-        seq_tiles(p, len, nl, full, active);
+        do {
+          ++b;
+          seq_counts<PREFIX>(p.t, b, len, nl);
+          seq_tiles<PREFIX>(p, len, nl, full, active);
+        } while (PREFIX && active == 0);  // (places are left, so a group with rows follows)
       }
     }
     unit();
@@ -260,7 +285,28 @@ struct Walk {
   // partial result of this segment: 2 c for the part's first segment, 2 c + 1
   // for its last
   __device__ __forceinline__ int part() const { return 2 * (int)blockIdx.x + (seg == 0 ? 0 : 1); }
+  // rows of the sequence (of the group) and key head
+  __device__ __forceinline__ int rows(const TreeParams& p) const { return PREFIX ? nl * p.group : p.rows; }
 };
+using Walk = WalkOf<false>;
+
+// A row's sequence and token: `tok` counts the tokens of all of a group's
+// sequences with PREFIX (tok < nl: the group has such a row).
+struct RowPlace {
+  int b, i;
+};
+template <bool PREFIX>
+__device__ __forceinline__ RowPlace row_place(const TreeLaunch& t, int b, int tok) {
+  if constexpr (!PREFIX) return RowPlace{b, tok};
+  const int m = tok / t.n;
+  return RowPlace{t.starts[b] + m, tok - m * t.n};
+}
+// Whether the row's token is one of its sequence's new ones.
+template <bool PREFIX>
+__device__ __forceinline__ bool row_live(const TreeLaunch& t, const RowPlace& r, int tok, int nl) {
+  if (tok >= nl) return false;
+  return !PREFIX || !t.new_len || r.i < t.new_len[r.b];
+}
 
 // The join record of the unit whose first tile lies in this segment (one
 // thread calls it for every segment, and first clear_rec).
@@ -271,7 +317,8 @@ __device__ __forceinline__ void clear_rec(const TreeParams& p) {
 __device__ __forceinline__ void clear_recs(const TreeParams& p) {
   for (int i = threadIdx.x; i < p.recs; i += blockDim.x) p.rec[i].parts = 0;
 }
-__device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const Walk& w) {
+template <bool PREFIX>
+__device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const WalkOf<PREFIX>& w) {
   if (w.t0 != 0) return;
   const bool cut = w.t1 < w.nt;
   JoinRec r = {1, 0, (int)blockIdx.x, w.b, w.hk, w.pair, 0, 0};
@@ -399,8 +446,8 @@ __device__ __forceinline__ uint32_t tile_bad(const Ring& ring, uint32_t tile, vo
 
 // The warp that loads the ring, page by page (whole warp; lane i issues the
 // tile's page i).
-template <int D, int NS, int TAG>
-__device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const Ring& ring, const CUtensorMap* tm_k,
+template <int D, int NS, int TAG, bool PREFIX>
+__device__ __forceinline__ void ring_producer(const TreeParams& p, WalkOf<PREFIX> w, const Ring& ring, const CUtensorMap* tm_k,
                                               const CUtensorMap* tm_v, volatile int* abort_flag, int lane) {
   using C = RingCfg<D, NS>;
   uint32_t* err = p.t.err;
@@ -410,7 +457,7 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
   uint32_t pos = 0;
   bool ok = true, flagged = false;
   do {
-    const int32_t* table = p.t.cache.page_table + (int64_t)w.b * p.t.cache.max_pages;
+    const int32_t* table = seq_table<PREFIX>(p.t, w.b);
     const int last_page = (w.keys - 1) >> p.t.cache.page_shift;  // -1: none
     // the lanes hold 32 columns of the page table from `have` on, and the 32
     // after them, which are under way while these are used
@@ -470,8 +517,8 @@ __device__ __forceinline__ void ring_producer(const TreeParams& p, Walk w, const
 // names those tokens; their values are put back at the end for the rows that
 // see them. The ring holds fewer than kNfRing tiles, so a list is not reused
 // before its segment's results are out.
-template <int D, int NS, int TAG>
-__device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ring& ring, uint32_t* nf,
+template <int D, int NS, int TAG, bool PREFIX>
+__device__ __forceinline__ void ring_guard(const TreeParams& p, WalkOf<PREFIX> w, const Ring& ring, uint32_t* nf,
                                            volatile int* abort_flag, int lane) {
   using C = RingCfg<D, NS>;
   static_assert(NS / 2 + 2 < kNfRing && NS / 2 + 4 < kTileFlags, "nf ring, tile flags");
@@ -539,13 +586,22 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, Walk w, const Ri
 // Row pointer of drafted token j's values in the pool, or null.
 __device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {
   const int64_t tok = (int64_t)len + j;
-  const int32_t pg = t.cache.page_table[(int64_t)b * t.cache.max_pages + (tok >> t.cache.page_shift)];
+  const int32_t pg = seq_table<false>(t, b)[tok >> t.cache.page_shift];
   if (!page_ok(t, pg)) return nullptr;
   return t.cache.v_pages + ((((int64_t)pg * t.cache.kv_heads + hk) << t.cache.page_shift) +
                             (tok & ((1 << t.cache.page_shift) - 1))) * d;
 }
 
-// tree_narrow.cu: up to 64 rows per unit.
+// Up to 64 rows per unit (tree_narrow.cuh), and more (tree_wide.cuh, with the
+// join of either's partial results). PREFIX: the rows of a group of sequences
+// over the tokens that they share.
+template <bool PREFIX>
 cudaError_t launch_tree_narrow(const TreeParams& p, const CUtensorMap* maps, cudaStream_t stream);
+template <bool PREFIX>
+cudaError_t launch_tree_rows(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream);
+extern template cudaError_t launch_tree_narrow<false>(const TreeParams&, const CUtensorMap*, cudaStream_t);
+extern template cudaError_t launch_tree_narrow<true>(const TreeParams&, const CUtensorMap*, cudaStream_t);
+extern template cudaError_t launch_tree_rows<false>(const TreeLaunch&, const CUtensorMap*, cudaStream_t);
+extern template cudaError_t launch_tree_rows<true>(const TreeLaunch&, const CUtensorMap*, cudaStream_t);
 
 }  // namespace wise

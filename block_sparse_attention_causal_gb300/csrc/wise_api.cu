@@ -358,6 +358,69 @@ int check_tree(const wise_paged_cache* c, int32_t heads, int32_t new_tokens) {
   return WISE_OK;
 }
 
+int check_prefix(const wise_paged_cache* c, int32_t heads, int32_t new_tokens, int32_t groups) {
+  const int st = check_tree(c, heads, new_tokens);
+  if (st != WISE_OK) return st;
+  if (groups < 1 || groups > c->batch) return WISE_ERR_INVALID_ARGUMENT;
+  // rows of a group, divided by the heads of a key head by multiplication; and
+  // the key tiles of all groups' units
+  const int64_t group = heads / c->kv_heads, rows = (int64_t)c->batch * group * new_tokens;
+  const int64_t units = (rows / 256 + groups) * c->kv_heads;
+  const int64_t tiles = ((int64_t)c->max_pages * c->page + 127) / 128 + kTreeOverhead;
+  return rows * group > UINT32_MAX || units > INT32_MAX / tiles ? WISE_ERR_UNSUPPORTED : WISE_OK;
+}
+
+// The arguments of wise_attn_tree and wise_attn_prefix, and their launch's.
+int tree_launch(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, const int32_t* new_len,
+                const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse, void* workspace,
+                size_t workspace_bytes, size_t need, TreeLaunch& t) {
+  int st;
+  if (!o || (out_dtype != WISE_BF16 && out_dtype != WISE_F32) || !(scale >= 0.f) || isinf(scale))
+    return WISE_ERR_INVALID_ARGUMENT;
+  if ((st = check_rows(q)) != WISE_OK) return st;
+  if (!aligned16(o) || misaligned4(lse) || misaligned4(new_len) || misaligned4(tree_mask)) return WISE_ERR_ALIGNMENT;
+  if (!workspace || workspace_bytes < need) return WISE_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return WISE_ERR_ALIGNMENT;
+  {
+    // results and partial results are written while other blocks still read
+    const int64_t batch = cache->batch, d = cache->head_dim, n = new_tokens, rows = batch * heads * n;
+    const struct {
+      const void* at;
+      int64_t bytes;
+    } outs[3] = {{o, rows * d * (out_dtype == WISE_F32 ? 4 : 2)},
+                 {lse, rows * 4},
+                 {workspace, (int64_t)need}};
+    for (int i = 0; i < 3; ++i) {
+      const void* at = outs[i].at;
+      const int64_t bytes = outs[i].bytes;
+      if (overlap_cache(cache, at, bytes) || overlap_rows(q, batch, heads, n, d, at, bytes) ||
+          overlap(at, bytes, new_len, batch * 4) || overlap(at, bytes, tree_mask, batch * n * ((n + 31) / 32) * 4) ||
+          overlap(at, bytes, outs[(i + 1) % 3].at, outs[(i + 1) % 3].bytes))
+        return WISE_ERR_INVALID_ARGUMENT;
+    }
+  }
+  memset(&t, 0, sizeof(t));
+  t.err = error_word();
+  if (!t.err) return WISE_ERR_CUDA;
+  t.cache = cache_view(cache);
+  t.head_dim = cache->head_dim;
+  t.heads = heads;
+  t.n = new_tokens;
+  t.q = rows_view(q);
+  t.new_len = new_len;
+  t.tree_mask = tree_mask;
+  t.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)cache->head_dim);
+  t.out_f32 = out_dtype == WISE_F32;
+  t.o = o;
+  t.lse = lse;
+  t.workspace = workspace;
+  return WISE_OK;
+}
+int tree_maps(CUtensorMap (&maps)[2], const wise_paged_cache* cache) {
+  const int st = encode_pages(&maps[0], cache->k_pages, cache);
+  return st == WISE_OK ? encode_pages(&maps[1], cache->v_pages, cache) : st;
+}
+
 // The weights and rotation of wise_cache_append_norm and wise_norm_rotate.
 int check_norm(const wise_rope* r, const wise_head_norm* n, int64_t heads, int64_t kv_heads, int32_t d,
                const int32_t* positions) {
@@ -883,51 +946,49 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
   int st = check_cache(cache, true);
   if (st != WISE_OK) return st;
   if ((st = check_tree(cache, heads, new_tokens)) != WISE_OK) return st;
-  if (!o || (out_dtype != WISE_BF16 && out_dtype != WISE_F32) || !(scale >= 0.f) || isinf(scale))
-    return WISE_ERR_INVALID_ARGUMENT;
-  if ((st = check_rows(q)) != WISE_OK) return st;
-  if (!aligned16(o) || misaligned4(lse) || misaligned4(new_len) || misaligned4(tree_mask)) return WISE_ERR_ALIGNMENT;
-  if (!workspace || workspace_bytes < wise_attn_tree_workspace(cache, heads, new_tokens)) return WISE_ERR_WORKSPACE;
-  if (!aligned16(workspace)) return WISE_ERR_ALIGNMENT;
-  {
-    // results and partial results are written while other blocks still read
-    const int64_t batch = cache->batch, d = cache->head_dim, n = new_tokens, rows = batch * heads * n;
-    const struct {
-      const void* at;
-      int64_t bytes;
-    } outs[3] = {{o, rows * d * (out_dtype == WISE_F32 ? 4 : 2)},
-                 {lse, rows * 4},
-                 {workspace, (int64_t)wise_attn_tree_workspace(cache, heads, new_tokens)}};
-    for (int i = 0; i < 3; ++i) {
-      const void* at = outs[i].at;
-      const int64_t bytes = outs[i].bytes;
-      if (overlap_cache(cache, at, bytes) || overlap_rows(q, batch, heads, n, d, at, bytes) ||
-          overlap(at, bytes, new_len, batch * 4) || overlap(at, bytes, tree_mask, batch * n * ((n + 31) / 32) * 4) ||
-          overlap(at, bytes, outs[(i + 1) % 3].at, outs[(i + 1) % 3].bytes))
-        return WISE_ERR_INVALID_ARGUMENT;
-    }
-  }
   TreeLaunch t;
-  memset(&t, 0, sizeof(t));
-  t.err = error_word();
-  if (!t.err) return WISE_ERR_CUDA;
-  t.cache = cache_view(cache);
-  t.head_dim = cache->head_dim;
-  t.heads = heads;
-  t.n = new_tokens;
-  t.q = rows_view(q);
-  t.new_len = new_len;
-  t.tree_mask = tree_mask;
-  t.scale = scale > 0.f ? scale : 1.0f / sqrtf((float)cache->head_dim);
-  t.out_f32 = out_dtype == WISE_F32;
-  t.o = o;
-  t.lse = lse;
-  t.workspace = workspace;
-  CUtensorMap maps[2];
-  st = encode_pages(&maps[0], cache->k_pages, cache);
-  if (st == WISE_OK) st = encode_pages(&maps[1], cache->v_pages, cache);
+  st = tree_launch(cache, heads, new_tokens, q, new_len, tree_mask, scale, out_dtype, o, lse, workspace, workspace_bytes,
+                   wise_attn_tree_workspace(cache, heads, new_tokens), t);
   if (st != WISE_OK) return st;
+  CUtensorMap maps[2];
+  if ((st = tree_maps(maps, cache)) != WISE_OK) return st;
   return launch_tree(t, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
+}
+
+size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, int32_t groups) {
+  if (check_cache(cache, false) != WISE_OK || check_prefix(cache, heads, new_tokens, groups) != WISE_OK) return 0;
+  return (size_t)prefix_workspace_bytes(cache->batch, cache->kv_heads, heads, new_tokens, cache->head_dim, groups);
+}
+
+int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, int32_t groups,
+                     const int32_t* group_starts, const int32_t* prefix_lengths, const int32_t* new_len,
+                     const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, wise_stream_t stream) {
+  int st = check_cache(cache, true);
+  if (st != WISE_OK) return st;
+  if ((st = check_prefix(cache, heads, new_tokens, groups)) != WISE_OK) return st;
+  if (!prefix_lengths || (!group_starts && groups != 1)) return WISE_ERR_INVALID_ARGUMENT;
+  if (misaligned4(group_starts) || misaligned4(prefix_lengths)) return WISE_ERR_ALIGNMENT;
+  const size_t need = wise_attn_prefix_workspace(cache, heads, new_tokens, groups);
+  PrefixLaunch p;
+  memset(&p, 0, sizeof(p));
+  st = tree_launch(cache, heads, new_tokens, q, new_len, tree_mask, scale, out_dtype, o, lse, workspace, workspace_bytes, need,
+                   p.t);
+  if (st != WISE_OK) return st;
+  const int64_t rows = (int64_t)cache->batch * heads * new_tokens;
+  const struct {
+    const void* at;
+    int64_t bytes;
+  } outs[3] = {{o, rows * cache->head_dim * (out_dtype == WISE_F32 ? 4 : 2)}, {lse, rows * 4}, {workspace, (int64_t)need}};
+  for (const auto& x : outs)
+    if (overlap(x.at, x.bytes, group_starts, ((int64_t)groups + 1) * 4) || overlap(x.at, x.bytes, prefix_lengths, (int64_t)groups * 4))
+      return WISE_ERR_INVALID_ARGUMENT;
+  p.groups = groups;
+  p.group_starts = group_starts;
+  p.prefix_lengths = prefix_lengths;
+  CUtensorMap maps[2];
+  if ((st = tree_maps(maps, cache)) != WISE_OK) return st;
+  return launch_prefix(p, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;
 }
 
 int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,

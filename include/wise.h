@@ -32,6 +32,8 @@
  *                        next token, a run of tokens, or a tree of drafted
  *                        tokens each of which sees the cache and its own
  *                        ancestors;
+ *   wise_attn_prefix     the same for a batch whose sequences share long
+ *                        prefixes: what is shared is read once for all;
  *   wise_cache_accept    the drafted tokens that are kept become the cache's
  *                        own;
  *   wise_cache_append_norm, wise_norm_rotate
@@ -543,6 +545,37 @@ int wise_attn_tree(const wise_paged_cache* cache, int32_t heads, int32_t new_tok
  */
 int wise_cache_accept(const wise_paged_cache* cache, int32_t path_tokens, const int32_t* path,
                       const int32_t* n_accepted, int32_t* new_lengths, wise_stream_t stream);
+
+/* Bytes of workspace wise_attn_prefix needs; 0 when the arguments are invalid.
+ * Reads no device memory (cache pointers may be NULL). */
+size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, int32_t groups);
+
+/*
+ * wise_attn_prefix -- wise_attn_tree for a batch whose sequences share prefixes:
+ * the caller says that the sequences of group g, group_starts[g] up to (not
+ * including) group_starts[g + 1], begin with the same prefix_lengths[g] tokens.
+ * Their keys and values are read once, through the page table of one of the
+ * sequences, for the rows of all. Results, arguments and refusals are those of
+ * wise_attn_tree over the same cache (a page table names the shared pages for
+ * each sequence, as ever), but for the order of sums: a row's shared and own
+ * parts are taken apart and joined in fp32.
+ *   groups         : 1 <= groups <= batch.
+ *   group_starts   : [groups + 1] int32, ascending (not strictly), in
+ *                    [0, batch]; sequences outside share nothing. NULL: one
+ *                    group of all sequences (groups 1).
+ *   prefix_lengths : [groups] int32. Whole tiles of 128 tokens are read
+ *                    together, the rest by each sequence. Sequences with fewer
+ *                    committed tokens share nothing (an empty place of a padded
+ *                    batch).
+ *   workspace      : wise_attn_prefix_workspace bytes.
+ * group_starts that are not ascending or out of range are flagged, and nothing
+ * is shared then; prefix_lengths below 0 or past the page table are flagged, and
+ * their groups share nothing (WISE_ERR_BAD_CACHE). Six launches.
+ */
+int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, int32_t groups,
+                     const int32_t* group_starts, const int32_t* prefix_lengths, const int32_t* new_len,
+                     const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse, void* workspace,
+                     size_t workspace_bytes, wise_stream_t stream);
 
 /* Norm of each head's values before the rotation:
  *     y = x / sqrt(mean(x^2) + eps) * w     (mean over head_dim values)
