@@ -245,6 +245,7 @@ struct NormLaunch {
   int64_t q_weight_stride, k_weight_stride;  // elements from head to head (0: shared)
   int32_t weight_f32;
   float eps;
+  int32_t part_heads, parts[2];  // set by launch_norm: heads of a block, blocks of q's and of k's
   uint32_t* err;
 };
 cudaError_t launch_norm(const NormLaunch& a, cudaStream_t stream);

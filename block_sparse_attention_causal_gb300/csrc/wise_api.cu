@@ -242,6 +242,7 @@ uint8_t* select_scratch() {
 // ------------------------------------------------------------- paged cache
 
 constexpr int64_t kMaxCacheTokens = 1ll << 30;  // per sequence
+constexpr int64_t kMaxNormHeads = 1ll << 18;    // of queries, keys and values together, of a call with norms
 
 // The shape of a cache; with `pointers`, its buffers too.
 int check_cache(const wise_paged_cache* c, bool pointers) {
@@ -1023,7 +1024,7 @@ int wise_cache_append_norm(const wise_paged_cache* cache, int32_t new_tokens, co
   if (st != WISE_OK) return st;
   if (new_tokens < 1 || (q && (heads < 1 || !q_out))) return WISE_ERR_INVALID_ARGUMENT;
   if (new_tokens > kMaxCacheTokens || (int64_t)cache->batch * new_tokens > INT32_MAX ||
-      2 * (int64_t)cache->kv_heads + (q ? heads : 0) > INT32_MAX)
+      2 * (int64_t)cache->kv_heads + (q ? heads : 0) > kMaxNormHeads)
     return WISE_ERR_UNSUPPORTED;
   const int64_t batch = cache->batch, d = cache->head_dim, n = new_tokens;
   if ((st = check_norm(rope, norm, q ? heads : 0, cache->kv_heads, cache->head_dim, positions)) != WISE_OK) return st;
@@ -1071,7 +1072,7 @@ int wise_norm_rotate(int32_t batch, int32_t new_tokens, int32_t head_dim, int32_
   if (head_dim != 64 && head_dim != 96 && head_dim != 128) return WISE_ERR_UNSUPPORTED;
   if (!k) kv_heads = 0;
   const int64_t b = batch, n = new_tokens, d = head_dim;
-  if (b * n > INT32_MAX || (int64_t)heads + kv_heads > INT32_MAX || b * n > INT64_MAX / 2 / d / ((int64_t)heads + kv_heads))
+  if (b * n > INT32_MAX || (int64_t)heads + kv_heads > kMaxNormHeads || b * n > INT64_MAX / 2 / d / ((int64_t)heads + kv_heads))
     return WISE_ERR_UNSUPPORTED;
   int st;
   if ((st = check_norm(rope, norm, heads, kv_heads, head_dim, positions)) != WISE_OK) return st;
