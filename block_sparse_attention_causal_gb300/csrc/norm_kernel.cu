@@ -325,7 +325,6 @@ cudaError_t launch_norm_d(NormLaunch a, cudaStream_t stream) {
                        : (a.pairs ? norm_kernel<D, true, 1> : norm_kernel<D, false, 1>);
   const size_t smem = (staged ? kStages * 2 * 256 * sizeof(uint4) : 0) +
                       (a.q_weight_stride != 0 || a.k_weight_stride != 0 ? (size_t)each * D * sizeof(float) : 0);
-  if (smem > 48 * 1024) cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   return launch_chained(kernel, grid, dim3(256), smem, stream, a);
 }
 

@@ -10,15 +10,18 @@
 // lies behind the last token, or in a key that a row does not see, has no way
 // into a sum. More than 256 rows are further launches, one after the other.
 //
-// Warp roles (384 threads): 0 TMA (a ring of K tiles), 1 MMA issue, 2 and 3 Q
-// and what belongs to it, 4-7 and 8-11 sums of alternate tiles, one key per thread.
+// Warp roles (640 threads): 0 TMA (a ring of K tiles), 1 MMA issue, 2 and 3 Q
+// and what belongs to it, then four groups of four warps that sum every fourth tile,
+// one key per thread (with two groups, the sums' latency took longer than the bytes
+// of K: 128 rows over 131K tokens 57 us instead of XX).
 // The key tiles of all (sequence, key head) units form the line of tree.cuh.
 #include "tree.cuh"
 
 namespace wise {
 namespace {
 
-constexpr int kThreads = 384;
+constexpr int kGroups = 4;  // of four warps that sum
+constexpr int kThreads = 128 + 128 * kGroups;
 constexpr int kMaxRows = 256;
 constexpr int kMaxSlots = 6;
 constexpr uint32_t kSmem = 232448u;
@@ -29,20 +32,22 @@ struct WeightsParams {
   float* weights;
   int64_t width;
   int32_t row0, nrows;  // this launch's rows of a unit
-  int32_t cols;         // nrows in whole blocks of 16
+  int32_t cols;         // nrows in whole blocks of 16, of 32 where there are more than 128
+  int32_t half;         // columns of one MMA: cols, or half of them
   int32_t slots;        // ring
+  int32_t q_bufs;       // buffers of Q
   uint32_t tmem_cols;
 };
 
-// Behind the ring and two Q buffers of `cols` rows:
+// Behind the ring and the Q buffers of `cols` rows:
 struct Small {
-  float lse2[2][kMaxRows];                // of even and odd segments: LSE in powers of two, +inf: the row adds nothing
+  float neg_lse2[2][kMaxRows];            // of a segment (its Q's buffer): -LSE in powers of two, -inf: the row adds nothing
   uint32_t words[2][kTreeMaxTokens * 4];  // [token][new token / 32]: who sees whom
   int plain[2][2];                        // rows from 0 on that all count, as either of its warps found
   uint64_t q_full[2];   // Q, lse2 and words of a segment are there (2 warps)
-  uint64_t seg_done[2];  // and no longer needed (8 warps)
-  uint64_t s_full[2];    // scores computed
-  uint64_t s_empty[2];   // and read (4 warps)
+  uint64_t seg_done[2];         // and no longer needed (all warps that sum)
+  uint64_t s_full[kGroups];     // a group's scores computed
+  uint64_t s_empty[kGroups];    // and read (4 warps)
   uint64_t full[kMaxSlots], empty[kMaxSlots];
   uint64_t drain;
   uint32_t flags[kTileFlags];
@@ -52,14 +57,14 @@ struct Small {
 };
 constexpr uint32_t kRoom = kSmem - (uint32_t)sizeof(Small);
 
-__device__ __forceinline__ void add8(const float* lse2, const uint32_t* s, float sl2, uint64_t (&sum)[2]) {
+__device__ __forceinline__ void add8(const float* neg_lse2, const uint32_t* s, float sl2, uint64_t (&sum)[2]) {
   const uint64_t sc = f2_pack(sl2, sl2);
 #pragma unroll
   for (int c = 0; c < 8; c += 4) {
-    const float4 l = *reinterpret_cast<const float4*>(lse2 + c);
+    const ulonglong2 l = *reinterpret_cast<const ulonglong2*>(neg_lse2 + c);
     float e0, e1, e2, e3;
-    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, f2_pack(-l.x, -l.y)), e0, e1);
-    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, f2_pack(-l.z, -l.w)), e2, e3);
+    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c]), __uint_as_float(s[c + 1])), sc, l.x), e0, e1);
+    f2_unpack(ffma2(f2_pack(__uint_as_float(s[c + 2]), __uint_as_float(s[c + 3])), sc, l.y), e2, e3);
     sum[0] = fadd2(sum[0], f2_pack(fast_exp2(e0), fast_exp2(e1)));
     sum[1] = fadd2(sum[1], f2_pack(fast_exp2(e2), fast_exp2(e3)));
   }
@@ -73,7 +78,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   constexpr uint32_t KV_BYTES = tile_bytes<D>(kTile);
   const uint32_t q_bytes = tile_bytes<D>(a.cols);
   uint8_t* sq = smem + a.slots * KV_BYTES;
-  Small& m = *reinterpret_cast<Small*>(sq + 2 * q_bytes);
+  Small& m = *reinterpret_cast<Small*>(sq + a.q_bufs * q_bytes);
   uint32_t* err = p.t.err;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if ((smem_u32(smem) & 1023u) != 0u) {  // swizzled tiles
@@ -84,7 +89,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 32) {
     for (int i = 0; i < 2; ++i) {
       mbar_init(&m.q_full[i], 2);
-      mbar_init(&m.seg_done[i], 8);
+      mbar_init(&m.seg_done[i], 4 * kGroups);
+    }
+    for (int i = 0; i < kGroups; ++i) {
       mbar_init(&m.s_full[i], 1);
       mbar_init(&m.s_empty[i], 4);
     }
@@ -112,6 +119,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t tbase = m.tmem_base;
   volatile int* abort_flag = &m.abort_flag;
   const int slots = a.slots;
+  // the buffer of a segment's Q, and how often it was used before
+  const int q_shift = a.q_bufs - 1;
+  auto q_buf = [&](int seg) { return seg & q_shift; };
+  auto q_turn = [&](int seg) { return (uint32_t)(seg >> q_shift); };
   Ring ring;
   ring.flags = m.flags;
   if (part.left > 0) {
@@ -177,31 +188,47 @@ __global__ void __launch_bounds__(kThreads, 1)
     } else if (warp == 1) {
       // ----------------------------------------------------------- MMA issue
       if (elect_one()) {
-        const uint32_t idesc = idesc_bf16_f32(128, a.cols, 0, 0);
+        const uint32_t idesc = idesc_bf16_f32(128, a.half, 0, 0);
         const uint64_t k_desc = smem_desc(smem_u32(smem), 16, 8 * kRowBytes, kSwizzle128);
         const uint64_t q_desc = smem_desc(smem_u32(sq), 16, 8 * kRowBytes, kSwizzle128);
         uint32_t tau = 0, turn = 0;
         int slot = 0;
         bool ok = true;
-        do {
-          ok = mbar_wait<1>(&m.q_full[w.seg & 1], (w.seg >> 1) & 1, abort_flag, err);
-          const uint64_t qd = q_desc + (uint64_t)(((w.seg & 1) * q_bytes) >> 4);
-          for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
-            const int buf = tau & 1;
-            ok = mbar_wait<1>(&m.full[slot], turn & 1, abort_flag, err) &&
-                 (tau < 2u || mbar_wait<1>(&m.s_empty[buf], ((tau >> 1) - 1) & 1, abort_flag, err));
-            if (!ok) break;
-            tc_fence_after();
-            const uint64_t kd = k_desc + (uint64_t)((slot * KV_BYTES) >> 4);
+        const uint32_t halves = (uint32_t)(a.cols / a.half);
+        // scores of half h of tile `tile`, whose K is in `at`
+        auto issue = [&](uint32_t tile, uint32_t h, int at, uint64_t qd) -> bool {
+          const int buf = (int)(tile % kGroups);
+          const uint32_t u = tile / kGroups * halves + h;  // uses of the buffer before
+          if (u > 0u && !mbar_wait<1>(&m.s_empty[buf], (u - 1) & 1, abort_flag, err)) return false;
+          tc_fence_after();
+          const uint64_t kd = k_desc + (uint64_t)((at * KV_BYTES) >> 4);
+          const uint32_t c0 = h * (uint32_t)a.half;
 #pragma unroll
-            for (int kk = 0; kk < D / 16; ++kk) {
-              const int c = kk / 4, wd = kk % 4;
-              umma_ss(tbase + buf * a.cols, kd + (uint64_t)((c * kTile * kRowBytes + wd * 32) >> 4),
-                      qd + (uint64_t)((c * a.cols * kRowBytes + wd * 32) >> 4), idesc, kk > 0);
+          for (int kk = 0; kk < D / 16; ++kk) {
+            const int c = kk / 4, wd = kk % 4;
+            umma_ss(tbase + buf * a.half, kd + (uint64_t)((c * kTile * kRowBytes + wd * 32) >> 4),
+                    qd + (uint64_t)(((c * a.cols + c0) * kRowBytes + wd * 32) >> 4), idesc, kk > 0);
+          }
+          umma_commit(&m.s_full[buf]);
+          if (h + 1u == halves) umma_commit(&m.empty[at]);
+          return true;
+        };
+        do {
+          ok = mbar_wait<1>(&m.q_full[q_buf(w.seg)], q_turn(w.seg) & 1, abort_flag, err);
+          const uint64_t qd = q_desc + (uint64_t)((q_buf(w.seg) * q_bytes) >> 4);
+          // the second halves follow two tiles behind the first ones: a group has one
+          // buffer, and the others' come in between while it works on the first
+          const int n = w.t1 - w.t0, lag = halves > 1u ? 2 : 0;
+          for (int i = 0; ok && i < n + lag; ++i) {
+            if (i < n) {
+              ok = mbar_wait<1>(&m.full[slot], turn & 1, abort_flag, err) && issue(tau, 0u, slot, qd);
+              ++tau;
+              if (++slot == slots) slot = 0, ++turn;
             }
-            umma_commit(&m.s_full[buf]);
-            umma_commit(&m.empty[slot]);
-            if (++slot == slots) slot = 0, ++turn;
+            if (ok && lag > 0 && i >= lag) {
+              const int back = min(i, n - 1) - (i - lag) + 1;  // the tile is so many slots back
+              ok = issue(tau - (uint32_t)back, 1u, (slot - back + slots) % slots, qd);
+            }
           }
         } while (ok && w.next(p));
         // every MMA of this thread done before TMEM and shared memory go
@@ -215,17 +242,22 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int th = threadIdx.x - 64;  // 0 .. 63
       bool ok = true;
       do {
-        const int buf = w.seg & 1;
-        if (w.seg >= 2) ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.seg_done[buf], ((w.seg >> 1) - 1) & 1, abort_flag, err));
+        const int buf = q_buf(w.seg);
+        if (q_turn(w.seg) > 0)
+          ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.seg_done[buf], (q_turn(w.seg) - 1) & 1, abort_flag, err));
         if (!ok) break;
         const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));  // rows of valid tokens come first
         uint8_t* dst = sq + buf * q_bytes;
-        constexpr int UNITS = D / 8;
-        const uint16_t* q = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh;
-        for (int x = th; x < a.cols * UNITS; x += 64) {
-          const int r = x / UNITS, u = x % UNITS, tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
+        // neighbouring lanes copy neighbouring 16-byte units of a row
+        constexpr int UNITS = D / 8, LANES = UNITS > 8 ? 16 : 8;
+        const int u = th % LANES;
+        const uint16_t* q = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh + u * 8;
+#pragma unroll 8
+        for (int r = th / LANES; r < a.cols; r += 64 / LANES) {
+          const int tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
           uint8_t* at = dst + unit_offset(a.cols, r, u);
-          if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn + u * 8);
+          if (u >= UNITS) continue;
+          if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn);
           else *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
         }
         int first = live;  // first row that adds nothing
@@ -234,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           float l = -INFINITY;
           if (r < live) l = a.lse[((int64_t)w.b * p.t.heads + w.hk * p.group + g) * p.t.n + tok];
           if (l == -INFINITY) first = min(first, r);
-          m.lse2[buf][r] = l == -INFINITY ? INFINITY : l * 1.4426950408889634f;
+          m.neg_lse2[buf][r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
         }
         first = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0) m.plain[buf][warp & 1] = first;
@@ -255,60 +287,80 @@ __global__ void __launch_bounds__(kThreads, 1)
       __syncwarp();
     } else {
       // ---------------------------------------------------------------- sums
-      const int s = (warp - 4) >> 2;  // tiles with this parity
+      const int s = (warp - 4) >> 2;  // every kGroups-th tile
       const int quarter = warp & 3, key = quarter * 32 + lane;
-      const uint32_t tS = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + s * a.cols;
+      const uint32_t tS = tbase + (static_cast<uint32_t>(quarter * 32) << 16) + s * a.half;
       const float sl2 = p.scale_log2;
-      uint32_t tau = 0;
+      uint32_t tau = 0, used = 0;
       bool ok = true;
       do {
-        const int buf = w.seg & 1;
-        ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.q_full[buf], (w.seg >> 1) & 1, abort_flag, err));
-        const float* lse2 = m.lse2[buf];
+        const int buf = q_buf(w.seg);
+        ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.q_full[buf], q_turn(w.seg) & 1, abort_flag, err));
+        const float* neg_lse2 = m.neg_lse2[buf];
         const int plain = ok ? min(m.plain[buf][0], m.plain[buf][1]) : 0;
         const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));
         float* row = a.weights + ((int64_t)w.b * p.t.cache.kv_heads + w.hk) * a.width;
         for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
-          if ((int)(tau & 1u) != s) continue;
+          if ((int)(tau % kGroups) != s) continue;
           const int pos = t * kTile + key;
           const bool in = pos < w.keys && pos < a.width;
           const bool fresh = pos >= w.len && a.row0 == 0;  // a new token's sum begins with the first launch
           float old = 0.f;
           if (in && !fresh) old = row[pos];
-          ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.s_full[s], (tau >> 1) & 1, abort_flag, err));
-          if (!ok) break;
-          const uint32_t bad = tile_bad<1>(ring, tau, abort_flag, err);
-          tc_fence_after();
-          const bool tail = (t + 1) * kTile > w.len;
+          // of the warp's keys: is one behind the committed tokens, is there one at all
+          const bool tail = t * kTile + quarter * 32 + 32 > w.len;
+          const bool some = t * kTile + quarter * 32 < w.keys;
           uint64_t sum[2] = {0ull, 0ull};
-          for (int c0 = 0; c0 < live; c0 += 16) {
-            uint32_t v[16];
-            __syncwarp();
-            tmem_ld_x16(tS + c0, v);
-            tmem_wait_ld16(v);
+          const int j = pos - w.len;  // (negative: a committed token)
+          const uint32_t* word = m.words[buf] + ((j > 0 ? j : 0) >> 5 & 3);
+          auto block = [&](int c0, const uint32_t (&v)[16]) {
             if (!tail && c0 + 16 <= plain) {
-              add8(lse2 + c0, v, sl2, sum);
-              add8(lse2 + c0 + 8, v + 8, sl2, sum);
+              add8(neg_lse2 + c0, v, sl2, sum);
+              add8(neg_lse2 + c0 + 8, v + 8, sl2, sum);
             } else {
-              // column by column: rows that do not see the key, or add nothing
-              const int j = pos - w.len;
-              float e = 0.f;
-#pragma unroll 1
-              for (int c = c0; c < min(c0 + 16, live); ++c) {
-                const int tok = row_token(p, a.row0 + c);
-                const bool sees = j < 0 || (j < w.nl && ((m.words[buf][tok * 4 + (j >> 5)] >> (j & 31)) & 1u));
-                float x = 0.f;
+              // rows that do not see the key, or add nothing (no branches: a warp's
+              // columns follow one another)
+              float e[2] = {0.f, 0.f};
 #pragma unroll
-                for (int k = 0; k < 16; ++k)
-                  if (c - c0 == k) x = __uint_as_float(v[k]);
-                if (sees && lse2[c] != INFINITY) e += fast_exp2(fmaf(x, sl2, -lse2[c]));
+              for (int c = 0; c < 16; ++c) {
+                const int tok = min(row_token(p, a.row0 + c0 + c), w.nl - 1);
+                const bool sees = (j < 0) | ((word[tok * 4] >> (j & 31)) & (j < w.nl));
+                const float l = neg_lse2[c0 + c];
+                const float x = fast_exp2(fmaf(__uint_as_float(v[c]), sl2, l));
+                e[c & 1] += sees & (l != -INFINITY) ? x : 0.f;
               }
-              sum[0] = fadd2(sum[0], f2_pack(e, 0.f));
+              sum[0] = fadd2(sum[0], f2_pack(e[0], e[1]));
             }
+          };
+          uint32_t bad = 0u;
+          for (int h0 = 0; ok && h0 < a.cols; h0 += a.half, ++used) {
+            ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.s_full[s], used & 1, abort_flag, err));
+            if (!ok) break;
+            if (h0 == 0) bad = tile_bad<1>(ring, tau, abort_flag, err);
+            tc_fence_after();
+            const int cols = some ? min(a.half, live - h0) : 0;
+            // the next 16 columns are on their way while these are summed
+            uint32_t v0[16], v1[16];
+            __syncwarp();
+            if (cols > 0) {
+              tmem_ld_x16(tS, v0);
+              for (int c0 = 0; c0 < cols; c0 += 32) {
+                __syncwarp();
+                tmem_wait_ld16(v0);
+                if (c0 + 16 < cols) tmem_ld_x16(tS + c0 + 16, v1);
+                block(h0 + c0, v0);
+                if (c0 + 16 >= cols) break;
+                __syncwarp();
+                tmem_wait_ld16(v1);
+                if (c0 + 32 < cols) tmem_ld_x16(tS + c0 + 32, v0);
+                block(h0 + c0 + 16, v1);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&m.s_empty[s]);
           }
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&m.s_empty[s]);
+          if (!ok) break;
           if (pos < w.keys && pos >= a.width) atomicOr(err, kErrBadCache);
           float x0, x1;
           f2_unpack(fadd2(sum[0], sum[1]), x0, x1);
@@ -369,12 +421,16 @@ cudaError_t launch_weights(const WeightsLaunch& w, const CUtensorMap* map, cudaS
   a.width = w.width;
   for (a.row0 = 0; a.row0 < p.rows; a.row0 += kMaxRows) {
     a.nrows = p.rows - a.row0 < kMaxRows ? p.rows - a.row0 : kMaxRows;
-    a.cols = (a.nrows + 15) / 16 * 16;
+    const bool halves = a.nrows > 128;
+    a.cols = halves ? (a.nrows + 31) / 32 * 32 : (a.nrows + 15) / 16 * 16;
+    a.half = halves ? a.cols / 2 : a.cols;
+    a.q_bufs = halves ? 1 : 2;  // (room for a deeper ring)
     a.tmem_cols = 32;
-    while (a.tmem_cols < 2u * (uint32_t)a.cols) a.tmem_cols *= 2;
-    const uint32_t chunks = w.head_dim > 64 ? 2 : 1, tile = kTile * chunks * kRowBytes, q = 2 * a.cols * chunks * kRowBytes;
+    while (a.tmem_cols < (uint32_t)kGroups * a.half) a.tmem_cols *= 2;
+    const uint32_t chunks = w.head_dim > 64 ? 2 : 1, tile = kTile * chunks * kRowBytes, q = a.q_bufs * a.cols * chunks * kRowBytes;
     a.slots = (int32_t)((kRoom - q) / tile);
     if (a.slots > kMaxSlots) a.slots = kMaxSlots;
+    static_assert(kRoom - 2u * 256u * kRowBytes >= 4u * kTile * 2u * kRowBytes, "four slots beside 256 rows");
     const uint32_t bytes = a.slots * tile + q + (uint32_t)sizeof(Small);
     const cudaError_t e = w.head_dim == 64   ? launch_d<64>(a, map, bytes, stream)
                           : w.head_dim == 96 ? launch_d<96>(a, map, bytes, stream)

@@ -256,7 +256,8 @@ def test_bad_entries_are_flagged_and_skipped():
     rng = np.random.default_rng(14)
     table, n_pages, free = _table(rng, [60], 16, 6)
     k = _pool(rng, 1, 64, 16, table, n_pages, [60])
-    weights = torch.rand((1, 1, 64), device="cuda")
+    weights = torch.from_numpy(rng.random((1, 1, 64)).astype(np.float32)).cuda()
+    weights[..., 16:32] += 1.0  # the second page's tokens are always among the kept
     good = wise.PagedCache(k, k.clone(), _i32(table), _i32([59]))
     q = _bf16(rng.standard_normal((1, 2, 1, 64)))
     _, lse = wise.tree_attention(q, good)
