@@ -15,6 +15,8 @@
 // one key per thread (with two groups, the sums' latency took longer than the bytes
 // of K: 128 rows over 131K tokens 57 us instead of XX).
 // The key tiles of all (sequence, key head) units form the line of tree.cuh.
+#include <type_traits>
+
 #include "tree.cuh"
 
 namespace wise {
@@ -125,6 +127,32 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto q_turn = [&](int seg) { return (uint32_t)(seg >> q_shift); };
   Ring ring;
   ring.flags = m.flags;
+  // rows of valid tokens, which come first
+  auto live_rows = [&](const Walk& x) { return max(0, min(a.nrows, x.nl * p.group - a.row0)); };
+  // Q of a segment by thread `th` of THREADS, swizzled as TMA would write it:
+  // neighbouring lanes copy neighbouring 16-byte units of a row
+  auto copy_q = [&](const Walk& x, int th, auto threads) {
+    constexpr int THREADS = decltype(threads)::value, UNITS = D / 8, LANES = UNITS > 8 ? 16 : 8;
+    const int u = th % LANES, live = live_rows(x);
+    uint8_t* dst = sq + q_buf(x.seg) * q_bytes;
+    const uint16_t* q = p.t.q.data + (int64_t)x.b * p.t.q.sb + (int64_t)x.hk * p.group * p.t.q.sh + u * 8;
+#pragma unroll 4
+    for (int r = th / LANES; r < a.cols; r += THREADS / LANES) {
+      const int tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
+      uint8_t* at = dst + unit_offset(a.cols, r, u);
+      if (u >= UNITS) continue;
+      if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn);
+      else *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  // the first segment's Q is copied by all but the first two warps (by the two that
+  // copy the later ones, 128 rows took 2.4 us)
+  constexpr int ALL = kThreads - 64;
+  auto first_q = [&] {
+    copy16_wait();
+    fence_proxy_async();
+    named_bar_sync(1, ALL);
+  };
   if (part.left > 0) {
     Walk w;
     w.start(p, part);
@@ -246,27 +274,23 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (q_turn(w.seg) > 0)
           ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.seg_done[buf], (q_turn(w.seg) - 1) & 1, abort_flag, err));
         if (!ok) break;
-        const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));  // rows of valid tokens come first
-        uint8_t* dst = sq + buf * q_bytes;
-        // neighbouring lanes copy neighbouring 16-byte units of a row
-        constexpr int UNITS = D / 8, LANES = UNITS > 8 ? 16 : 8;
-        const int u = th % LANES;
-        const uint16_t* q = p.t.q.data + (int64_t)w.b * p.t.q.sb + (int64_t)w.hk * p.group * p.t.q.sh + u * 8;
-#pragma unroll 8
-        for (int r = th / LANES; r < a.cols; r += 64 / LANES) {
-          const int tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
-          uint8_t* at = dst + unit_offset(a.cols, r, u);
-          if (u >= UNITS) continue;
-          if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn);
-          else *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+        const int live = live_rows(w);
+        float l[kMaxRows / 64];
+#pragma unroll
+        for (int k = 0; k < kMaxRows / 64; ++k) {
+          const int r = th + 64 * k, tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
+          l[k] = -INFINITY;
+          if (r < live) l[k] = a.lse[((int64_t)w.b * p.t.heads + w.hk * p.group + g) * p.t.n + tok];
         }
+        if (w.seg == 0) copy_q(w, th, std::integral_constant<int, ALL>());
+        else copy_q(w, th, std::integral_constant<int, 64>());
         int first = live;  // first row that adds nothing
-        for (int r = th; r < a.cols; r += 64) {
-          const int tok = row_token(p, a.row0 + r), g = a.row0 + r - tok * p.group;
-          float l = -INFINITY;
-          if (r < live) l = a.lse[((int64_t)w.b * p.t.heads + w.hk * p.group + g) * p.t.n + tok];
-          if (l == -INFINITY) first = min(first, r);
-          m.neg_lse2[buf][r] = l == -INFINITY ? -INFINITY : l * -1.4426950408889634f;
+#pragma unroll
+        for (int k = 0; k < kMaxRows / 64; ++k) {
+          const int r = th + 64 * k;
+          if (r >= a.cols) break;
+          if (l[k] == -INFINITY) first = min(first, r);
+          m.neg_lse2[buf][r] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
         }
         first = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0) m.plain[buf][warp & 1] = first;
@@ -279,9 +303,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             else v = i >= j0 + 31 ? 0xffffffffu : i < j0 ? 0u : (2u << (i - j0)) - 1u;
             m.words[buf][x] = v;
           }
-        copy16_wait();
-        fence_proxy_async();
-        __syncwarp();
+        if (w.seg == 0) {
+          first_q();
+        } else {
+          copy16_wait();
+          fence_proxy_async();
+          __syncwarp();
+        }
         if (lane == 0) mbar_arrive(&m.q_full[buf]);
       } while (w.next(p));
       __syncwarp();
@@ -293,12 +321,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       const float sl2 = p.scale_log2;
       uint32_t tau = 0, used = 0;
       bool ok = true;
+      copy_q(w, (int)threadIdx.x - 64, std::integral_constant<int, ALL>());
+      first_q();
       do {
         const int buf = q_buf(w.seg);
         ok = __all_sync(0xffffffffu, mbar_wait<1>(&m.q_full[buf], q_turn(w.seg) & 1, abort_flag, err));
         const float* neg_lse2 = m.neg_lse2[buf];
         const int plain = ok ? min(m.plain[buf][0], m.plain[buf][1]) : 0;
-        const int live = max(0, min(a.nrows, w.nl * p.group - a.row0));
+        const int live = live_rows(w);
         float* row = a.weights + ((int64_t)w.b * p.t.cache.kv_heads + w.hk) * a.width;
         for (int t = w.t0; ok && t < w.t1; ++t, ++tau) {
           if ((int)(tau % kGroups) != s) continue;
