@@ -213,7 +213,11 @@ struct TreeLaunch {
   float* lse;
   void* workspace;
   uint32_t* err;
-  const int32_t* skip;    // null, or [batch]: tokens at the front of each sequence that are left out
+  // For wise_attn_prefix's two launches (null and 0 elsewhere):
+  const int32_t* skip;    // [batch]: tokens at the front of each sequence that are left out
+  const int32_t* limit;   // blocks that share the work (the others leave at once)
+  int32_t beside;         // runs beside the launch before it, which it waits for at its end
+  int32_t rows_apart;     // records of all units, and no join
   // for groups of sequences over what they share: cache.batch counts groups, cache.lengths
   // are their shared tokens, cache.page_table and the rest are the sequences'
   const int32_t* starts;  // [groups + 1]: each group's first sequence

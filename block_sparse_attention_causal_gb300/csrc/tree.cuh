@@ -187,7 +187,8 @@ __device__ __forceinline__ void find_part(const TreeParams& p, int* scratch, Lin
     total += sums[w];
   }
   const int cta = blockIdx.x;
-  part.ctas = PREFIX ? max(min((int)gridDim.x, total), 1) : min((int)gridDim.x, total);
+  const int grid = p.t.limit ? *p.t.limit : (int)gridDim.x;
+  part.ctas = max(min(grid, total), 1);  // (an empty line: a batch that shares nothing)
   part.per = total / part.ctas;
   part.more = total - part.per * part.ctas;
   const int x0 = cta < part.ctas ? part.begin(cta) : total;
@@ -582,6 +583,19 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, WalkOf<PREFIX> w
   } while (ok && w.next(p));
   __syncwarp();
 }
+
+// The wait for the launch before this one: at the start, or, for a launch that runs
+// beside it (whatever came before that one is complete then: its blocks wait for it
+// before they let this one start), at the end, since a launch must not end before
+// those it follows.
+__device__ __forceinline__ void wait_at_start(const TreeLaunch& t) {
+  if (!t.beside) grid_wait();
+}
+__device__ __forceinline__ void wait_at_end(const TreeLaunch& t) {
+  if (t.beside) grid_wait();
+}
+// Whether the block has no part in the work.
+__device__ __forceinline__ bool left_out(const TreeLaunch& t) { return t.limit && (int)blockIdx.x >= *t.limit; }
 
 // Row pointer of drafted token j's values in the pool, or null.
 __device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {

@@ -187,7 +187,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   prefetch_tables(p);
-  grid_wait();
+  wait_at_start(p.t);
+  if (left_out(p.t)) {
+    grid_trigger();
+    wait_at_end(p.t);
+    return;
+  }
   // tensor memory only now: a kernel before this one that still runs could wait
   // for what this one holds
   if (warp == 2) {
@@ -572,6 +577,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
+  wait_at_end(p.t);
 }
 
 template <int D, int N, bool PREFIX>

@@ -164,7 +164,12 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   prefetch_tables(p);
-  grid_wait();
+  wait_at_start(p.t);
+  if (left_out(p.t)) {
+    grid_trigger();
+    wait_at_end(p.t);
+    return;
+  }
   // tensor memory only now: a kernel before this one that still runs could wait
   // for what this one holds
   if (warp == 2) {
@@ -608,6 +613,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
+  wait_at_end(p.t);
 }
 
 // Whether a record names parts that exist. After a wait that ran out a CTA
@@ -617,18 +623,11 @@ __device__ __forceinline__ bool rec_ok(const TreeParams& p, const int4& ra, cons
          ra.w < p.t.cache.batch && rb.x >= 0 && rb.x < p.t.cache.kv_heads && rb.y >= 0 && rb.y < p.pairs;
 }
 
-// Rows of a record's sequence (group) and key head.
-template <bool PREFIX>
-__device__ __forceinline__ int rec_rows(const TreeParams& p, int b) {
-  if constexpr (PREFIX) return (p.t.starts[b + 1] - p.t.starts[b]) * p.t.n * p.group;
-  return p.rows;
-}
-
 // Joins the partial results of a row whose unit was cut, in the line's order,
 // whatever the order in which they were written. grid.x: join records, grid.y:
 // rows (kJoinWarps of them per block, or one whose parts the warps share).
 constexpr int kJoinWarps = 4;
-template <int D, bool SHARE, bool PREFIX>
+template <int D, bool SHARE>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreeParams p) {
   constexpr int E = D / 32;
   constexpr int BATCH = 8;  // parts loaded at a time
@@ -642,7 +641,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
   const int4 rb = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rb.x;
   const int row = rb.y * 256 + r;
-  if (!rec_ok(p, ra, rb) || r >= p.row_slots || row >= rec_rows<PREFIX>(p, b)) return;
+  if (!rec_ok(p, ra, rb) || r >= p.row_slots || row >= p.rows) return;
   float m = -INFINITY, l = 0.f, acc[E];
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -712,8 +711,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
     m = top;
   }
   const int tok = row_token(p, row), h = hk * p.group + (row - tok * p.group);
-  const RowPlace place = row_place<PREFIX>(p.t, b, tok);
-  const int64_t out_row = ((int64_t)place.b * p.t.heads + h) * p.t.n + place.i;
+  const int64_t out_row = ((int64_t)b * p.t.heads + h) * p.t.n + tok;
   const float inv = 1.f / l;
 #pragma unroll
   for (int e = 0; e < E; ++e) acc[e] = l == 0.f ? 0.f : acc[e] * inv;
@@ -732,7 +730,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_kernel(const TreePa
 // The same for wide units: a lane holds a row, a warp four columns of a block of
 // 32 rows, the block's warps 16 columns. The first partial results are asked for
 // before the maxima and sums that weigh them are known.
-template <int D, bool PREFIX>
+template <int D>
 __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const TreeParams p) {
   constexpr int BATCH = 10;
   __shared__ float ss[kJoinWarps][2][32];
@@ -744,9 +742,7 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
   const int4 rc = *(reinterpret_cast<const int4*>(&p.rec[blockIdx.x]) + 1);
   const int parts = ra.x, first_part = ra.y, first_cta = ra.z, b = ra.w, hk = rc.x;
   const int r = rb * 32 + lane, row = rc.y * 256 + r;
-  if (!rec_ok(p, ra, rc)) return;
-  const int rows = rec_rows<PREFIX>(p, b);
-  if (rc.y * 256 + rb * 32 >= rows) return;
+  if (!rec_ok(p, ra, rc) || rc.y * 256 + rb * 32 >= p.rows) return;
   auto part_at = [&](int k) -> int64_t { return k == 0 ? first_part : 2 * (first_cta + k); };
   const float* st = p.part_s + r;
   const float4* po = reinterpret_cast<const float4*>(p.part_o) + (rb * (D / 4) + c4) * 32 + lane;
@@ -796,10 +792,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
       acc.x += x[i].x * g, acc.y += x[i].y * g, acc.z += x[i].z * g, acc.w += x[i].w * g;
     }
   }
-  if (row >= rows) return;
+  if (row >= p.rows) return;
   const int tok = row_token(p, row), h = hk * p.group + (row - tok * p.group);
-  const RowPlace place = row_place<PREFIX>(p.t, b, tok);
-  const int64_t out_row = ((int64_t)place.b * p.t.heads + h) * p.t.n + place.i;
+  const int64_t out_row = ((int64_t)b * p.t.heads + h) * p.t.n + tok;
   const float inv = sum == 0.f ? 0.f : 1.f / sum;
   const bool zero = sum == 0.f;
   const float4 o = make_float4(zero ? 0.f : acc.x * inv, zero ? 0.f : acc.y * inv, zero ? 0.f : acc.z * inv,
@@ -814,11 +809,12 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
 struct WorkspaceLayout {
   int64_t recs, row_slots, part_o, part_s, bytes;  // offsets in bytes
 };
-// rows: of a (sequence, key head); of a group at most, with `by_cta` records.
-WorkspaceLayout workspace_layout(int64_t batch, int64_t kv_heads, int64_t rows, int64_t d, bool by_cta) {
+// rows: of a (sequence, key head), or of a (group, key head) at most; all_units: a
+// record of each unit.
+WorkspaceLayout workspace_layout(int64_t batch, int64_t kv_heads, int64_t rows, int64_t d, bool all_units) {
   WorkspaceLayout w;
   const int64_t units = batch * kv_heads * ((rows + 255) / 256);
-  w.recs = units < kTreeCtas && !by_cta ? units : kTreeCtas;
+  w.recs = units < kTreeCtas || all_units ? units : kTreeCtas;
   w.row_slots = rows <= 64 ? rows : rows < 256 ? (rows + 31) / 32 * 32 : 256;
   w.part_o = w.recs * (int64_t)sizeof(JoinRec);
   w.part_s = w.part_o + 2 * kTreeCtas * w.row_slots * d * 4;
@@ -847,22 +843,21 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
   cudaError_t e = p.rows > 128  ? launch_rows<D, 256, PREFIX>(p, maps, stream)
                   : p.rows > 64 ? launch_rows<D, 128, PREFIX>(p, maps, stream)
                                 : launch_tree_narrow<PREFIX>(p, maps, stream);
-  if (e != cudaSuccess) return e;
+  if (e != cudaSuccess || p.t.rows_apart) return e;
   // few rows: a row's parts are shared by a block's warps
   const bool wide = p.rows > 64;
   const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
   const int jobs = wide ? p.row_slots / 32 * (D / 4) : share ? p.row_slots * kJoinWarps : p.row_slots;
   const dim3 grid((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
-  auto join = wide    ? tree_join_wide_kernel<D, PREFIX>
-              : share ? tree_join_kernel<D, true, PREFIX>
-                      : tree_join_kernel<D, false, PREFIX>;
+  auto join = wide ? tree_join_wide_kernel<D> : share ? tree_join_kernel<D, true> : tree_join_kernel<D, false>;
   return launch_chained(join, grid, dim3(32 * kJoinWarps), 0, stream, p);
 }
 
 }  // namespace
 
+// What a launch's kernels get.
 template <bool PREFIX>
-cudaError_t launch_tree_rows(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream) {
+TreeParams tree_params(const TreeLaunch& t) {
   TreeParams p;
   p.t = t;
   p.group = t.heads / t.cache.kv_heads;
@@ -876,14 +871,20 @@ cudaError_t launch_tree_rows(const TreeLaunch& t, const CUtensorMap* maps, cudaS
   // Measured: of 4, 6 and 8 places for wide units, and 0 to 3 for narrow ones, 8
   // and 2 gave the shortest times.
   p.overhead = p.rows > 64 ? kWideOverhead : kNarrowOverhead;
-  const WorkspaceLayout w = workspace_layout(t.cache.batch, t.cache.kv_heads, p.rows, t.head_dim, PREFIX);
+  const WorkspaceLayout w = workspace_layout(t.cache.batch, t.cache.kv_heads, p.rows, t.head_dim, t.rows_apart);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(t.workspace) + 31) / 32 * 32);
   p.recs = (int32_t)w.recs;
-  p.by_unit = !PREFIX && (int64_t)t.cache.batch * t.cache.kv_heads * p.pairs <= kTreeCtas;
+  p.by_unit = t.rows_apart || (int64_t)t.cache.batch * t.cache.kv_heads * p.pairs <= kTreeCtas;
   p.row_slots = (int32_t)w.row_slots;
   p.rec = reinterpret_cast<JoinRec*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);
   p.part_s = reinterpret_cast<float*>(ws + w.part_s);
+  return p;
+}
+
+template <bool PREFIX>
+cudaError_t launch_tree_rows(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream) {
+  const TreeParams p = tree_params<PREFIX>(t);
   switch (t.head_dim) {
     case 64: return launch_d<64, PREFIX>(p, maps, stream);
     case 96: return launch_d<96, PREFIX>(p, maps, stream);

@@ -570,7 +570,7 @@ size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, 
  *   workspace      : wise_attn_prefix_workspace bytes.
  * group_starts that are not ascending or out of range are flagged, and nothing
  * is shared then; prefix_lengths below 0 or past the page table are flagged, and
- * their groups share nothing (WISE_ERR_BAD_CACHE). Six launches.
+ * their groups share nothing (WISE_ERR_BAD_CACHE). Four launches.
  */
 int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, int32_t groups,
                      const int32_t* group_starts, const int32_t* prefix_lengths, const int32_t* new_len,
