@@ -44,8 +44,9 @@ __device__ __forceinline__ int evict_length(const EvictLaunch& e, int b, bool fl
 template <int C>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictLaunch e) {
   __shared__ uint32_t hist[3][2048];
-  __shared__ uint32_t sums[kSelWarps], found[2];
-  __shared__ uint32_t greater[kSelWarps], equal[kSelWarps], totals[2];
+  __shared__ uint32_t sums[kSelWarps], found[3];
+  __shared__ uint32_t greater[kSelWarps], equal[kSelWarps];
+  __shared__ uint2 totals[C];  // of each block of the cluster: weights above the cut, weights at it
   grid_wait();
   grid_trigger();
   auto cluster = cg::this_cluster();
@@ -115,19 +116,27 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictLaunch e
     }
     if (lane == 31) sums[warp] = before;
     __syncthreads();
-    before -= n0 + n1;
-    for (int k = 0; k < warp; ++k) before += sums[k];
+    before += __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0u) - n0 - n1;
     if (before < left && left <= before + n1) {
       found[0] = (uint32_t)bin;
       found[1] = left - before;
+      found[2] = n1;
     } else if (before + n1 < left && left <= before + n1 + n0) {
       found[0] = (uint32_t)bin - 1u;
       found[1] = left - before - n1;
+      found[2] = n0;
     }
     __syncthreads();
     cut |= found[0] << shift;
     left = found[1];
+    const bool all = left == found[2];  // every weight that begins with these bits is taken
     __syncthreads();
+    if (all) {
+      // (a cut of 0 only where the least of all keys, NaN's, are taken: all of them)
+      left = cut == 0u ? left : 0u;
+      cut -= cut == 0u ? 0u : 1u;
+      break;
+    }
   }
   // all weights above the cut, and the first `left` of those at it
   uint32_t gt = 0u, eq = 0u;
@@ -142,24 +151,18 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictLaunch e
     equal[warp] = eq;
   }
   __syncthreads();
-  uint32_t gt_before = 0u, eq_before = 0u, all_gt = 0u, all_eq = 0u;
-  for (int k = 0; k < kSelWarps; ++k) {
-    if (k == warp) gt_before = all_gt, eq_before = all_eq;
-    all_gt += greater[k];
-    all_eq += equal[k];
-  }
-  if (C > 1) {
-    if (tid == 0) {
-      totals[0] = all_gt;
-      totals[1] = all_eq;
-    }
+  uint32_t gt_before = __reduce_add_sync(0xffffffffu, lane < warp ? greater[lane] : 0u);
+  uint32_t eq_before = __reduce_add_sync(0xffffffffu, lane < warp ? equal[lane] : 0u);
+  if constexpr (C > 1) {
+    // this block's totals to every block
+    if (warp == kSelWarps - 1 && lane < C)
+      *cluster.map_shared_rank(&totals[rank], lane) = make_uint2(gt_before + gt, eq_before + eq);
     cluster.sync();
-    for (int r = 0; r < rank; ++r) {
-      const uint32_t* o = cluster.map_shared_rank(totals, r);
-      gt_before += o[0];
-      eq_before += o[1];
+#pragma unroll
+    for (int r = 0; r < C; ++r) {
+      gt_before += r < rank ? totals[r].x : 0u;
+      eq_before += r < rank ? totals[r].y : 0u;
     }
-    cluster.sync();  // no block leaves while another reads its memory
   }
   const uint32_t below = (1u << lane) - 1u;
   int32_t* out = list + e.sink;
