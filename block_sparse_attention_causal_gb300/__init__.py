@@ -608,21 +608,24 @@ def _check_cache(cache: PagedCache) -> Tuple[_lib.PagedCacheDesc, int]:
 
 def _check_rows(name: str, t: torch.Tensor, batch: int, heads: Optional[int], d: int, dev: int) -> _lib.Rows:
     """The C view of rows [batch, heads, n, d] (any strides of the first three axes)."""
+    # everything at once, as in _check_cache; what fails is named below
+    if isinstance(t, torch.Tensor) and t.dim() == 4:
+        b, h, n, last = t.shape
+        sb, sh, sn, sd = t.stride()
+        if (sd == 1 and last == d and b == batch and 1 <= n <= _MAX_I32 and (h == heads or heads is None and h <= _MAX_I32)
+                and t.dtype == _BF16 and t.get_device() == dev >= 0):
+            # the stride of an axis of length 1 says nothing
+            return _lib.Rows(t.data_ptr(), (sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0))
     if not isinstance(t, torch.Tensor) or t.dtype != torch.bfloat16 or t.dim() != 4:
         raise ValueError(f"{name} must be a bfloat16 [batch, heads, tokens, head_dim] tensor")
     if max(t.shape) > _MAX_I32:
         raise ValueError(f"{name}'s axes must be shorter than 2^31")
     if not t.is_cuda or t.get_device() != dev:
         raise ValueError(f"{name} must be on the current device cuda:{dev}, not on {t.device}")
-    b, h, n, last = t.shape
-    if b != batch or last != d or n < 1 or (heads is not None and h != heads):
+    if t.shape[0] != batch or t.shape[3] != d or t.shape[2] < 1 or (heads is not None and t.shape[1] != heads):
         raise ValueError(f"{name} of shape {tuple(t.shape)} does not fit the cache (batch {batch}, "
                          + (f"{heads} heads, " if heads is not None else "") + f"head_dim {d})")
-    sb, sh, sn, sd = t.stride()
-    if sd != 1:
-        raise ValueError(f"{name} must be contiguous in its last axis")
-    # the stride of an axis of length 1 says nothing
-    return _lib.Rows(t.data_ptr(), (sb if b > 1 else 0, sh if h > 1 else 0, sn if n > 1 else 0))
+    raise ValueError(f"{name} must be contiguous in its last axis")
 
 
 def _check_stream(stream: Optional[torch.cuda.Stream], dev: int) -> int:
@@ -674,19 +677,20 @@ def _check_norms(q_norm: Optional[torch.Tensor], heads: int, k_norm: Optional[to
     """The C descriptor of the norms, or None."""
     if q_norm is None and k_norm is None:
         return None
-    at, step, kind = [None, None], [0, 0], None
-    for i, (name, w, h) in enumerate((("q_norm", q_norm, heads), ("k_norm", k_norm, kv_heads))):
-        if w is None:
-            continue
-        if not isinstance(w, torch.Tensor) or w.dtype not in _OUT or kind not in (None, w.dtype):
-            raise ValueError("q_norm and k_norm must be bfloat16 or float32, both of one type")
-        kind = w.dtype
-        per_head = w.dim() == 2
-        at[i] = _check_array(name, w, kind, (h, d) if per_head else (d,), dev)
-        step[i] = d if per_head else 0
+    q_at = k_at = None
+    q_step = k_step = 0
+    kind = (k_norm if q_norm is None else q_norm).dtype if isinstance(k_norm if q_norm is None else q_norm, torch.Tensor) else None
+    if kind not in _OUT:
+        raise ValueError("q_norm and k_norm must be bfloat16 or float32, both of one type")
+    if q_norm is not None:
+        q_step = d if q_norm.dim() == 2 else 0
+        q_at = _check_array("q_norm", q_norm, kind, (heads, d) if q_step else (d,), dev)
+    if k_norm is not None:
+        k_step = d if isinstance(k_norm, torch.Tensor) and k_norm.dim() == 2 else 0
+        k_at = _check_array("k_norm", k_norm, kind, (kv_heads, d) if k_step else (d,), dev)
     if not (isinstance(eps, (int, float)) and 0.0 < eps < math.inf):
         raise ValueError("norm_eps must be positive and finite")
-    return _lib.HeadNorm(at[0], at[1], step[0], step[1], _OUT[kind], eps)
+    return _lib.HeadNorm(q_at, k_at, q_step, k_step, _OUT[kind], eps)
 
 
 def cache_append(cache: PagedCache, k: torch.Tensor, v: torch.Tensor, *, q: Optional[torch.Tensor] = None,

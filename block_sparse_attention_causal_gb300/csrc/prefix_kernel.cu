@@ -14,11 +14,6 @@
 // bound by the tensor core and the softmax, the own parts by the cache's bytes); and
 // the join of everything that belongs to a row.
 #include "tree_wide.cuh"
-#ifndef COST_WIDE
-#define COST_WIDE 1.65f
-#define COST_MID 1.1f
-#define COST_NARROW 0.9f
-#endif
 
 namespace wise {
 
@@ -49,6 +44,7 @@ struct PlanParams {
 constexpr int kPlanThreads = 1024;
 __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) {
   __shared__ unsigned long long places[2];  // of the shared part and of the own parts
+  prefetch_tables(p.own);
   grid_wait();
   grid_trigger();
   const CacheView& c = p.own.t.cache;
@@ -224,8 +220,13 @@ PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64
   return w;
 }
 
-// Time of a place of the line, relative (microseconds a key tile measured alone).
-float place_cost(const TreeParams& p) { return p.rows > 128 ? COST_WIDE : p.rows > 64 ? COST_MID : COST_NARROW; }
+// Time of a place of the line, in microseconds, by the rows of a unit: what decides
+// how the SMs are shared out. (64 next tokens behind 32K and up to 1K of their own:
+// 80.8, 77.3, 76.1, 83.0, 88.2 us with 0.6, 0.8, 0.85, 1.0, 1.2 for up to 16 rows; trees
+// of 5 with 25 rows 51.5, 47.1, 45.9, 47.1 us with 0.8, 1.0, 1.2, 1.5.)
+float place_cost(const TreeParams& p) {
+  return p.rows > 128 ? 1.65f : p.rows > 64 ? 1.f : p.rows > 32 ? 1.6f : p.rows > 16 ? 1.2f : 0.85f;
+}
 
 }  // namespace
 
