@@ -668,6 +668,9 @@ def _check_positions(rope: Optional[Rope], positions: Optional[torch.Tensor], ba
             raise ValueError("a rope with axes needs positions [axes, batch, n]")
         n_axes = positions.shape[0]
         shape = (n_axes, batch, n)
+        if rotary == 0:  # (no pair turns with any)
+            _check_array("positions", positions, torch.int32, shape, dev)
+            return None, None
     pos = None if positions is None else _check_array("positions", positions, torch.int32, shape, dev)
     return _lib.RopeDesc(steps, axes, rotary, n_axes, flags, 0), pos
 

@@ -27,6 +27,7 @@ struct Plan {
   int32_t* leader;  // [groups]
   int32_t* skip;    // [batch] the sequence's shared tokens
   int32_t* group;   // [batch] its group, where it shares any
+  int32_t* live;    // [batch] its new tokens, as far as the page table holds them
   int32_t* limit;   // [2] blocks of the shared part and of the own parts
 };
 struct PlanParams {
@@ -95,6 +96,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
   for (int b = threadIdx.x; b < c.batch; b += kPlanThreads) {
     int len, nl, full, active;
     seq_counts<false>(p.own.t, b, len, nl);
+    p.plan.live[b] = nl;
     seq_tiles<false>(p.own, len, nl, full, active);
     sum += (unsigned long long)seq_line<false>(p.own, full, active);
   }
@@ -210,7 +212,7 @@ PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64
   PrefixLayout w;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t per = heads / kv_heads * n, rows = batch * heads * n;
-  w.shared = up((3 * groups + 1 + 2 * batch + 2) * 4);
+  w.shared = up((3 * groups + 1 + 3 * batch + 2) * 4);
   w.own = w.shared + up(workspace_layout(groups, kv_heads, per * batch, d, true).bytes);
   w.o_own = w.own + up(workspace_layout(batch, kv_heads, per, d, true).bytes);
   w.o_shared = w.o_own + up(rows * d * 4);
@@ -245,12 +247,14 @@ cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaSt
   plan.leader = plan.length + x.groups;
   plan.skip = plan.leader + x.groups;
   plan.group = plan.skip + c.batch;
-  plan.limit = plan.group + c.batch;
+  plan.live = plan.group + c.batch;
+  plan.limit = plan.live + c.batch;
   // what is shared: a cache of the groups
   TreeLaunch shared = x.t;
   shared.cache.batch = x.groups;
   shared.cache.lengths = plan.length;
   shared.tree_mask = nullptr;
+  shared.new_len = plan.live;
   shared.starts = plan.starts;
   shared.leader = plan.leader;
   shared.sequences = c.batch;

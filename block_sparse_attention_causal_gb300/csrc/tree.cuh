@@ -306,7 +306,7 @@ __device__ __forceinline__ RowPlace row_place(const TreeLaunch& t, int b, int to
 template <bool PREFIX>
 __device__ __forceinline__ bool row_live(const TreeLaunch& t, const RowPlace& r, int tok, int nl) {
   if (tok >= nl) return false;
-  return !PREFIX || !t.new_len || r.i < t.new_len[r.b];
+  return !PREFIX || r.i < t.new_len[r.b];
 }
 
 // The join record of the unit whose first tile lies in this segment (one

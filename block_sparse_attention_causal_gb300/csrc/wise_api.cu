@@ -971,11 +971,6 @@ int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_t
   if (!prefix_lengths || (!group_starts && groups != 1)) return WISE_ERR_INVALID_ARGUMENT;
   if (misaligned4(group_starts) || misaligned4(prefix_lengths)) return WISE_ERR_ALIGNMENT;
   const size_t need = wise_attn_prefix_workspace(cache, heads, new_tokens, groups);
-  PrefixLaunch p;
-  memset(&p, 0, sizeof(p));
-  st = tree_launch(cache, heads, new_tokens, q, new_len, tree_mask, scale, out_dtype, o, lse, workspace, workspace_bytes, need,
-                   p.t);
-  if (st != WISE_OK) return st;
   const int64_t rows = (int64_t)cache->batch * heads * new_tokens;
   const struct {
     const void* at;
@@ -984,6 +979,11 @@ int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_t
   for (const auto& x : outs)
     if (overlap(x.at, x.bytes, group_starts, ((int64_t)groups + 1) * 4) || overlap(x.at, x.bytes, prefix_lengths, (int64_t)groups * 4))
       return WISE_ERR_INVALID_ARGUMENT;
+  PrefixLaunch p;
+  memset(&p, 0, sizeof(p));
+  st = tree_launch(cache, heads, new_tokens, q, new_len, tree_mask, scale, out_dtype, o, lse, workspace, workspace_bytes, need,
+                   p.t);
+  if (st != WISE_OK) return st;
   p.groups = groups;
   p.group_starts = group_starts;
   p.prefix_lengths = prefix_lengths;
