@@ -4,7 +4,11 @@
 // slots 0, 1, ... of other pages.
 //
 // Two launches: the selection writes each head's list of kept places, the move
-// copies their rows.
+// copies their rows. Measured (one GB300): 16 sequences of up to 8K, 8 key heads of
+// 128, cut to 4K (474 MB): 86.8 us, 14 of them the selection and 70 the move, which
+// runs at a copy's rate; one of 32K cut to 2K: 21 us, 16 the selection (eight blocks a
+// head; of one pass over 11 bits 1.5 us are the cluster's barrier, 2.5 the counts of
+// eight blocks).
 #include <cooperative_groups.h>
 
 #include "internal.h"
