@@ -196,9 +196,9 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedJoin j) {
   if (j.plan.skip[b] > 0) {
     const int g = j.plan.group[b];
     const int row = (b - j.plan.starts[g]) * own.rows + r;
-    add_unit<D>(j.shared, ((int64_t)g * kv_heads + hk) * j.shared.pairs + (row >> 8), row & 255, out_row, c4, m, l, acc);
+    add_unit<D>(j.shared, unit_rec<true>(j.shared, g, hk, row >> 8), row & 255, out_row, c4, m, l, acc);
   }
-  add_unit<D>(own, ((int64_t)b * kv_heads + hk) * own.pairs + (r >> 8), r & 255, out_row, c4, m, l, acc);
+  add_unit<D>(own, unit_rec<false>(own, b, hk, r >> 8), r & 255, out_row, c4, m, l, acc);
   const bool zero = l == 0.f;
   const float inv = zero ? 0.f : 1.f / l;
   const float4 o = make_float4(zero ? 0.f : acc.x * inv, zero ? 0.f : acc.y * inv, zero ? 0.f : acc.z * inv,
@@ -218,8 +218,8 @@ PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t per = heads / kv_heads * n, rows = batch * heads * n;
   w.shared = up((3 * groups + 1 + 3 * batch + 2) * 4);
-  w.own = w.shared + up(workspace_layout(groups, kv_heads, per * batch, d, true).bytes);
-  w.o_own = w.own + up(workspace_layout(batch, kv_heads, per, d, true).bytes);
+  w.own = w.shared + up(workspace_layout(shared_units(groups, kv_heads, per * batch), per * batch, d, true).bytes);
+  w.o_own = w.own + up(workspace_layout(tree_units(batch, kv_heads, per), per, d, true).bytes);
   w.o_shared = w.o_own + up(rows * d * 4);
   w.lse_own = w.o_shared + up(rows * d * 4);
   w.lse_shared = w.lse_own + up(rows * 4);

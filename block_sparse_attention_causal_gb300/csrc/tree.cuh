@@ -318,6 +318,15 @@ __device__ __forceinline__ void clear_rec(const TreeParams& p) {
 __device__ __forceinline__ void clear_recs(const TreeParams& p) {
   for (int i = threadIdx.x; i < p.recs; i += blockDim.x) p.rec[i].parts = 0;
 }
+// Place of a unit's record where each has one. PREFIX: a group's units follow those
+// of the rows before it, one place later for each group (its last unit may be part
+// of 256 rows only).
+template <bool PREFIX>
+__device__ __forceinline__ int64_t unit_rec(const TreeParams& p, int b, int hk, int pair) {
+  if constexpr (PREFIX)
+    return ((int64_t)p.t.starts[b] * p.t.n * p.group / 256 + b + pair) * p.t.cache.kv_heads + hk;
+  else return ((int64_t)b * p.t.cache.kv_heads + hk) * p.pairs + pair;
+}
 template <bool PREFIX>
 __device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f, const WalkOf<PREFIX>& w) {
   if (w.t0 != 0) return;
@@ -329,7 +338,7 @@ __device__ __forceinline__ void write_rec(const TreeParams& p, const LinePart& f
     r.parts = f.owner(f.x1 + (w.nt - w.t1) - 1) - (int)blockIdx.x + 1;
     r.first_part = w.part();
   }
-  if (p.by_unit) p.rec[(w.b * p.t.cache.kv_heads + w.hk) * p.pairs + w.pair] = r;
+  if (p.by_unit) p.rec[unit_rec<PREFIX>(p, w.b, w.hk, w.pair)] = r;
   else if (cut) p.rec[blockIdx.x] = r;
 }
 
@@ -585,11 +594,13 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, WalkOf<PREFIX> w
 }
 
 // The wait for the launch before this one: at the start, or, for a launch that runs
-// beside it (whatever came before that one is complete then: its blocks wait for it
-// before they let this one start), at the end, since a launch must not end before
-// those it follows.
+// beside it, at the end, since a launch must not end before those it follows. What
+// came before both is complete by then, as the blocks of the one before wait for it
+// before they let this one start; the fence keeps loads from what an SM's L1 cache
+// may still hold from earlier.
 __device__ __forceinline__ void wait_at_start(const TreeLaunch& t) {
-  if (!t.beside) grid_wait();
+  if (t.beside) __threadfence();
+  else grid_wait();
 }
 __device__ __forceinline__ void wait_at_end(const TreeLaunch& t) {
   if (t.beside) grid_wait();

@@ -7,7 +7,8 @@ namespace wise {
 template cudaError_t launch_tree_rows<false>(const TreeLaunch&, const CUtensorMap*, cudaStream_t);
 
 int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim) {
-  return workspace_layout(batch, kv_heads, (int64_t)(heads / kv_heads) * n, head_dim, false).bytes;
+  const int64_t rows = (int64_t)(heads / kv_heads) * n;
+  return workspace_layout(tree_units(batch, kv_heads, rows), rows, head_dim, false).bytes;
 }
 
 cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream_t stream) {

@@ -809,11 +809,9 @@ __global__ void __launch_bounds__(32 * kJoinWarps) tree_join_wide_kernel(const T
 struct WorkspaceLayout {
   int64_t recs, row_slots, part_o, part_s, bytes;  // offsets in bytes
 };
-// rows: of a (sequence, key head), or of a (group, key head) at most; all_units: a
-// record of each unit.
-WorkspaceLayout workspace_layout(int64_t batch, int64_t kv_heads, int64_t rows, int64_t d, bool all_units) {
+// units: of `rows` rows at most; all_units: a record of each.
+WorkspaceLayout workspace_layout(int64_t units, int64_t rows, int64_t d, bool all_units) {
   WorkspaceLayout w;
-  const int64_t units = batch * kv_heads * ((rows + 255) / 256);
   w.recs = units < kTreeCtas || all_units ? units : kTreeCtas;
   w.row_slots = rows <= 64 ? rows : rows < 256 ? (rows + 31) / 32 * 32 : 256;
   w.part_o = w.recs * (int64_t)sizeof(JoinRec);
@@ -855,6 +853,11 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
 
 }  // namespace
 
+// Units of a cache whose (sequence, key head) has `rows` rows; of groups of
+// sequences with `rows` rows in all (unit_rec's places).
+inline int64_t tree_units(int64_t batch, int64_t kv_heads, int64_t rows) { return batch * kv_heads * ((rows + 255) / 256); }
+inline int64_t shared_units(int64_t groups, int64_t kv_heads, int64_t rows) { return (rows / 256 + groups + 1) * kv_heads; }
+
 // What a launch's kernels get.
 template <bool PREFIX>
 TreeParams tree_params(const TreeLaunch& t) {
@@ -871,10 +874,12 @@ TreeParams tree_params(const TreeLaunch& t) {
   // Measured: of 4, 6 and 8 places for wide units, and 0 to 3 for narrow ones, 8
   // and 2 gave the shortest times.
   p.overhead = p.rows > 64 ? kWideOverhead : kNarrowOverhead;
-  const WorkspaceLayout w = workspace_layout(t.cache.batch, t.cache.kv_heads, p.rows, t.head_dim, t.rows_apart);
+  const int64_t units = PREFIX ? shared_units(t.cache.batch, t.cache.kv_heads, p.rows)
+                               : tree_units(t.cache.batch, t.cache.kv_heads, p.rows);
+  const WorkspaceLayout w = workspace_layout(units, p.rows, t.head_dim, t.rows_apart);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(t.workspace) + 31) / 32 * 32);
   p.recs = (int32_t)w.recs;
-  p.by_unit = t.rows_apart || (int64_t)t.cache.batch * t.cache.kv_heads * p.pairs <= kTreeCtas;
+  p.by_unit = t.rows_apart || units <= kTreeCtas;
   p.row_slots = (int32_t)w.row_slots;
   p.rec = reinterpret_cast<JoinRec*>(ws);
   p.part_o = reinterpret_cast<float*>(ws + w.part_o);

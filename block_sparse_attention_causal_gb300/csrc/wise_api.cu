@@ -1146,7 +1146,7 @@ int wise_cache_weights(const wise_paged_cache* cache, int32_t heads, int32_t new
 }
 
 size_t wise_cache_evict_workspace(const wise_paged_cache* cache, int32_t budget) {
-  if (check_cache(cache, false) != WISE_OK || budget < 1) return 0;
+  if (check_cache(cache, false) != WISE_OK || budget < 1 || (int64_t)cache->batch * cache->kv_heads > INT32_MAX / 8) return 0;
   return (size_t)cache->batch * cache->kv_heads * budget * 4;
 }
 

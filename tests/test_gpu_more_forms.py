@@ -153,6 +153,49 @@ def test_calls_one_after_the_other():
     wise.check_device()
 
 
+def test_inputs_rewritten_in_place_between_calls():
+    """Lengths, page table, groups, new tokens' counts, queries and pages that are
+    written again, at the same addresses, right before each call: every call sees
+    what was written last."""
+    g = torch.Generator(device="cuda").manual_seed(13)
+    b, h, hk, d, page, n, cols, pages = 6, 8, 2, 64, 16, 2, 40, 120
+    k, v = (_randn(g, 3, pages, hk, page, d) for _ in range(2))
+    kinds = []
+    for i in range(5):
+        prefix = [256, 128, 400, 384, 130][i]
+        table = torch.randperm(pages, generator=g, device="cuda")[:cols].to(torch.int32).expand(b, cols).clone()
+        own = torch.randperm(pages, generator=g, device="cuda")[:b * 10].to(torch.int32).reshape(b, 10)
+        table[:, prefix // page:prefix // page + 10] = own
+        table[:, prefix // page] = table[0, prefix // page]
+        lengths = prefix + torch.randint(0, 100, (b,), generator=g, device="cuda").to(torch.int32)
+        starts = _i32([[0, 6], [1, 5], [0, 3], [2, 6], [0, 6]][i])
+        kinds.append(dict(lengths=lengths, table=table, starts=starts, pre=_i32([prefix]), q=_randn(g, b, h, n, d),
+                          news=torch.randint(0, n + 1, (b,), generator=g, device="cuda").to(torch.int32), k=k[i % 3], v=v[(i + 1) % 3]))
+    wants = []
+    for x in kinds:
+        cache = wise.PagedCache(x["k"].contiguous(), x["v"].contiguous(), x["table"], x["lengths"])
+        o, lse = wise.prefix_attention(x["q"], cache, x["pre"], group_starts=x["starts"], new_len=x["news"])
+        w = wise.cache_weights(x["q"], cache, lse, torch.zeros((b, hk, 700), device="cuda"), new_len=x["news"])
+        torch.cuda.synchronize()
+        wants.append((o, lse, w))
+    wise.check_device()
+    now = {key: torch.empty_like(t) for key, t in kinds[0].items()}
+    cache = wise.PagedCache(now["k"], now["v"], now["table"], now["lengths"])
+    o, lse, w = (torch.empty_like(t) for t in wants[0])
+    order = np.random.default_rng(14).integers(0, 5, 150)
+    got = []
+    for i in order:
+        for key, t in kinds[i].items():
+            now[key].copy_(t)
+        w.zero_()
+        wise.prefix_attention(now["q"], cache, now["pre"], group_starts=now["starts"], new_len=now["news"], out=o, lse=lse)
+        wise.cache_weights(now["q"], cache, lse, w, new_len=now["news"])
+        got.append((o.clone(), lse.clone(), w.clone()))
+    wise.check_device()
+    for i, x in zip(order, got):
+        assert _same(x, wants[i])
+
+
 def test_two_graphs_in_turn():
     a, b = _Server(2), _Server(3, b=4, hk=1, h=4, d=128, page=16, prompt=200, steps=3)
     wants = [_reference(x) for x in (a, b)]

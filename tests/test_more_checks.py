@@ -221,3 +221,14 @@ def test_oracle_kept_tokens():
     assert C.kept_tokens(w, 8, 3, 0, 1) == [0, 1, 6]
     assert C.kept_tokens(w, 8, 7, 0, 0) == [0, 1, 3, 4, 5, 6, 7]  # NaN goes first
     assert C.kept_tokens(w, 8, 8, 2, 2) == list(range(8))
+
+
+def test_prefix_workspace_grows_with_the_batch_alone(lib):
+    """Two rows of fp32 results a query row, records of the units, partial results
+    of the blocks (304 of 256 rows and statistics): no product of groups and rows."""
+    for batch, groups in ((64, 1), (64, 64), (8192, 1), (8192, 8192), (65535, 65535)):
+        c = _cache(batch=batch, kv_heads=8, head_dim=128, page=64, kp=None, vp=None, table=None, lengths=None)
+        rows = batch * 32
+        parts = 304 * (256 * 128 + 2 * 256) * 4
+        most = rows * 2 * (128 + 1) * 4 + 2 * parts + (batch * 8 + (batch * 4 // 256 + groups + 1) * 8) * 32 + (3 * groups + 3 * batch + 3) * 4 + 8192
+        assert 0 < lib.wise_attn_prefix_workspace(c, 32, 1, groups) <= most
