@@ -823,7 +823,10 @@ def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.T
     read once for all of them. The page table names the shared pages for each
     sequence; whole tiles of 128 tokens are shared, the rest is read by each
     sequence. Sequences outside the groups, or shorter than their group's
-    prefix, share nothing. Everything else is as in :func:`tree_attention`."""
+    prefix, share nothing. Everything else is as in :func:`tree_attention`,
+    which is the faster call until sharing saves some 70 to 130 MB of keys and
+    values (next tokens, 32/8 heads of 128: 4 sequences from 8K shared tokens
+    on, 16 from 2K, 64 from 512)."""
     desc, dev = _check_cache(cache)
     handle = _check_stream(stream, dev)
     lib = _lib.load()
