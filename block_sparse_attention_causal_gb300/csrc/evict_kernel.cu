@@ -6,9 +6,8 @@
 // Two launches: the selection writes each head's list of kept places, the move
 // copies their rows. Measured (one GB300): 16 sequences of up to 8K, 8 key heads of
 // 128, cut to 4K (474 MB): 86.8 us, 14 of them the selection and 70 the move, which
-// runs at a copy's rate; one of 32K cut to 2K: 21 us, 16 the selection (eight blocks a
-// head; of one pass over 11 bits 1.5 us are the cluster's barrier, 2.5 the counts of
-// eight blocks).
+// runs at a copy's rate; one of 32K cut to 2K: 17.4 us, 12 the selection (eight blocks
+// a head; 21.3 us when each block summed all 2048 counts of all eight).
 #include <cooperative_groups.h>
 
 #include "internal.h"
@@ -40,15 +39,24 @@ __device__ __forceinline__ int evict_length(const EvictLaunch& e, int b, bool fl
   return (int)(l < 0 ? 0 : l > most ? most : l);
 }
 
+__device__ __forceinline__ uint32_t inclusive_sum(uint32_t x, int lane) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t v = __shfl_up_sync(0xffffffffu, x, o);
+    if (lane >= o) x += v;
+  }
+  return x;
+}
+
 // A cluster of C blocks per (sequence, key head); block r holds the r-th part of
 // the places that compete, each of its warps consecutive ones. The weight that
 // the last kept place has is found from the top, 11, 11 and 10 bits at a time:
-// each block counts its weights by those bits in shared memory, and all blocks
-// sum the counts of all.
+// each block counts its weights by those bits in shared memory, and one warp of each
+// sums the counts of all, first of 64 bins together, then of the 64 that matter.
 template <int C>
 __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictLaunch e) {
-  __shared__ uint32_t hist[3][2048];
-  __shared__ uint32_t sums[kSelWarps], found[3];
+  __shared__ uint32_t hist[3][2048], coarse[3][kSelWarps];
+  __shared__ uint32_t found[3];
   __shared__ uint32_t greater[kSelWarps], equal[kSelWarps];
   __shared__ uint2 totals[C];  // of each block of the cluster: weights above the cut, weights at it
   grid_wait();
@@ -100,35 +108,41 @@ __global__ void __launch_bounds__(kSelThreads) select_kernel(const EvictLaunch e
     each([&](int, uint32_t key, bool in) {
       if (in && (pass == 0 || (key >> above) == (cut >> above))) atomicAdd(&h[(key >> shift) & 2047u], 1u);
     });
+    // sums of 64 bins, a warp each; then, by one warp, the 64 bins in which the last
+    // place lies, and the bin among them, both over the counts of all blocks
+    __syncthreads();
+    const uint2 x = *reinterpret_cast<const uint2*>(h + 64 * warp + 2 * lane);
+    const uint32_t x64 = __reduce_add_sync(0xffffffffu, x.x + x.y);
+    if (lane == 0) coarse[pass][warp] = x64;
     if (C == 1) __syncthreads();
     else cluster.sync();
-    // from the highest bin on: thread t has bins 2047 - 2t and 2046 - 2t
-    const int bin = 2047 - 2 * tid;
-    uint32_t n1 = 0u, n0 = 0u;
+    if (warp == 0) {
+      // from the highest on: lane l has sums 31 - l, then bins 63 - 2l and 62 - 2l
+      uint32_t n = 0u;
 #pragma unroll
-    for (int r = 0; r < C; ++r) {
-      const uint32_t* o = C == 1 ? h : cluster.map_shared_rank(h, r);
-      const uint2 x = *reinterpret_cast<const uint2*>(o + bin - 1);
-      n0 += x.x;
-      n1 += x.y;
-    }
-    uint32_t before = n0 + n1;
+      for (int r = 0; r < C; ++r) n += (C == 1 ? coarse[pass] : cluster.map_shared_rank(coarse[pass], r))[31 - lane];
+      uint32_t before = inclusive_sum(n, lane) - n;
+      const uint32_t at = __ballot_sync(0xffffffffu, before < left && left <= before + n);
+      const int c = 31 - (__ffs(at) - 1);  // (there is one: `left` places are left)
+      const uint32_t rest = left - __shfl_sync(0xffffffffu, before, 31 - c);
+      const int bin = 64 * c + 63 - 2 * lane;
+      uint32_t n1 = 0u, n0 = 0u;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t v = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= o) before += v;
-    }
-    if (lane == 31) sums[warp] = before;
-    __syncthreads();
-    before += __reduce_add_sync(0xffffffffu, lane < warp ? sums[lane] : 0u) - n0 - n1;
-    if (before < left && left <= before + n1) {
-      found[0] = (uint32_t)bin;
-      found[1] = left - before;
-      found[2] = n1;
-    } else if (before + n1 < left && left <= before + n1 + n0) {
-      found[0] = (uint32_t)bin - 1u;
-      found[1] = left - before - n1;
-      found[2] = n0;
+      for (int r = 0; r < C; ++r) {
+        const uint2 y = *reinterpret_cast<const uint2*>((C == 1 ? h : cluster.map_shared_rank(h, r)) + bin - 1);
+        n0 += y.x;
+        n1 += y.y;
+      }
+      before = inclusive_sum(n0 + n1, lane) - n0 - n1;
+      if (before < rest && rest <= before + n1) {
+        found[0] = (uint32_t)bin;
+        found[1] = rest - before;
+        found[2] = n1;
+      } else if (before + n1 < rest && rest <= before + n1 + n0) {
+        found[0] = (uint32_t)bin - 1u;
+        found[1] = rest - before - n1;
+        found[2] = n0;
+      }
     }
     __syncthreads();
     cut |= found[0] << shift;
