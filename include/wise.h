@@ -614,7 +614,7 @@ typedef struct wise_rope {
  *   rope       : NULL: no rotation.
  *   norm       : NULL: no norm.
  * The rest is as in wise_cache_append; q_out must not overlap the weights or the
- * axes either. One launch.
+ * axes either, and heads + 2 kv_heads is at most 2^18. One launch.
  */
 int wise_cache_append_norm(const wise_paged_cache* cache, int32_t new_tokens, const wise_rows* k, const wise_rows* v,
                            int32_t heads, const wise_rows* q, void* q_out, const int32_t* new_len,
@@ -624,7 +624,8 @@ int wise_cache_append_norm(const wise_paged_cache* cache, int32_t new_tokens, co
 /*
  * wise_norm_rotate -- the same for dense rows: queries and keys as a prompt's
  * attention (wise_attn_discover, wise_attn_sparse) takes them.
- *   batch, new_tokens (n), head_dim in {64, 96, 128}; batch * n < 2^31.
+ *   batch, new_tokens (n), head_dim in {64, 96, 128}; batch * n < 2^31;
+ *   heads + kv_heads <= 2^18.
  *   q, q_out   : [batch, heads, n, head_dim]; q_out dense, 16-byte aligned.
  *   k, k_out   : [batch, kv_heads, n, head_dim]; k NULL: kv_heads and k_out
  *                are ignored.
