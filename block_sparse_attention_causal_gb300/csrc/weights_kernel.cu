@@ -18,8 +18,8 @@
 //
 // Measured (one GB300): next tokens of 32 sequences of up to 8K, 32/8 heads of 128,
 // 339 MB: 57.8 us, 86 % of a copy's rate (4 us before the first tile, 2 after the
-// last); 128 rows of each key head over 32K tokens 20.3 us, 0.85 us a tile (its bytes
-// 0.74); 256 rows over 131K 92 us, bound by the sums.
+// last); 128 rows of each key head over 32K tokens 19.5 us, 0.8 us a tile (its bytes
+// 0.74); 256 rows over 131K 85 us, bound by the sums.
 #include <type_traits>
 
 #include "tree.cuh"
@@ -374,22 +374,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (h0 == 0) bad = tile_bad<1>(ring, tau, abort_flag, err);
             tc_fence_after();
             const int cols = some ? min(a.half, live - h0) : 0;
-            // the next 16 columns are on their way while these are summed
-            uint32_t v0[16], v1[16];
-            __syncwarp();
-            if (cols > 0) {
-              tmem_ld_x16(tS, v0);
-              for (int c0 = 0; c0 < cols; c0 += 32) {
-                __syncwarp();
-                tmem_wait_ld16(v0);
-                if (c0 + 16 < cols) tmem_ld_x16(tS + c0 + 16, v1);
-                block(h0 + c0, v0);
-                if (c0 + 16 >= cols) break;
-                __syncwarp();
-                tmem_wait_ld16(v1);
-                if (c0 + 32 < cols) tmem_ld_x16(tS + c0 + 32, v0);
-                block(h0 + c0 + 16, v1);
-              }
+            // the scores of 32 rows at a time (16, with the next 16 on their way: 256 rows
+            // over 131K tokens 92 us instead of 85; 48 spill registers, 113 us)
+            for (int c0 = 0; c0 < cols; c0 += 32) {
+              uint32_t v0[16], v1[16];
+              const bool both = c0 + 16 < cols;
+              __syncwarp();
+              tmem_ld_x16(tS + c0, v0);
+              if (both) tmem_ld_x16(tS + c0 + 16, v1);
+              tmem_wait_ld16(v0);
+              if (both) tmem_wait_ld16(v1);
+              block(h0 + c0, v0);
+              if (both) block(h0 + c0 + 16, v1);
             }
             tc_fence_before();
             __syncwarp();
