@@ -218,16 +218,19 @@ __global__ void __launch_bounds__(kMoveThreads) move_kernel(const EvictLaunch e)
   const int64_t unit = blockIdx.x / e.chunks;
   const int64_t i0 = (int64_t)(blockIdx.x - unit * e.chunks) * kMoveTokens;
   const int b = (int)(unit / e.cache.kv_heads), hk = (int)(unit % e.cache.kv_heads);
-  const int keep = min(evict_length(e, b, false), e.budget);
+  const int len = evict_length(e, b, false), keep = min(len, e.budget);
   const int some = (int)max((int64_t)0, min((int64_t)kMoveTokens, keep - i0));
   if (threadIdx.x < kMoveTokens) {
     const int64_t i = i0 + threadIdx.x;
     float weight = 0.f;
     if (i < keep) {
       const int32_t src = e.list[unit * e.list_width + i];
-      weight = e.weights[unit * e.width + src];
-      int64_t f = row_offset(e.cache, e.cache.page_table + (int64_t)b * e.cache.max_pages, e.cache.max_pages, src, hk, D, e.err);
-      const int64_t t = row_offset(e.cache, e.to_table + (int64_t)b * e.to_pages, e.to_pages, i, hk, D, e.err);
+      int64_t f = -1, t = -1;
+      if (src >= 0 && src < len) {  // (else the workspace was written by another call meanwhile)
+        weight = e.weights[unit * e.width + src];
+        f = row_offset(e.cache, e.cache.page_table + (int64_t)b * e.cache.max_pages, e.cache.max_pages, src, hk, D, e.err);
+        t = row_offset(e.cache, e.to_table + (int64_t)b * e.to_pages, e.to_pages, i, hk, D, e.err);
+      }
       if (t < 0 || f == t) f = -1;  // (in its place already)
       from[threadIdx.x] = f;
       to[threadIdx.x] = t;

@@ -567,7 +567,7 @@ size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, 
  *                    together, the rest by each sequence. Sequences with fewer
  *                    committed tokens share nothing (an empty place of a padded
  *                    batch).
- *   workspace      : wise_attn_prefix_workspace bytes.
+ *   workspace      : wise_attn_prefix_workspace bytes (as for wise_attn_tree).
  * group_starts that are not ascending or out of range are flagged, and nothing
  * is shared then; prefix_lengths below 0 or past the page table are flagged, and
  * their groups share nothing (WISE_ERR_BAD_CACHE). Four launches.
@@ -677,7 +677,8 @@ size_t wise_cache_evict_workspace(const wise_paged_cache* cache, int32_t budget)
  *   new_lengths: [batch] int32: min(lengths[b], budget).
  *   weights_out: float32 [batch, kv_heads, width_out], width_out >= budget;
  *                entries behind the kept tokens are zero.
- *   workspace  : wise_cache_evict_workspace bytes (device, 16-byte aligned).
+ *   workspace  : wise_cache_evict_workspace bytes (device, 16-byte aligned;
+ *                scratch, one for each call that may run at the same time).
  * The outputs and the workspace must not overlap each other or the inputs
  * (refused), nor the pools one another. Drafted tokens behind the committed ones
  * stay behind. Lengths that are negative, or past the page table or width, are
