@@ -811,8 +811,8 @@ def tree_attention(q: torch.Tensor, cache: PagedCache, *, new_len: Optional[torc
 
 
 def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.Tensor, *,
-                     group_starts: Optional[torch.Tensor] = None, new_len: Optional[torch.Tensor] = None,
-                     tree_mask: Optional[torch.Tensor] = None, want_lse: bool = True,
+                     group_starts: Optional[torch.Tensor] = None, max_members: int = 0,
+                     new_len: Optional[torch.Tensor] = None, tree_mask: Optional[torch.Tensor] = None, want_lse: bool = True,
                      out_dtype: torch.dtype = torch.bfloat16, scale: float = 0.0, out: Optional[torch.Tensor] = None,
                      lse: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None,
                      stream: Optional[torch.cuda.Stream] = None):
@@ -823,7 +823,8 @@ def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.T
     read once for all of them. The page table names the shared pages for each
     sequence; whole tiles of 128 tokens are shared, the rest is read by each
     sequence. Sequences outside the groups, or shorter than their group's
-    prefix, share nothing. Everything else is as in :func:`tree_attention`,
+    prefix, share nothing. max_members, the sequences of the largest group at
+    most, lets small groups take a kernel for few rows. Everything else is as in :func:`tree_attention`,
     which is the faster call until sharing saves some 70 to 130 MB of keys and
     values (next tokens, 32/8 heads of 128: 4 sequences from 8K shared tokens
     on, 16 from 2K, 64 from 512)."""
@@ -840,6 +841,8 @@ def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.T
     groups = prefix_lengths.shape[0] if isinstance(prefix_lengths, torch.Tensor) and prefix_lengths.dim() == 1 else 0
     if not 1 <= groups <= b or (group_starts is None and groups != 1):
         raise ValueError("prefix_lengths must be an int32 [groups] tensor of 1 to batch groups (one without group_starts)")
+    if not isinstance(max_members, int) or not 0 <= max_members <= _MAX_I32:
+        raise ValueError("max_members must be a non-negative whole number below 2^31")
     pre = _check_array("prefix_lengths", prefix_lengths, torch.int32, (groups,), dev)
     starts = None if group_starts is None else _check_array("group_starts", group_starts, torch.int32, (groups + 1,), dev)
     nl = None if new_len is None else _check_array("new_len", new_len, torch.int32, (b,), dev)
@@ -864,7 +867,7 @@ def prefix_attention(q: torch.Tensor, cache: PagedCache, prefix_lengths: torch.T
     else:
         ws_ptr = own = torch._C._cuda_cudaCachingAllocator_raw_alloc(max(nbytes, 16), handle)
     try:
-        st = lib.wise_attn_prefix(desc, heads, n, qr, groups, starts, pre, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr,
+        st = lib.wise_attn_prefix(desc, heads, n, qr, groups, max_members, starts, pre, nl, mask, scale, _OUT[out_dtype], o_ptr, lse_ptr,
                                   ws_ptr, nbytes, handle)
     finally:
         if own:

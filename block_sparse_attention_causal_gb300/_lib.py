@@ -140,8 +140,8 @@ _SIGNATURES = {
     "wise_attn_tree": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp, _sz, _vp]),
     "wise_cache_accept": (ctypes.c_int, [_cp, _i32, _vp, _vp, _vp, _vp]),
     "wise_attn_prefix_workspace": (_sz, [_cp, _i32, _i32, _i32]),
-    "wise_attn_prefix": (ctypes.c_int, [_cp, _i32, _i32, _rp, _i32, _vp, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp, _vp,
-                                        _sz, _vp]),
+    "wise_attn_prefix": (ctypes.c_int, [_cp, _i32, _i32, _rp, _i32, _i32, _vp, _vp, _vp, _vp, ctypes.c_float, _i32, _vp, _vp,
+                                        _vp, _sz, _vp]),
     "wise_cache_append_norm": (ctypes.c_int, [_cp, _i32, _rp, _rp, _i32, _rp, _vp, _vp, _vp, _op, _np, _vp]),
     "wise_norm_rotate": (ctypes.c_int, [_i32, _i32, _i32, _i32, _rp, _vp, _i32, _rp, _vp, _vp, _op, _np, _vp]),
     "wise_cache_weights": (ctypes.c_int, [_cp, _i32, _i32, _rp, _vp, _vp, _vp, ctypes.c_float, _vp, _i64, _vp]),

@@ -222,7 +222,8 @@ struct TreeLaunch {
   // are their shared tokens, cache.page_table and the rest are the sequences'
   const int32_t* starts;  // [groups + 1]: each group's first sequence
   const int32_t* leader;  // [groups]: the sequence whose page table is read
-  int32_t sequences;      // of all groups, at most
+  int32_t sequences;      // of all groups
+  int32_t members;        // of a group, at most
 };
 int64_t tree_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim);
 // maps = {K, V}: 3-D tensor maps [n_pages, kv_heads * page, d] with boxes of one
@@ -281,6 +282,7 @@ struct PrefixLaunch {
   int32_t groups;
   const int32_t* group_starts;  // [groups + 1] or null: one group of all sequences
   const int32_t* prefix_lengths;  // [groups]
+  int32_t members;                // sequences of a group, at most
 };
 int64_t prefix_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim, int32_t groups);
 cudaError_t launch_prefix(const PrefixLaunch& p, const CUtensorMap* maps, cudaStream_t stream);

@@ -37,7 +37,7 @@ struct Plan {
 };
 struct PlanParams {
   TreeParams shared, own;
-  int32_t groups;
+  int32_t groups, members;
   const int32_t* group_starts;
   const int32_t* prefix_lengths;
   Plan plan;
@@ -80,6 +80,10 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
       const uint32_t m = __ballot_sync(0xffffffffu, b + lane < b1 && c.lengths[b + lane] >= prefix);
       if (sharing == 0 && m != 0u) leader = b + __ffs(m) - 1;
       sharing += __popc(m);
+    }
+    if (b1 - b0 > p.members) {  // more rows than the launch is made for
+      if (lane == 0) atomicOr(p.own.t.err, kErrBadCache);
+      len = 0;
     }
     if (sharing < 2) len = 0;
     for (int b = b0 + lane; b < b1; b += 32) {
@@ -213,12 +217,13 @@ __global__ void __launch_bounds__(128) shared_join_kernel(const SharedJoin j) {
 struct PrefixLayout {
   int64_t shared, own, o_own, o_shared, lse_own, lse_shared, bytes;  // offsets in bytes; the plan's words at 0
 };
-PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64_t n, int64_t d, int64_t groups) {
+PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64_t n, int64_t d, int64_t groups,
+                           int64_t members) {
   PrefixLayout w;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t per = heads / kv_heads * n, rows = batch * heads * n;
   w.shared = up((3 * groups + 1 + 3 * batch + 2) * 4);
-  w.own = w.shared + up(workspace_layout(shared_units(groups, kv_heads, per * batch), per * batch, d, true).bytes);
+  w.own = w.shared + up(workspace_layout(shared_units(groups, kv_heads, per * batch), per * members, d, true).bytes);
   w.o_own = w.own + up(workspace_layout(tree_units(batch, kv_heads, per), per, d, true).bytes);
   w.o_shared = w.o_own + up(rows * d * 4);
   w.lse_own = w.o_shared + up(rows * d * 4);
@@ -238,12 +243,12 @@ float place_cost(const TreeParams& p) {
 }  // namespace
 
 int64_t prefix_workspace_bytes(int32_t batch, int32_t kv_heads, int32_t heads, int32_t n, int32_t head_dim, int32_t groups) {
-  return prefix_layout(batch, kv_heads, heads, n, head_dim, groups).bytes;
+  return prefix_layout(batch, kv_heads, heads, n, head_dim, groups, batch).bytes;
 }
 
 cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaStream_t stream) {
   const CacheView& c = x.t.cache;
-  const PrefixLayout w = prefix_layout(c.batch, c.kv_heads, x.t.heads, x.t.n, x.t.head_dim, x.groups);
+  const PrefixLayout w = prefix_layout(c.batch, c.kv_heads, x.t.heads, x.t.n, x.t.head_dim, x.groups, x.members);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(x.t.workspace) + 255) / 256 * 256);
   int32_t* words = reinterpret_cast<int32_t*>(ws);
   Plan plan;
@@ -263,6 +268,7 @@ cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaSt
   shared.starts = plan.starts;
   shared.leader = plan.leader;
   shared.sequences = c.batch;
+  shared.members = x.members;
   shared.limit = plan.limit;
   shared.rows_apart = 1;
   shared.workspace = ws + w.shared;
@@ -280,7 +286,7 @@ cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaSt
   own.o = ws + w.o_own;
   own.lse = reinterpret_cast<float*>(ws + w.lse_own);
   const TreeParams ps = tree_params<true>(shared), po = tree_params<false>(own);
-  const PlanParams pp{ps, po, x.groups, x.group_starts, x.prefix_lengths, plan, place_cost(ps), place_cost(po)};
+  const PlanParams pp{ps, po, x.groups, x.members, x.group_starts, x.prefix_lengths, plan, place_cost(ps), place_cost(po)};
   cudaError_t e = launch_chained(plan_kernel, dim3(1), dim3(kPlanThreads), 0, stream, pp);
   if (e == cudaSuccess) e = launch_tree_rows<true>(shared, maps, stream);
   if (e == cudaSuccess) e = launch_tree_rows<false>(own, maps, stream);

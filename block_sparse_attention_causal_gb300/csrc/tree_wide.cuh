@@ -865,7 +865,7 @@ TreeParams tree_params(const TreeLaunch& t) {
   p.t = t;
   p.group = t.heads / t.cache.kv_heads;
   p.group_mul = (uint32_t)((0x100000000ull + p.group - 1) / p.group);
-  p.rows = p.group * t.n * (PREFIX ? t.sequences : 1);
+  p.rows = p.group * t.n * (PREFIX ? t.members : 1);
   p.pairs = (p.rows + 255) / 256;
   p.mask_words = (t.n + 31) / 32;
   p.scale_log2 = t.scale * 1.4426950408889634f;
@@ -874,7 +874,7 @@ TreeParams tree_params(const TreeLaunch& t) {
   // Measured: of 4, 6 and 8 places for wide units, and 0 to 3 for narrow ones, 8
   // and 2 gave the shortest times.
   p.overhead = p.rows > 64 ? kWideOverhead : kNarrowOverhead;
-  const int64_t units = PREFIX ? shared_units(t.cache.batch, t.cache.kv_heads, p.rows)
+  const int64_t units = PREFIX ? shared_units(t.cache.batch, t.cache.kv_heads, (int64_t)p.group * t.n * t.sequences)
                                : tree_units(t.cache.batch, t.cache.kv_heads, p.rows);
   const WorkspaceLayout w = workspace_layout(units, p.rows, t.head_dim, t.rows_apart);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(t.workspace) + 31) / 32 * 32);

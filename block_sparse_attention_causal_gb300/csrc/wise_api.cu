@@ -962,13 +962,13 @@ size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, 
 }
 
 int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, int32_t groups,
-                     const int32_t* group_starts, const int32_t* prefix_lengths, const int32_t* new_len,
-                     const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse, void* workspace,
-                     size_t workspace_bytes, wise_stream_t stream) {
+                     int32_t max_members, const int32_t* group_starts, const int32_t* prefix_lengths,
+                     const int32_t* new_len, const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse,
+                     void* workspace, size_t workspace_bytes, wise_stream_t stream) {
   int st = check_cache(cache, true);
   if (st != WISE_OK) return st;
   if ((st = check_prefix(cache, heads, new_tokens, groups)) != WISE_OK) return st;
-  if (!prefix_lengths || (!group_starts && groups != 1)) return WISE_ERR_INVALID_ARGUMENT;
+  if (!prefix_lengths || (!group_starts && groups != 1) || max_members < 0) return WISE_ERR_INVALID_ARGUMENT;
   if (misaligned4(group_starts) || misaligned4(prefix_lengths)) return WISE_ERR_ALIGNMENT;
   const size_t need = wise_attn_prefix_workspace(cache, heads, new_tokens, groups);
   const int64_t rows = (int64_t)cache->batch * heads * new_tokens;
@@ -987,6 +987,7 @@ int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_t
   p.groups = groups;
   p.group_starts = group_starts;
   p.prefix_lengths = prefix_lengths;
+  p.members = max_members == 0 || max_members > cache->batch ? cache->batch : max_members;
   CUtensorMap maps[2];
   if ((st = tree_maps(maps, cache)) != WISE_OK) return st;
   return launch_prefix(p, maps, reinterpret_cast<cudaStream_t>(stream)) == cudaSuccess ? WISE_OK : WISE_ERR_CUDA;

@@ -560,6 +560,9 @@ size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, 
  * each sequence, as ever), but for the order of sums: a row's shared and own
  * parts are taken apart and joined in fp32.
  *   groups         : 1 <= groups <= batch.
+ *   max_members    : sequences of the largest group at most, where the caller
+ *                    knows it: small groups take a kernel for few rows. 0: not
+ *                    known. Larger groups are flagged and share nothing.
  *   group_starts   : [groups + 1] int32, ascending (not strictly), in
  *                    [0, batch]; sequences outside share nothing. NULL: one
  *                    group of all sequences (groups 1).
@@ -573,9 +576,9 @@ size_t wise_attn_prefix_workspace(const wise_paged_cache* cache, int32_t heads, 
  * their groups share nothing (WISE_ERR_BAD_CACHE). Four launches.
  */
 int wise_attn_prefix(const wise_paged_cache* cache, int32_t heads, int32_t new_tokens, const wise_rows* q, int32_t groups,
-                     const int32_t* group_starts, const int32_t* prefix_lengths, const int32_t* new_len,
-                     const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse, void* workspace,
-                     size_t workspace_bytes, wise_stream_t stream);
+                     int32_t max_members, const int32_t* group_starts, const int32_t* prefix_lengths,
+                     const int32_t* new_len, const int32_t* tree_mask, float scale, int32_t out_dtype, void* o, float* lse,
+                     void* workspace, size_t workspace_bytes, wise_stream_t stream);
 
 /* Norm of each head's values before the rotation:
  *     y = x / sqrt(mean(x^2) + eps) * w     (mean over head_dim values)

@@ -55,6 +55,24 @@ def test_many_sequences_in_many_groups():
     wise.check_device()
     # sum a |v| below 4; both sides within 2 * 2^-8 + 2^-10 of it (weights rounded to bf16, scores' sums)
     assert float((o - ro).abs().max()) <= 2 * (2.0 ** -7 + 2.0 ** -10) * 4.0 and float((lse - rl).abs().max()) <= 2.0 ** -14
+    # with the groups' size known, by the kernel for few rows
+    o, lse = wise.prefix_attention(q, cache, _i32([prefix] * groups), group_starts=starts, max_members=members, out_dtype=torch.float32)
+    wise.check_device()
+    assert float((o - ro).abs().max()) <= 2 * (2.0 ** -7 + 2.0 ** -10) * 4.0 and float((lse - rl).abs().max()) <= 2.0 ** -14
+
+
+@pytest.mark.parametrize("most", [1, 2, 3, 6, 40])
+def test_groups_larger_than_said_share_nothing(most):
+    """Sizes of groups that are not what the caller said are flagged; results stay."""
+    rng = np.random.default_rng(33)
+    starts, prefixes = [0, 2, 3, 6], [256, 300, 390]
+    lengths = [260, 270, 300, 400, 390, 444]
+    cache, table = _shared_cache(rng, starts, prefixes, lengths, [3] * 6, 2, 96, 32)
+    q = _bf16(rng.standard_normal((6, 12, 3, 96)))
+    sees = _mask(rng, 6, 3, "run")[0]
+    got = wise.prefix_attention(q, cache, _i32(prefixes), group_starts=_i32(starts), max_members=most, out_dtype=torch.float32)
+    assert wise.device_status() == (wise._lib.WISE_ERR_BAD_CACHE if most < 3 else 0)
+    _check(q, cache, table, sees, lengths, [3] * 6, got, torch.float32)
 
 
 def test_rows_past_the_page_table_are_empty():
@@ -286,7 +304,7 @@ def test_given_buffers():
     for bad in (lambda: wise.prefix_attention(q, cache, s.pre, workspace=ws), lambda: wise.prefix_attention(q, cache, s.pre, out=out[:1]),
                 lambda: wise.prefix_attention(q[:, :3], cache, s.pre), lambda: wise.prefix_attention(q, cache, _i32([300, 300])),
                 lambda: wise.prefix_attention(q, cache, s.pre.long()), lambda: wise.prefix_attention(q, cache, s.pre, group_starts=_i32([0])),
-                lambda: wise.prefix_attention(q, cache, s.pre, out_dtype=torch.float16),
+                lambda: wise.prefix_attention(q, cache, s.pre, out_dtype=torch.float16), lambda: wise.prefix_attention(q, cache, s.pre, max_members=-1),
                 lambda: wise.cache_weights(q, cache, lse[:, :2], s.weights), lambda: wise.cache_weights(q, cache, lse, s.weights[0]),
                 lambda: wise.cache_weights(q, cache, lse, s.weights.double()), lambda: wise.cache_weights(q, cache, lse.half(), s.weights),
                 lambda: wise.cache_weights(q, cache, lse, s.weights[..., ::2]),

@@ -46,7 +46,7 @@ BAD_CACHES = [
 def test_bad_cache_descriptors(lib, bad, status):
     c = _cache(**bad)
     assert lib.wise_cache_append_norm(c, 1, _rows(), _rows(), 0, None, None, None, None, None, None, None) == status
-    assert lib.wise_attn_prefix(c, 2, 1, _rows(), 1, None, 16, None, None, 0.0, 0, 16, None, 16, 1 << 30, None) == status
+    assert lib.wise_attn_prefix(c, 2, 1, _rows(), 1, 0, None, 16, None, None, 0.0, 0, 16, None, 16, 1 << 30, None) == status
     assert lib.wise_cache_weights(c, 2, 1, _rows(), 16, None, None, 0.0, 64 * MB, 8, None) == status
     assert lib.wise_cache_evict(c, 16, 8, 4, 0, 0, 16, 1, 64 * MB, 65 * MB, 8, 66 * MB, 1 << 20, None) == status
 
@@ -110,15 +110,15 @@ def test_prefix_arguments(lib):
     ws = lib.wise_attn_prefix_workspace(_cache(), 4, 3, 1)
     assert ws > lib.wise_attn_tree_workspace(_cache(), 4, 3)
 
-    def call(c=None, heads=4, n=3, q=None, groups=1, starts=None, pre=48 * MB, new_len=None, mask=None, scale=0.0, dtype=0,
+    def call(c=None, heads=4, n=3, q=None, groups=1, members=0, starts=None, pre=48 * MB, new_len=None, mask=None, scale=0.0, dtype=0,
              o=32 * MB, lse=None, w=64 * MB, wb=ws):
-        return lib.wise_attn_prefix(c or _cache(), heads, n, q or _rows(), groups, starts, pre, new_len, mask, scale, dtype, o, lse,
+        return lib.wise_attn_prefix(c or _cache(), heads, n, q or _rows(), groups, members, starts, pre, new_len, mask, scale, dtype, o, lse,
                                     w, wb, None)
     assert call(heads=3) == INVALID and call(heads=0) == INVALID and call(n=0) == INVALID and call(n=129) == UNSUPPORTED
     assert call(groups=0) == INVALID and call(groups=3) == INVALID  # more groups than sequences
     assert call(groups=2, wb=1 << 30) == INVALID                    # two groups without their starts
     assert call(pre=None) == INVALID and call(pre=2) == ALIGNMENT and call(starts=50 * MB + 1) == ALIGNMENT
-    assert call(dtype=2) == INVALID and call(scale=-1.0) == INVALID and call(scale=float("nan")) == INVALID
+    assert call(members=-1) == INVALID and call(dtype=2) == INVALID and call(scale=-1.0) == INVALID and call(scale=float("nan")) == INVALID
     assert call(o=None) == INVALID and call(o=8) == ALIGNMENT and call(lse=2) == ALIGNMENT and call(mask=2) == ALIGNMENT
     assert call(new_len=2) == ALIGNMENT and call(q=_rows(strides=(64, 64, 12))) == ALIGNMENT
     assert call(w=None) == WORKSPACE and call(wb=ws - 1) == WORKSPACE and call(w=64 * MB + 8) == ALIGNMENT
