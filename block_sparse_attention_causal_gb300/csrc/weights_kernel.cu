@@ -17,9 +17,10 @@
 // The key tiles of all (sequence, key head) units form the line of tree.cuh.
 //
 // Measured (one GB300): next tokens of 32 sequences of up to 8K, 32/8 heads of 128,
-// 339 MB: 57.8 us, 86 % of a copy's rate (4 us before the first tile, 2 after the
-// last); 128 rows of each key head over 32K tokens 19.5 us, 0.8 us a tile (its bytes
-// 0.74); 256 rows over 131K 85 us, bound by the sums.
+// 339 MB: 57.5 us, 87 % of a copy's rate (4 us before the first tile, 2 after the
+// last); 128 rows of each key head over 32K tokens 18.6 us, 0.8 us a tile (its bytes
+// 0.74); 256 rows over 131K 83 us, bound by the sums; 1600 rows over 1000 62 us, seven
+// launches of 9.
 #include <type_traits>
 
 #include "tree.cuh"
@@ -49,9 +50,10 @@ struct WeightsParams {
 // Behind the ring and the Q buffers of `cols` rows:
 struct Small {
   float neg_lse2[2][kMaxRows];            // of a segment (its Q's buffer): -LSE in powers of two, -inf: the row adds nothing
-  uint32_t words[2][kTreeMaxTokens * 4];  // [token][new token / 32]: who sees whom
+  uint32_t sees[2][kTreeMaxTokens][kMaxRows / 32];  // of each new token: the rows that see it
+  uint32_t counts[2][kMaxRows / 32];                // the rows that add something
   int plain[2][2];                        // rows from 0 on that all count, as either of its warps found
-  uint64_t q_full[2];   // Q, lse2 and words of a segment are there (2 warps)
+  uint64_t q_full[2];   // Q and what belongs to it are there (2 warps)
   uint64_t seg_done[2];         // and no longer needed (all warps that sum)
   uint64_t s_full[kGroups];     // a group's scores computed
   uint64_t s_empty[kGroups];    // and read (4 warps)
@@ -148,6 +150,30 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (u >= UNITS) continue;
       if (r < live) copy16(at, q + (int64_t)g * p.t.q.sh + (int64_t)tok * p.t.q.sn);
       else *reinterpret_cast<uint4*>(at) = make_uint4(0u, 0u, 0u, 0u);
+    }
+  };
+  // The rows that see each new token, turned round from the mask: 32 rows a word, a
+  // token's rows next to each other.
+  auto turn_mask = [&](const Walk& x, int th, auto threads) {
+    if (x.t1 * kTile <= x.len) return;
+    constexpr int THREADS = decltype(threads)::value;
+    uint32_t* to = &m.sees[q_buf(x.seg)][0][0];
+    const int words = (a.cols + 31) / 32;
+    auto below = [](int k) -> uint32_t { return k <= 0 ? 0u : k >= 32 ? 0xffffffffu : (1u << k) - 1u; };
+    for (int y = th; y < x.nl * words; y += THREADS) {
+      const int j = y / words, w = y - j * words, row = a.row0 + 32 * w;  // the word's first row
+      uint32_t v = 0u;
+      if (!p.t.tree_mask) {
+        v = ~below(j * p.group - row);  // the rows of tokens j and later
+      } else {
+        const int last = min(row_token(p, row + 31), x.nl - 1);
+        const int32_t* mask = p.t.tree_mask + (int64_t)x.b * p.t.n * p.mask_words + (j >> 5);
+#pragma unroll 4
+        for (int i = row_token(p, row); i <= last; ++i)
+          if (((uint32_t)mask[(int64_t)i * p.mask_words] >> (j & 31)) & 1u)
+            v |= below((i + 1) * p.group - row) & ~below(i * p.group - row);
+      }
+      to[j * (kMaxRows / 32) + w] = v;
     }
   };
   // the first segment's Q is copied by all but the first two warps (by the two that
@@ -289,25 +315,20 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         if (w.seg == 0) copy_q(w, th, std::integral_constant<int, ALL>());
         else copy_q(w, th, std::integral_constant<int, 64>());
+        if (w.seg == 0) turn_mask(w, th, std::integral_constant<int, ALL>());
+        else turn_mask(w, th, std::integral_constant<int, 64>());
         int first = live;  // first row that adds nothing
 #pragma unroll
         for (int k = 0; k < kMaxRows / 64; ++k) {
           const int r = th + 64 * k;
-          if (r >= a.cols) break;
+          const uint32_t some = __ballot_sync(0xffffffffu, l[k] != -INFINITY);
+          if (lane == 0) m.counts[buf][r >> 5] = some;
+          if (r >= a.cols) continue;
           if (l[k] == -INFINITY) first = min(first, r);
           m.neg_lse2[buf][r] = l[k] == -INFINITY ? -INFINITY : l[k] * -1.4426950408889634f;
         }
         first = __reduce_min_sync(0xffffffffu, first);
         if (lane == 0) m.plain[buf][warp & 1] = first;
-        // which new tokens each token sees
-        if (w.t1 * kTile > w.len)
-          for (int x = th; x < w.nl * 4; x += 64) {
-            const int i = x >> 2, j0 = (x & 3) * 32;
-            uint32_t v = 0u;
-            if (p.t.tree_mask) v = (x & 3) < p.mask_words ? (uint32_t)p.t.tree_mask[((int64_t)w.b * p.t.n + i) * p.mask_words + (x & 3)] : 0u;
-            else v = i >= j0 + 31 ? 0xffffffffu : i < j0 ? 0u : (2u << (i - j0)) - 1u;
-            m.words[buf][x] = v;
-          }
         if (w.seg == 0) {
           first_q();
         } else {
@@ -327,6 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       uint32_t tau = 0, used = 0;
       bool ok = true;
       copy_q(w, (int)threadIdx.x - 64, std::integral_constant<int, ALL>());
+      turn_mask(w, (int)threadIdx.x - 64, std::integral_constant<int, ALL>());
       first_q();
       do {
         const int buf = q_buf(w.seg);
@@ -347,22 +369,28 @@ __global__ void __launch_bounds__(kThreads, 1)
           const bool some = t * kTile + quarter * 32 < w.keys;
           uint64_t sum[2] = {0ull, 0ull};
           const int j = pos - w.len;  // (negative: a committed token)
-          const uint32_t* word = m.words[buf] + ((j > 0 ? j : 0) >> 5 & 3);
+          // the words of rows that see the key
+          const uint32_t* sees = m.sees[buf][min(max(j, 0), kTreeMaxTokens - 1)];
           auto block = [&](int c0, const uint32_t (&v)[16]) {
             if (!tail && c0 + 16 <= plain) {
               add8(neg_lse2 + c0, v, sl2, sum);
               add8(neg_lse2 + c0 + 8, v + 8, sl2, sum);
             } else {
-              // rows that do not see the key, or add nothing (no branches: a warp's
-              // columns follow one another)
+              // rows that do not see the key, or add nothing, are left out, whatever
+              // their scores are
+              const uint32_t bits = ((j < 0 ? 0xffffffffu : j < w.nl ? sees[c0 >> 5] : 0u) & m.counts[buf][c0 >> 5]) >> (c0 & 16);
               float e[2] = {0.f, 0.f};
 #pragma unroll
-              for (int c = 0; c < 16; ++c) {
-                const int tok = min(row_token(p, a.row0 + c0 + c), w.nl - 1);
-                const bool sees = (j < 0) | ((word[tok * 4] >> (j & 31)) & (j < w.nl));
-                const float l = neg_lse2[c0 + c];
-                const float x = fast_exp2(fmaf(__uint_as_float(v[c]), sl2, l));
-                e[c & 1] += sees & (l != -INFINITY) ? x : 0.f;
+              for (int c = 0; c < 16; c += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(neg_lse2 + c0 + c);
+                const float x0 = fast_exp2(fmaf(__uint_as_float(v[c]), sl2, l.x));
+                const float x1 = fast_exp2(fmaf(__uint_as_float(v[c + 1]), sl2, l.y));
+                const float x2 = fast_exp2(fmaf(__uint_as_float(v[c + 2]), sl2, l.z));
+                const float x3 = fast_exp2(fmaf(__uint_as_float(v[c + 3]), sl2, l.w));
+                e[0] += (bits >> c) & 1u ? x0 : 0.f;
+                e[1] += (bits >> (c + 1)) & 1u ? x1 : 0.f;
+                e[0] += (bits >> (c + 2)) & 1u ? x2 : 0.f;
+                e[1] += (bits >> (c + 3)) & 1u ? x3 : 0.f;
               }
               sum[0] = fadd2(sum[0], f2_pack(e[0], e[1]));
             }
