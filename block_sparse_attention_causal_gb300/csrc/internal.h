@@ -10,7 +10,12 @@ namespace wise {
 // precedes them in the stream: a kernel that has triggered (grid_trigger) lets
 // the next one's blocks start and set themselves up while it still runs. Every
 // block calls grid_wait before its first access to global memory, which waits
-// until the kernels before it are complete and their writes visible. What those
+// until the kernels before it are complete and their writes visible, and before
+// it triggers: when a launch's blocks start, the launch two before it is complete.
+// One launch runs beside the one before it instead (the own parts of
+// wise_attn_prefix): it calls grid_wait at its end, and what it reads was ordered
+// by a word that the plan, two launches before it, released and it acquires
+// (TreeLaunch::go). What earlier kernels
 // may have written is loaded plainly, never with __ldg: that names data which
 // nothing writes while the kernel runs, so the compiler may move it above the
 // wait.
@@ -200,6 +205,7 @@ cudaError_t launch_cache_accept(const AcceptLaunch& a, cudaStream_t stream);
 // Attention of new tokens over a paged cache (tree_wide.cuh, tree_narrow.cuh). The key
 // tiles and kTreeOverhead places of each unit must number at most 2^31 - 1.
 constexpr int kTreeMaxTokens = 128;
+constexpr uint64_t kPlanTag = 0x706c616eull << 32;  // upper half of TreeLaunch::go
 constexpr int kTreeOverhead = 8;  // at most this many places of the line of work per unit, besides its key tiles
 struct TreeLaunch {
   CacheView cache;
@@ -216,7 +222,9 @@ struct TreeLaunch {
   // For wise_attn_prefix's two launches (null and 0 elsewhere):
   const int32_t* skip;    // [batch]: tokens at the front of each sequence that are left out
   const int32_t* limit;   // blocks that share the work (the others leave at once)
-  int32_t beside;         // runs beside the launch before it, which it waits for at its end
+  // Set: runs beside the launch before it, which it waits for at its end. The plan's
+  // word: kPlanTag, and the blocks that share the work below it; taken back by the join.
+  const uint64_t* go;
   int32_t rows_apart;     // records of all units, and no join
   // for groups of sequences over what they share: cache.batch counts groups, cache.lengths
   // are their shared tokens, cache.page_table and the rest are the sequences'

@@ -27,13 +27,14 @@ template cudaError_t launch_tree_rows<true>(const TreeLaunch&, const CUtensorMap
 namespace {
 
 struct Plan {
+  uint64_t* go;     // kPlanTag and, below it, the blocks of the own parts: written last
   int32_t* starts;  // [groups + 1]
   int32_t* length;  // [groups] shared tokens, whole tiles
   int32_t* leader;  // [groups]
   int32_t* skip;    // [batch] the sequence's shared tokens
   int32_t* group;   // [batch] its group, where it shares any
   int32_t* live;    // [batch] its new tokens, as far as the page table holds them
-  int32_t* limit;   // [2] blocks of the shared part and of the own parts
+  int32_t* limit;   // blocks of the shared part
 };
 struct PlanParams {
   TreeParams shared, own;
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kPlanThreads) plan_kernel(const PlanParams p) 
     int blocks = a == 0.f ? 0 : (int)((float)kTreeCtas * a / (a + b) + 0.5f);
     if (a != 0.f) blocks = min(max(blocks, 1), kTreeCtas - 1);
     p.plan.limit[0] = blocks;
-    p.plan.limit[1] = kTreeCtas - blocks;
+    st_release_gpu(p.plan.go, kPlanTag | (uint32_t)(kTreeCtas - blocks));
   }
 }
 
@@ -186,6 +187,7 @@ template <int D>
 __global__ void __launch_bounds__(128) shared_join_kernel(const SharedJoin j) {
   grid_wait();
   grid_trigger();
+  if (blockIdx.x == 0 && threadIdx.x == 0) *j.plan.go = 0ull;  // a later call's own parts must not take it for theirs
   const TreeParams& own = j.own;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int kv_heads = own.t.cache.kv_heads, per = kv_heads * (D / 16);
@@ -222,7 +224,7 @@ PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64
   PrefixLayout w;
   auto up = [](int64_t x) { return (x + 255) / 256 * 256; };
   const int64_t per = heads / kv_heads * n, rows = batch * heads * n;
-  w.shared = up((3 * groups + 1 + 3 * batch + 2) * 4);
+  w.shared = up(8 + (3 * groups + 1 + 3 * batch + 1) * 4);
   w.own = w.shared + up(workspace_layout(shared_units(groups, kv_heads, per * batch), per * members, d, true).bytes);
   w.o_own = w.own + up(workspace_layout(tree_units(batch, kv_heads, per), per, d, true).bytes);
   w.o_shared = w.o_own + up(rows * d * 4);
@@ -250,9 +252,9 @@ cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaSt
   const CacheView& c = x.t.cache;
   const PrefixLayout w = prefix_layout(c.batch, c.kv_heads, x.t.heads, x.t.n, x.t.head_dim, x.groups, x.members);
   uint8_t* ws = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(x.t.workspace) + 255) / 256 * 256);
-  int32_t* words = reinterpret_cast<int32_t*>(ws);
   Plan plan;
-  plan.starts = words;
+  plan.go = reinterpret_cast<uint64_t*>(ws);
+  plan.starts = reinterpret_cast<int32_t*>(ws + 8);
   plan.length = plan.starts + x.groups + 1;
   plan.leader = plan.length + x.groups;
   plan.skip = plan.leader + x.groups;
@@ -278,8 +280,7 @@ cudaError_t launch_prefix(const PrefixLaunch& x, const CUtensorMap* maps, cudaSt
   // each sequence's own
   TreeLaunch own = x.t;
   own.skip = plan.skip;
-  own.limit = plan.limit + 1;
-  own.beside = 1;
+  own.go = plan.go;
   own.rows_apart = 1;
   own.workspace = ws + w.own;
   own.out_f32 = 1;

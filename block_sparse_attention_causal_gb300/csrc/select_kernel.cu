@@ -287,16 +287,6 @@ constexpr int kEmitStage = 1024;  // column entries staged per warp in the emit
 // a finalize-only launch, by a memset) before the finalize kernel runs.
 constexpr uint64_t kLbAggregate = 1ull << 62, kLbInclusive = 2ull << 62, kLbValue = (1ull << 62) - 1;
 
-
-__device__ __forceinline__ uint64_t ld_acquire_gpu(const uint64_t* p) {
-  uint64_t v;
-  asm volatile("ld.acquire.gpu.global.u64 %0, [%1];" : "=l"(v) : "l"(p) : "memory");
-  return v;
-}
-__device__ __forceinline__ void st_release_gpu(uint64_t* p, uint64_t v) {
-  asm volatile("st.release.gpu.global.u64 [%0], %1;" ::"l"(p), "l"(v) : "memory");
-}
-
 // Rank the units of one group of (batch, head) slices by cost (listed
 // blocks), heaviest first, ties by unit index, and write their global order:
 // a stable counting sort. The units are split into order_segs contiguous

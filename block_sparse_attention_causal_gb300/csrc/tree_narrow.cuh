@@ -187,8 +187,12 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   prefetch_tables(p);
-  wait_at_start(p.t);
-  if (left_out(p.t)) {
+  const int blocks = wait_at_start(p.t, misc + 2);
+  if (blocks < 0) {
+    clear_recs(p);
+    if (threadIdx.x == 0) atomicOr(err, kErrInternal);
+  }
+  if ((int)blockIdx.x >= blocks) {
     grid_trigger();
     wait_at_end(p.t);
     return;
@@ -201,7 +205,7 @@ __global__ void __launch_bounds__(kNarrowThreads, 1)
   }
   grid_trigger();
   LinePart part;
-  find_part<kNarrowThreads, PREFIX>(p, scratch, part);
+  find_part<kNarrowThreads, PREFIX>(p, scratch, part, blocks);
   const uint32_t tbase = *tmem_base_slot;
   if (threadIdx.x == 128) clear_rec(p);
   WalkOf<PREFIX> w;

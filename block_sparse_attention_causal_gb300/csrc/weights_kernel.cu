@@ -124,7 +124,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   }
   grid_trigger();
   LinePart part;
-  find_part<kThreads>(p, m.scratch, part);
+  find_part<kThreads>(p, m.scratch, part, (int)gridDim.x);
   const uint32_t tbase = m.tmem_base;
   volatile int* abort_flag = &m.abort_flag;
   const int slots = a.slots;
