@@ -240,6 +240,7 @@ cudaError_t launch_tree(const TreeLaunch& t, const CUtensorMap* maps, cudaStream
 
 // Rows normed per head and rotated (norm_kernel.cu): into a paged cache, or
 // dense ones.
+constexpr int64_t kMaxNormHeads = 1ll << 18;  // of queries, keys and values together
 struct NormLaunch {
   CacheView cache;  // paged
   int32_t paged;

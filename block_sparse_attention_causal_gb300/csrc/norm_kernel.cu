@@ -11,6 +11,7 @@ namespace {
 
 constexpr int kStages = 4;   // heads under way in shared memory (2: 126 us for a prompt of 32K, 4: 121, 6 and 8 the same)
 constexpr int kHeads = 16;   // heads of a block at most (8, 16, 32: 121.9, 121.2, 121.0 us; an image's 71, 64, 66)
+static_assert(kMaxNormHeads / kHeads + 3 <= 65535, "the grid's second axis");
 
 __device__ __forceinline__ void copy16(void* dst, const void* src) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
@@ -318,7 +319,6 @@ cudaError_t launch_norm_d(NormLaunch a, cudaStream_t stream) {
   // are two blocks per SM: 2K tokens take 12.3 us so, 14.4 with one or four per SM.
   int each = kHeads;
   while (each > 1 && blocks * parts(each) < 152 * 2) each /= 2;
-  while (parts(each) > 65535) each *= 2;  // (the grid's second axis)
   const dim3 grid((unsigned)blocks, (unsigned)parts(each));
   const bool staged = each >= 4;
   auto kernel = staged ? (a.pairs ? norm_kernel<D, true, kStages> : norm_kernel<D, false, kStages>)

@@ -242,7 +242,6 @@ uint8_t* select_scratch() {
 // ------------------------------------------------------------- paged cache
 
 constexpr int64_t kMaxCacheTokens = 1ll << 30;  // per sequence
-constexpr int64_t kMaxNormHeads = 1ll << 18;    // of queries, keys and values together, of a call with norms
 
 // The shape of a cache; with `pointers`, its buffers too.
 int check_cache(const wise_paged_cache* c, bool pointers) {
