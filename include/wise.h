@@ -78,6 +78,11 @@
  *   blocks may start, and set themselves up, while the kernel before them in
  *   the stream still runs, and wait for it before they touch its memory. Later
  *   work on the stream sees nothing of this.
+ * - What a call reads must be there when its stream comes to the call, and must
+ *   not change until the call is complete (work of other streams included). The
+ *   paged-cache kernels read lengths and counts of new tokens several times and
+ *   rely on finding the same each time: a call whose lengths change under it may
+ *   never end.
  * - Argument, shape and alignment errors are reported before any launch and
  *   nothing is written. A failed launch returns WISE_ERR_CUDA. Kernel-side
  *   problems (a malformed support list or page table, a wait that timed out) are recorded in
