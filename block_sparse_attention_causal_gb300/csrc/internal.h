@@ -221,7 +221,7 @@ struct TreeLaunch {
   uint32_t* err;
   // For wise_attn_prefix's two launches (null and 0 elsewhere):
   const int32_t* skip;    // [batch]: tokens at the front of each sequence that are left out
-  const int32_t* limit;   // blocks that share the work (the others leave at once)
+  const int32_t* limit;   // the shared part's: blocks that have a share in it (the others leave at once)
   // Set: runs beside the launch before it, which it waits for at its end. The plan's
   // word: kPlanTag, and the blocks that share the work below it; taken back by the join.
   const uint64_t* go;

@@ -603,13 +603,14 @@ __device__ __forceinline__ void ring_guard(const TreeParams& p, WalkOf<PREFIX> w
 // orders everything that the plan's own wait had made visible, and the barrier hands
 // it on to the block; the fence does so for copies by TMA. Returns the blocks that
 // share the work (the others leave at once), or -1: the word is not there (it is not
-// waited for). `blocks`: a word of shared memory. (Against a fence without the word,
-// in graphs: trees of three groups 48.2 instead of 47.5 us, 64 next tokens behind 32K
-// 77.8 and 77.9.)
+// waited for). `blocks`: a word of shared memory. (In graphs, against a fence without
+// the word: 64 next tokens behind 32K 78.0 instead of 77.4 us, trees of three groups
+// 46.4 and 46.8.) PREFIX: the shared part, which waits, on a share of the SMs.
+template <bool PREFIX>
 __device__ __forceinline__ int wait_at_start(const TreeLaunch& t, volatile uint32_t* blocks) {
-  if (!t.go) {
+  if (PREFIX || !t.go) {
     grid_wait();
-    return t.limit ? *t.limit : (int)gridDim.x;
+    return PREFIX ? *t.limit : (int)gridDim.x;
   }
   if (threadIdx.x == 0) {
     const uint64_t word = ld_acquire_gpu(t.go);
@@ -619,8 +620,9 @@ __device__ __forceinline__ int wait_at_start(const TreeLaunch& t, volatile uint3
   asm volatile("fence.proxy.async.global;" ::: "memory");
   return (int)*blocks;
 }
+template <bool PREFIX>
 __device__ __forceinline__ void wait_at_end(const TreeLaunch& t) {
-  if (t.go) grid_wait();
+  if (!PREFIX && t.go) grid_wait();
 }
 // Row pointer of drafted token j's values in the pool, or null.
 __device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {

@@ -164,14 +164,14 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tma_prefetch_desc(&tm_v);
   }
   prefetch_tables(p);
-  const int blocks = wait_at_start(p.t, misc + 2);
-  if (blocks < 0) {
+  const int blocks = wait_at_start<PREFIX>(p.t, misc + 2);
+  if (!PREFIX && blocks < 0) {
     clear_recs(p);
     if (threadIdx.x == 0) atomicOr(err, kErrInternal);
   }
   if ((int)blockIdx.x >= blocks) {
     grid_trigger();
-    wait_at_end(p.t);
+    wait_at_end<PREFIX>(p.t);
     return;
   }
   // tensor memory only now: a kernel before this one that still runs could wait
@@ -617,7 +617,7 @@ __global__ void __launch_bounds__(kWideThreads, 1)
     tc_fence_after();
     tmem_dealloc(tbase, C::TMEM_COLS);
   }
-  wait_at_end(p.t);
+  wait_at_end<PREFIX>(p.t);
 }
 
 // Whether a record names parts that exist. After a wait that ran out a CTA
