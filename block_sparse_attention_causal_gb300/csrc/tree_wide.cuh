@@ -845,14 +845,18 @@ cudaError_t launch_d(const TreeParams& p, const CUtensorMap* maps, cudaStream_t 
   cudaError_t e = p.rows > 128  ? launch_rows<D, 256, PREFIX>(p, maps, stream)
                   : p.rows > 64 ? launch_rows<D, 128, PREFIX>(p, maps, stream)
                                 : launch_tree_narrow<PREFIX>(p, maps, stream);
-  if (e != cudaSuccess || p.t.rows_apart) return e;
-  // few rows: a row's parts are shared by a block's warps
-  const bool wide = p.rows > 64;
-  const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
-  const int jobs = wide ? p.row_slots / 32 * (D / 4) : share ? p.row_slots * kJoinWarps : p.row_slots;
-  const dim3 grid((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
-  auto join = wide ? tree_join_wide_kernel<D> : share ? tree_join_kernel<D, true> : tree_join_kernel<D, false>;
-  return launch_chained(join, grid, dim3(32 * kJoinWarps), 0, stream, p);
+  if constexpr (PREFIX) {
+    return e;  // (always rows_apart)
+  } else {
+    if (e != cudaSuccess || p.t.rows_apart) return e;
+    // few rows: a row's parts are shared by a block's warps
+    const bool wide = p.rows > 64;
+    const bool share = (int64_t)p.recs * p.row_slots < kTreeCtas * 16;
+    const int jobs = wide ? p.row_slots / 32 * (D / 4) : share ? p.row_slots * kJoinWarps : p.row_slots;
+    const dim3 grid((unsigned)p.recs, (unsigned)((jobs + kJoinWarps - 1) / kJoinWarps));
+    auto join = wide ? tree_join_wide_kernel<D> : share ? tree_join_kernel<D, true> : tree_join_kernel<D, false>;
+    return launch_chained(join, grid, dim3(32 * kJoinWarps), 0, stream, p);
+  }
 }
 
 }  // namespace
