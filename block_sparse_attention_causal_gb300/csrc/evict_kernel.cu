@@ -7,7 +7,10 @@
 // copies their rows. Measured (one GB300): 16 sequences of up to 8K, 8 key heads of
 // 128, cut to 4K (474 MB): 86.8 us, 14 of them the selection and 70 the move, which
 // runs at a copy's rate; one of 32K cut to 2K: 17.4 us, 12 the selection (eight blocks
-// a head; 21.3 us when each block summed all 2048 counts of all eight).
+// a head; 21.3 us when each block summed all 2048 counts of all eight). Weights that are
+// mostly equal count into few words of shared memory, which costs little: a prompt of
+// 32K with all weights 0 or all 1 17.9 us, with nine of ten 0 15.6, spread 15.6 to
+// 17.9; 40 sequences of 32K cut to 2K (one block a head) 208, 202, 204 us.
 #include <cooperative_groups.h>
 
 #include "internal.h"

@@ -14,8 +14,13 @@
 // bound by the tensor core and the softmax, the own parts by the cache's bytes); and
 // the join of everything that belongs to a row.
 //
+// Both parts round a softmax weight to bf16 (2^-8) before it meets V, as the attention
+// without sharing does; its sum, the maxima and all partial results are fp32, and O is
+// rounded once more where it is bf16. (Root mean square error of bf16 results against
+// 64 bits 2.3e-3 of their size, 1.7e-3 of it the last rounding.)
+//
 // Measured (one GB300): next tokens of 64 sequences, 32/8 heads of 128, behind 32K shared
-// and up to 1K of their own (299 MB, 35 GFLOP): 76.2 us, 97 when the parts ran one after
+// and up to 1K of their own (299 MB, 35 GFLOP): 78 us, 97 when the parts ran one after
 // the other, each with its own join. The plan takes 4 us, the parts start 1 and 3 us
 // later, the first tiles are 6 us on, and the join ends 8 us behind the last of them.
 #include "tree_wide.cuh"
@@ -237,7 +242,17 @@ PrefixLayout prefix_layout(int64_t batch, int64_t kv_heads, int64_t heads, int64
 // Time of a place of the line, in microseconds, by the rows of a unit: what decides
 // how the SMs are shared out. (64 next tokens behind 32K and up to 1K of their own:
 // 80.8, 77.3, 76.1, 83.0, 88.2 us with 0.6, 0.8, 0.85, 1.0, 1.2 for up to 16 rows; trees
-// of 5 with 25 rows 51.5, 47.1, 45.9, 47.1 us with 0.8, 1.0, 1.2, 1.5.)
+// of 5 with 25 rows 51.5, 47.1, 45.9, 47.1 us with 0.8, 1.0, 1.2, 1.5.) Each constant
+// swept with the others as they are, 32/8 heads of 64, 96 and 128 behind 8K and 32K,
+// 256, 1K and 4K tokens of their own; how far the one taken is behind the sweep's best:
+//   24 shared rows, 1.2 (of 0.8, 1.0, 1.2, 1.5)         0 to 12 % (best 1.0 to 1.5)
+//   48 shared rows, 1.6 (of 0.8, 1.0, 1.2, 1.6, 2.0)    0 to 9 %  (0.8 to 1.6)
+//   40 own rows, 1.6 (of the same)                      0 to 10 % (1.2 with 4K, else 1.6)
+//   96 shared rows, 1.0 (of 0.6, 0.8, 1.0, 1.25, 1.6)   0 to 10 % (0.8 to 1.6)
+//   192 shared rows, 1.65 (of 1.1, 1.35, 1.65, 2, 2.4)  0 to 8 %  (1.65 to 2.4)
+//   256 shared rows, 1.65 (of the same)                 0 to 17 % (1.65 to 2.4; 17 % with 64
+//                                                       dimensions and 4K of their own)
+// A constant half as large as the best costs up to 1.6 times the time.
 float place_cost(const TreeParams& p) {
   return p.rows > 128 ? 1.65f : p.rows > 64 ? 1.f : p.rows > 32 ? 1.6f : p.rows > 16 ? 1.2f : 0.85f;
 }

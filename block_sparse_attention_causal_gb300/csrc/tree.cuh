@@ -28,7 +28,9 @@ constexpr int kTreeCtas = 152;   // SMs of a GB300
 constexpr int kNfRing = 16;      // segments whose taken-out values are remembered
 
 // A unit's partial results: CTA `first_cta`'s part `first_part`, then part
-// 2 c of each later CTA c; parts < 2: nothing to join.
+// 2 c of each later CTA c. parts 1: the unit was not cut, its rows are in the
+// launch's own outputs (only the join of shared prefixes reads those); less: no
+// record.
 struct JoinRec {
   int32_t parts, first_part, first_cta, b, hk, pair, pad0, pad1;
 };
@@ -37,12 +39,12 @@ struct TreeParams {
   TreeLaunch t;
   int32_t group;        // query heads per key head
   uint32_t group_mul;   // ceil(2^32 / group), for rows / group
-  int32_t rows;         // rows of a (sequence, key head): group * n
+  int32_t rows;         // rows of a (sequence, key head): group * n; of a group of sequences: times its members, at most
   int32_t pairs;        // units per (sequence, key head): ceil(rows / 256)
   int32_t row_slots;    // rows of a partial result: min(rows, 256), in whole blocks of 32 for wide units
   int32_t mask_words;   // words of a mask row
-  int32_t recs;         // join records: one per unit if there are at most kTreeCtas, else one per CTA
-  int32_t by_unit;
+  int32_t recs;         // join records: one per unit if there are at most kTreeCtas or a
+  int32_t by_unit;      // join reads all units (TreeLaunch::rows_apart), else one per CTA
   int32_t overhead;     // places of the line before a unit's tiles
   float scale_log2;
   JoinRec* rec;
