@@ -1024,7 +1024,8 @@ def cache_evict(cache: PagedCache, weights: torch.Tensor, budget: int, page_tabl
     else:
         wo = _check_array("weights_out", weights_out, torch.float32,
                           (b, hk, weights_out.shape[2] if isinstance(weights_out, torch.Tensor) and weights_out.dim() == 3 else 0), dev)
-    nbytes = lib.wise_cache_evict_workspace(desc, budget)
+    # (no workspace for a budget that the call refuses: its size is the budget's)
+    nbytes = lib.wise_cache_evict_workspace(desc, budget) if budget <= pages * desc.page else 0
     own = 0
     if workspace is not None:
         _check_bytes("workspace", workspace, nbytes, weights.device)
