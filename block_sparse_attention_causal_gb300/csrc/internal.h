@@ -15,10 +15,9 @@ namespace wise {
 // One launch runs beside the one before it instead (the own parts of
 // wise_attn_prefix): it calls grid_wait at its end, and what it reads was ordered
 // by a word that the plan, two launches before it, released and it acquires
-// (TreeLaunch::go). What earlier kernels
-// may have written is loaded plainly, never with __ldg: that names data which
-// nothing writes while the kernel runs, so the compiler may move it above the
-// wait.
+// (TreeLaunch::go). What earlier kernels may have written is loaded plainly, never
+// with __ldg: that names data which nothing writes while the kernel runs, so the
+// compiler may move it above the wait.
 template <class... P, class... A>
 inline cudaError_t launch_chained(void (*kernel)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
                                   const A&... args) {

@@ -626,6 +626,7 @@ template <bool PREFIX>
 __device__ __forceinline__ void wait_at_end(const TreeLaunch& t) {
   if (!PREFIX && t.go) grid_wait();
 }
+
 // Row pointer of drafted token j's values in the pool, or null.
 __device__ __forceinline__ const uint16_t* draft_value(const TreeLaunch& t, int d, int b, int hk, int len, int j) {
   const int64_t tok = (int64_t)len + j;
